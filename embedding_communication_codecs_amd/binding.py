@@ -24,6 +24,7 @@ QC_MIN_BUCKET, QC_MAX_BUCKET, QC_MAX_WORKERS = 64, 65536, 65535
 QC_INDEX_SHIFT = 12
 QC_MAX_LIST_BUCKET = 32768
 QC_MAX_TOPK_BUCKET = 65536
+QC_CKPT_GROUP = 32
 
 EXPORTS = (
     "qc_encode_uniform", "qc_encode_uniform_stochastic", "qc_encode_uniform_multi", "qc_encode_fp8_rowwise",
@@ -32,6 +33,8 @@ EXPORTS = (
     "qc_sum_int8_shared", "qc_tensor_index", "qc_encode_topk", "qc_decode_topk", "qc_topk_accumulate",
     "qc_encode_uniform_stochastic_multi", "qc_encode_qsgd_multi", "qc_encode_ternary_multi", "qc_encode_sign_multi",
     "qc_bucket_absmax_multi", "qc_encode_int8_shared_multi", "qc_encode_topk_multi",
+    "qc_encode_int8_rowwise", "qc_matmul_int8", "qc_ckpt8_bytes", "qc_encode_ckpt8", "qc_decode_ckpt8",
+    "qc_ckpt8_wgrad_workspace", "qc_ckpt8_wgrad", "qc_swiglu_ckpt8", "qc_swiglu_ckpt8_backward",
     "qc_decode", "qc_decode_multi", "qc_dequant_accumulate", "qc_majority_vote", "qc_payload_bytes", "qc_status_str",
 )
 
@@ -81,6 +84,15 @@ def lib() -> ctypes.CDLL:
             "qc_absmax_combine": [P, I32, I64, P, P],
             "qc_encode_int8_shared": [P, P, I64, I32, P, P, P, P],
             "qc_sum_int8_shared": [P, I32, I64, I32, P, P, I32, P, P],
+            "qc_encode_int8_rowwise": [P, I32, I64, I64, I64, P, I64, P, P],
+            "qc_matmul_int8": [P, P, I64, P, P, I64, I64, I64, I64, P, I32, I64, P],
+            "qc_ckpt8_bytes": [I64, I64, P, P],
+            "qc_encode_ckpt8": [P, I32, I64, I64, I64, P, P, P],
+            "qc_decode_ckpt8": [P, P, I64, I64, P, I32, I64, P],
+            "qc_ckpt8_wgrad_workspace": [I64, I64, I64, I32],
+            "qc_ckpt8_wgrad": [P, I32, I64, P, P, I64, I64, I64, P, I32, I64, I32, P, I64, P],
+            "qc_swiglu_ckpt8": [P, P, I32, I64, I64, I64, P, I64, P, P, P, P, P],
+            "qc_swiglu_ckpt8_backward": [P, I32, I64, P, P, P, P, I64, I64, P, P, I64, P],
             "qc_payload_bytes": [I32, I64, I32, I32],
             "qc_status_str": [I32],
         }
@@ -89,6 +101,7 @@ def lib() -> ctypes.CDLL:
             fn.argtypes = args
             fn.restype = ctypes.c_int
         L.qc_payload_bytes.restype = I64
+        L.qc_ckpt8_wgrad_workspace.restype = I64
         L.qc_status_str.restype = ctypes.c_char_p
         _lib = L
     return _lib
@@ -405,6 +418,114 @@ def qc_majority_vote(words, m, n, out_words, stream=None):
     _check(lib().qc_majority_vote(
         _ptr(words, max(m, 0) * pb if pb is not None else None, "words"), m, n,
         _ptr(out_words, pb, "out_words"), _stream(stream)))
+
+
+# ------------------------------------------------------- matrix operators
+
+
+def _mat(t, rows, cols, ld, esize, name):
+    """Device address of a [rows][cols] matrix with row stride ld (elements),
+    checking that the tensor has elements of esize bytes and memory for all of
+    it; it may be a view into a wider matrix."""
+    if t is None:
+        return None
+    if isinstance(t, int):
+        return t
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.element_size() != esize:
+        raise ValueError(f"{name} has elements of {t.element_size()} bytes, the call takes {esize}")
+    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must have neighbouring elements in a row")
+    if t.dim() == 2 and t.shape[0] > 1 and t.stride(0) != ld:
+        raise ValueError(f"{name} has a row stride of {t.stride(0)}, the call says {ld}")
+    if rows > 0 and cols > 0:
+        have = t.untyped_storage().nbytes() // esize - t.storage_offset()
+        need = (rows - 1) * ld + cols
+        if have < need:
+            raise ValueError(f"{name} holds {have} elements, the call needs {need}")
+    return t.data_ptr()
+
+
+def _esize(qtype):
+    return 2 if qtype == QC_BF16 else 4
+
+
+def _ckpt(codes, exps, rows, dim, name):
+    cb, eb = (ckpt8_bytes(rows, dim) if rows >= 0 and dim > 0 else (None, None))
+    return _ptr(codes, cb, name + "codes"), _ptr(exps, eb, name + "exps")
+
+
+def ckpt8_bytes(rows: int, dim: int) -> tuple[int, int]:
+    """(code bytes, exponent bytes) of a checkpoint of [rows][dim]."""
+    cb, eb = ctypes.c_int64(), ctypes.c_int64()
+    _check(lib().qc_ckpt8_bytes(rows, dim, ctypes.byref(cb), ctypes.byref(eb)))
+    return cb.value, eb.value
+
+
+qc_ckpt8_bytes = ckpt8_bytes
+
+
+def qc_encode_int8_rowwise(x, xtype, rows, dim, ldx, codes, ldq, scale, stream=None):
+    _check(lib().qc_encode_int8_rowwise(
+        _mat(x, rows, dim, ldx, _esize(xtype), "x"), xtype, rows, dim, ldx,
+        _mat(codes, rows, -(-dim // 16) * 16, ldq, 1, "codes"), ldq, _ptr(scale, 4 * max(rows, 0), "scale"),
+        _stream(stream)))
+
+
+def qc_matmul_int8(a, a_scale, lda, b, b_scale, ldb, m, n, k, c, ctype, ldc, stream=None):
+    kp = -(-k // 16) * 16
+    _check(lib().qc_matmul_int8(
+        _mat(a, m, kp, lda, 1, "a"), _ptr(a_scale, 4 * max(m, 0), "a_scale"), lda,
+        _mat(b, n, kp, ldb, 1, "b"), _ptr(b_scale, 4 * max(n, 0), "b_scale"), ldb, m, n, k,
+        _mat(c, m, n, ldc, _esize(ctype), "c"), ctype, ldc, _stream(stream)))
+
+
+def qc_encode_ckpt8(x, xtype, rows, dim, ldx, codes, exps, stream=None):
+    _check(lib().qc_encode_ckpt8(_mat(x, rows, dim, ldx, _esize(xtype), "x"), xtype, rows, dim, ldx,
+                                 *_ckpt(codes, exps, rows, dim, ""), _stream(stream)))
+
+
+def qc_decode_ckpt8(codes, exps, rows, dim, out, otype, ldo, stream=None):
+    _check(lib().qc_decode_ckpt8(*_ckpt(codes, exps, rows, dim, ""), rows, dim,
+                                 _mat(out, rows, dim, ldo, _esize(otype), "out"), otype, ldo, _stream(stream)))
+
+
+def qc_ckpt8_wgrad_workspace(rows, n, dim, dytype) -> int:
+    """Bytes of workspace qc_ckpt8_wgrad needs for these sizes."""
+    need = int(lib().qc_ckpt8_wgrad_workspace(rows, n, dim, dytype))
+    if need < 0:
+        _check(QC_ERR_ARG)
+    return need
+
+
+def qc_ckpt8_wgrad(dy, dytype, ldy, codes, exps, rows, n, dim, dw, wtype, ldw, accumulate, workspace=None,
+                   stream=None):
+    """workspace: a GPU tensor of at least qc_ckpt8_wgrad_workspace() bytes, or
+    None where that is 0."""
+    if workspace is not None and isinstance(workspace, int):
+        raise ValueError("workspace must be a GPU tensor")
+    _check(lib().qc_ckpt8_wgrad(
+        _mat(dy, rows, n, ldy, _esize(dytype), "dy"), dytype, ldy, *_ckpt(codes, exps, rows, dim, ""), rows, n, dim,
+        _mat(dw, n, dim, ldw, _esize(wtype), "dw"), wtype, ldw, 1 if accumulate else 0,
+        _ptr(workspace, None, "workspace"), 0 if workspace is None else _bytes(workspace), _stream(stream)))
+
+
+def qc_swiglu_ckpt8(gate, up, xtype, ldx, rows, dim, h, ldh, gate_codes, gate_exps, up_codes, up_exps, stream=None):
+    es = _esize(xtype)
+    _check(lib().qc_swiglu_ckpt8(
+        _mat(gate, rows, dim, ldx, es, "gate"), _mat(up, rows, dim, ldx, es, "up"), xtype, ldx, rows, dim,
+        _mat(h, rows, dim, ldh, es, "h"), ldh, *_ckpt(gate_codes, gate_exps, rows, dim, "gate_"),
+        *_ckpt(up_codes, up_exps, rows, dim, "up_"), _stream(stream)))
+
+
+def qc_swiglu_ckpt8_backward(dh, dhtype, lddh, gate_codes, gate_exps, up_codes, up_exps, rows, dim, dgate, dup, ldg,
+                             stream=None):
+    es = _esize(dhtype)
+    _check(lib().qc_swiglu_ckpt8_backward(
+        _mat(dh, rows, dim, lddh, es, "dh"), dhtype, lddh, *_ckpt(gate_codes, gate_exps, rows, dim, "gate_"),
+        *_ckpt(up_codes, up_exps, rows, dim, "up_"), rows, dim, _mat(dgate, rows, dim, ldg, es, "dgate"),
+        _mat(dup, rows, dim, ldg, es, "dup"), ldg, _stream(stream)))
 
 
 def qc_payload_bytes(fmt, n, group, bits) -> int:

@@ -34,7 +34,7 @@ FLAGS = [
     "-Wno-unused-function",
 ]
 SOURCES = ["k_encode.hip", "k_encode_codecs.hip", "k_encode_list.hip", "k_encode_list_codecs.hip", "k_fp8.hip", "k_decode.hip", "k_accumulate.hip", "k_vote.hip", "k_shared_sum.hip",
-           "k_topk.hip", "qc_api.cpp"]
+           "k_topk.hip", "k_int8_rows.hip", "k_matmul_int8.hip", "k_ckpt8.hip", "k_ckpt8_wgrad.hip", "qc_api.cpp"]
 
 
 def _compile(src: str) -> str:

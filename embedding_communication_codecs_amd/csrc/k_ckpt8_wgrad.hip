@@ -1,0 +1,376 @@
+// k_ckpt8_wgrad.hip -- the weight gradient of a linear layer whose input was
+// kept in 8 bits: dW[n][d] (+)= sum over tokens t of dY[t][n] * X[t][d], X the
+// values a checkpoint holds (codes times a power of two per 32 channels).
+//
+// X's values are exact in bf16, so they go to v_mfma_f32_16x16x32_bf16 as
+// they are and every product is exact in fp32: nothing is rounded but the
+// fp32 sums.  A bf16 dY goes in as it is too; an fp32 dY as three bf16
+// pieces of 8 mantissa bits each, which add up to it exactly.
+//
+// Both operands are summed over their slow axis.  Tiles of 64 tokens lie
+// in LDS as [token][channel] and are read with ds_read_b64_tr_b16, which
+// hands each lane four tokens of one channel.
+#include "qc_lds.hpp"
+#include "qc_launch.hpp"
+
+namespace qc {
+namespace {
+
+typedef __attribute__((address_space(3))) s16x4* lds4;
+
+struct Args {
+    const void* dy;
+    int64_t ldy;
+    const uint8_t* codes;
+    const uint8_t* exps;
+    int64_t pitch, epitch;
+    int64_t rows, n, dim;
+    int64_t rows_per_split;  // a multiple of the token tile
+    void* out;               // dW, or the first split's partial sums
+    int64_t ldw, split_stride;
+    int32_t out_bf16, accumulate;
+    bool wide;  // rows of dW start at multiples of four elements
+};
+
+// Byte offset of 16-byte piece `c` of token `t` in a tile of `row_bytes` a
+// token.  A fragment read takes 32 bytes of each of 16 tokens; the xor puts
+// eight neighbouring tokens on different banks.
+__device__ __forceinline__ int place(int t, int c, int row_bytes) { return t * row_bytes + ((c ^ (2 * (t & 7))) << 4); }
+
+// Four bf16 values from four codes: code * step is exact, so its upper half
+// is the bf16 value.  (c + 128) is read from a byte of the word xor 0x80..,
+// and 128 * step taken off again in the multiply-add, exactly.
+__device__ __forceinline__ u32x2 held4(uint32_t word, float step, float off) {
+    const uint32_t w = word ^ 0x80808080u;
+    const uint32_t a = __float_as_uint(__builtin_fmaf((float)(w & 0xFFu), step, off));
+    const uint32_t b = __float_as_uint(__builtin_fmaf((float)((w >> 8) & 0xFFu), step, off));
+    const uint32_t c = __float_as_uint(__builtin_fmaf((float)((w >> 16) & 0xFFu), step, off));
+    const uint32_t d = __float_as_uint(__builtin_fmaf((float)(w >> 24), step, off));
+    return u32x2{__builtin_amdgcn_perm(b, a, 0x07060302u), __builtin_amdgcn_perm(d, c, 0x07060302u)};
+}
+
+// The three pieces of an fp32 value (8 mantissa bits each, cut off, so their
+// sum is exact); an infinity or a NaN is its first piece alone.
+__device__ __forceinline__ void pieces(float x, uint32_t (&p)[3]) {
+    const uint32_t b = __float_as_uint(x);
+    if ((b & kInfBits) == kInfBits) {
+        p[0] = bf16_bits(x);
+        p[1] = p[2] = 0;
+        return;
+    }
+    const float r = x - __uint_as_float(b & 0xFFFF0000u);
+    const uint32_t rb = __float_as_uint(r);
+    p[0] = b >> 16;
+    p[1] = rb >> 16;
+    p[2] = __float_as_uint(r - __uint_as_float(rb & 0xFFFF0000u)) >> 16;
+}
+
+// One block: BN output channels (columns of dY) x BD input channels (columns
+// of X), WN x WD waves, TK tokens a step.  P: pieces of dY (1: bf16, 3:
+// fp32).  DMA: dY's rows are 16-byte aligned and n a multiple of 8: they are
+// loaded straight into LDS (P = 1 only).
+template <int P, bool DMA, int BN, int BD, int WN, int WD, int TK>
+__global__ void __launch_bounds__(WN * WD * WAVE)
+k_ckpt8_wgrad(Args g) {
+    constexpr int NW = WN * WD, THREADS = NW * WAVE;
+    constexpr int FN = BN / WN / 16, FD = BD / WD / 16;
+    constexpr int YB = BN * 2, XB = BD * 2;      // bytes of a token in a tile
+    constexpr int YT = TK * YB, XT = TK * XB;    // bytes of a tile
+    constexpr int TILE = P * YT + XT;            // pieces of dY first, then X
+    constexpr int XG = TK * BD / 32 / THREADS;   // groups of X a thread converts
+    static_assert(XG >= 1, "a group for every thread");
+    __shared__ __align__(1024) uint8_t lds[2 * TILE];
+
+    const int64_t tn = (g.n + BN - 1) / BN;
+    const int64_t n0 = ((int64_t)blockIdx.x % tn) * BN, d0 = ((int64_t)blockIdx.x / tn) * BD;
+    const int64_t t_first = (int64_t)blockIdx.y * g.rows_per_split;
+    const int64_t t_end = min(g.rows, t_first + g.rows_per_split);
+    const int l = lane_id(), w = wave_id();
+    const int wn = w % WN, wd = w / WN;
+
+    f32x4 acc[FD][FN] = {};
+
+    // ---- X: codes and steps of this thread's groups, then bf16 into LDS
+    u32x4 xw[XG][2];
+    float xstep[XG];
+    auto x_get = [&](int64_t t0) {
+#pragma unroll
+        for (int i = 0; i < XG; ++i) {
+            const int id = i * THREADS + threadIdx.x;
+            const int64_t t = t0 + id / (BD / 32);
+            const int64_t d = d0 + (id % (BD / 32)) * 32;
+            const bool in = t < t_end && d < g.dim;
+            xw[i][0] = xw[i][1] = u32x4{0, 0, 0, 0};
+            xstep[i] = 0.0f;
+            if (in) {
+                const uint8_t* p = g.codes + t * g.pitch + d;
+                xw[i][0] = ld_u4(p);
+                xw[i][1] = ld_u4(p + 16);
+                xstep[i] = ckpt_step(g.exps[t * g.epitch + d / 32]);
+            }
+        }
+    };
+    auto x_put = [&](uint8_t* tile) {
+#pragma unroll
+        for (int i = 0; i < XG; ++i) {
+            const int id = i * THREADS + threadIdx.x;
+            const int t = id / (BD / 32), c = (id % (BD / 32)) * 4;
+            const float off = -128.0f * xstep[i];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const u32x2 a = held4(xw[i][h >> 1][2 * (h & 1)], xstep[i], off);
+                const u32x2 b = held4(xw[i][h >> 1][2 * (h & 1) + 1], xstep[i], off);
+                *reinterpret_cast<u32x4*>(tile + place(t, c + h, XB)) = u32x4{a.x, a.y, b.x, b.y};
+            }
+        }
+    };
+
+    // ---- dY
+    const uint32_t lds0 = lds_addr(lds);
+    constexpr int YN = TK * YB / 1024 / NW;  // loads a wave (DMA)
+    constexpr int TPL = 1024 / YB;           // tokens a load
+    int yoff[YN > 0 ? YN : 1];
+    auto y_offsets = [&](int last) {
+#pragma unroll
+        for (int i = 0; i < YN; ++i) {
+            const int t = (w * YN + i) * TPL + l / (YB / 16);
+            const int c = (l % (YB / 16)) ^ (2 * (t & 7));
+            const int64_t col = min(n0 + c * 8, g.n - 8);  // pieces past n repeat its last one
+            yoff[i] = (int)(min(t, last) * g.ldy + (col - n0)) * 2;
+        }
+    };
+    auto y_dma = [&](int buf, int64_t t0) {
+        const int64_t left = t_end - t0;
+        if (left < TK) y_offsets((int)left - 1);  // tokens past the end repeat the last one
+        const auto rsrc = buffer_of(static_cast<const uint8_t*>(g.dy) + (t0 * g.ldy + n0) * 2, -1);
+#pragma unroll
+        for (int i = 0; i < YN; ++i) load_lds16(rsrc, lds0 + buf * TILE + (w * YN + i) * 1024, yoff[i], 0);
+    };
+    constexpr int YC = TK * BN / 8 / THREADS;  // pieces of 8 values a thread stages
+    float yv[DMA ? 1 : YC][8];
+    auto y_get = [&](int64_t t0) {
+#pragma unroll
+        for (int i = 0; i < YC; ++i) {
+            const int id = i * THREADS + threadIdx.x;
+            const int64_t t = t0 + id / (BN / 8), col = n0 + (id % (BN / 8)) * 8;
+            const int64_t left = t < t_end ? g.n - col : 0;
+            if constexpr (P == 1) load8(static_cast<const BF16*>(g.dy) + t * g.ldy + col, left, yv[i]);
+            else load8(static_cast<const float*>(g.dy) + t * g.ldy + col, left, yv[i]);
+        }
+    };
+    auto y_put = [&](uint8_t* tile) {
+#pragma unroll
+        for (int i = 0; i < YC; ++i) {
+            const int id = i * THREADS + threadIdx.x;
+            const int at = place(id / (BN / 8), id % (BN / 8), YB);
+            uint32_t o[P][4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                if constexpr (P == 1) {  // bf16 values again: exact
+                    o[0][h] = (__float_as_uint(yv[i][2 * h]) >> 16) | (__float_as_uint(yv[i][2 * h + 1]) & 0xFFFF0000u);
+                } else {
+                    uint32_t a[3], b[3];
+                    pieces(yv[i][2 * h], a);
+                    pieces(yv[i][2 * h + 1], b);
+#pragma unroll
+                    for (int q = 0; q < P; ++q) o[q][h] = a[q] | (b[q] << 16);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < P; ++q)
+                *reinterpret_cast<u32x4*>(tile + q * YT + at) = u32x4{o[q][0], o[q][1], o[q][2], o[q][3]};
+        }
+    };
+
+    // ---- fragments: lane l reads 8 bytes of token r*16 + l/4, 16 channels
+    // by four lanes, and gets four tokens of channel l % 16
+    const int ft = l >> 2;  // 0..15
+    auto frag = [&](const uint8_t* tile, int row_bytes, int f, int kk) {
+        const int c = f * 2 + ((l & 3) >> 1);
+        s16x4 p[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            p[r] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds4)(tile + place(kk * 32 + r * 16 + ft, c, row_bytes) + 8 * (l & 1)));
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
+        return __builtin_bit_cast(bf16x8, s16x8{p[0].x, p[0].y, p[0].z, p[0].w, p[1].x, p[1].y, p[1].z, p[1].w});
+    };
+    auto compute = [&](const uint8_t* tile) {
+#pragma unroll
+        for (int kk = 0; kk < TK / 32; ++kk) {
+            bf16x8 fx[FD];
+#pragma unroll
+            for (int i = 0; i < FD; ++i) fx[i] = frag(tile + P * YT, XB, wd * FD + i, kk);
+#pragma unroll
+            for (int q = 0; q < P; ++q)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+                    const bf16x8 fy = frag(tile + q * YT, YB, wn * FN + j, kk);
+#pragma unroll
+                    for (int i = 0; i < FD; ++i)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[i], fy, acc[i][j], 0, 0, 0);
+                }
+        }
+    };
+
+    if (t_first < t_end) {
+        if constexpr (DMA) {
+            y_offsets(TK - 1);
+            y_dma(0, t_first);
+        } else {
+            y_get(t_first);
+            y_put(lds);
+        }
+        x_get(t_first);
+        x_put(lds + P * YT);
+        int buf = 0;
+        for (int64_t t0 = t_first; t0 < t_end; t0 += TK, buf ^= 1) {
+            lds_landed();
+            const bool more = t0 + TK < t_end;
+            if (more) {
+                x_get(t0 + TK);
+                if constexpr (DMA) y_dma(buf ^ 1, t0 + TK);
+                else y_get(t0 + TK);
+            }
+            if constexpr (DMA) {
+                if (t_end - t0 < TK) {  // tokens past the end: zeros (X's are zeros too; an infinity times zero is not)
+                    const int first = (int)(t_end - t0) * YB;
+                    for (int at = first + threadIdx.x * 16; at < YT; at += THREADS * 16)
+                        *reinterpret_cast<u32x4*>(lds + buf * TILE + at) = u32x4{0, 0, 0, 0};
+                    __syncthreads();
+                }
+            }
+            compute(lds + buf * TILE);
+            if (more) {
+                x_put(lds + (buf ^ 1) * TILE + P * YT);
+                if constexpr (!DMA) y_put(lds + (buf ^ 1) * TILE);
+            }
+        }
+    }
+
+    // ---- lane l: output channel l % 16, input channels 4 * (l / 16) .. + 3
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+        const int64_t n = n0 + (wn * FN + j) * 16 + (l & 15);
+        if (n >= g.n) continue;
+#pragma unroll
+        for (int i = 0; i < FD; ++i) {
+            const int64_t d = d0 + (wd * FD + i) * 16 + 4 * (l >> 4);
+            const int64_t left = g.dim - d;
+            if (left <= 0) continue;
+            f32x4 v = acc[i][j];
+            if (g.out_bf16) {
+                BF16* o = static_cast<BF16*>(g.out) + n * g.ldw + d;
+                if (g.wide && left >= 4)
+                    *reinterpret_cast<u32x2*>(o) = u32x2{bf16_pair(v.x, v.y), bf16_pair(v.z, v.w)};
+                else
+                    for (int e = 0; e < 4; ++e)
+                        if (e < left) put(o + e, v[e]);
+            } else {
+                float* o = static_cast<float*>(g.out) + (int64_t)blockIdx.y * g.split_stride + n * g.ldw + d;
+                if (g.wide && left >= 4) {
+                    if (g.accumulate) v += *reinterpret_cast<const f32x4*>(o);
+                    *reinterpret_cast<f32x4*>(o) = v;
+                } else {
+                    for (int e = 0; e < 4; ++e)
+                        if (e < left) o[e] = g.accumulate ? o[e] + v[e] : v[e];
+                }
+            }
+        }
+    }
+}
+
+// dW (+)= the splits' partial sums, added in the splits' order.
+__global__ void __launch_bounds__(256)
+k_ckpt8_wgrad_join(const float* __restrict__ part, int32_t splits, int64_t n, int64_t dim, int64_t ldp,
+                   void* __restrict__ out, int64_t ldw, int32_t out_bf16, int32_t accumulate) {
+    const int64_t pieces_row = ldp / 4;
+    const int64_t total = n * pieces_row;
+    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < total; id += (int64_t)gridDim.x * 256) {
+        const int64_t r = id / pieces_row, d = (id - r * pieces_row) * 4;
+        const float* p = part + r * ldp + d;
+        f32x4 v = ld_f4(p);
+        for (int s = 1; s < splits; ++s) v += ld_f4(p + (int64_t)s * n * ldp);
+        for (int e = 0; e < 4; ++e) {
+            if (d + e >= dim) continue;
+            if (out_bf16) put(static_cast<BF16*>(out) + r * ldw + d + e, v[e]);
+            else {
+                float* o = static_cast<float*>(out) + r * ldw + d + e;
+                *o = accumulate ? *o + v[e] : v[e];
+            }
+        }
+    }
+}
+
+struct Plan {
+    int tile;  // 256 or 128
+    int32_t splits;
+    int64_t rows_per_split;
+};
+
+Plan plan_of(int64_t rows, int64_t n, int64_t dim, bool bf16) {
+    const auto tiles = [&](int64_t b) { return ((n + b - 1) / b) * ((dim + b - 1) / b); };
+    Plan p{128, 1, 0};
+    if (bf16 && tiles(256) >= 192) p.tile = 256;
+    const int64_t steps = (rows + 63) / 64, t = tiles(p.tile);
+    int64_t s = t >= 256 ? 1 : (512 + t - 1) / t;
+    s = s < steps / 4 ? s : steps / 4;  // at least four steps a split
+    if (s < 1) s = 1;
+    p.rows_per_split = ((steps + s - 1) / s) * 64;
+    if (p.rows_per_split < 64) p.rows_per_split = 64;
+    p.splits = (int32_t)(rows > 0 ? (rows + p.rows_per_split - 1) / p.rows_per_split : 1);
+    return p;
+}
+
+int64_t part_pitch(int64_t dim) { return (dim + 3) & ~int64_t(3); }
+
+template <int P, bool DMA, int B, int WN, int WD, int TK>
+hipError_t launch_tile(const Args& g, const Plan& p, hipStream_t stream) {
+    const dim3 grid((unsigned)(((g.n + B - 1) / B) * ((g.dim + B - 1) / B)), (unsigned)p.splits);
+    hipLaunchKernelGGL((k_ckpt8_wgrad<P, DMA, B, B, WN, WD, TK>), grid, dim3(WN * WD * WAVE), 0, stream, g);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t ckpt8_wgrad_workspace(int64_t rows, int64_t n, int64_t dim, bool bf16) {
+    const Plan p = plan_of(rows, n, dim, bf16);
+    return p.splits > 1 ? p.splits * n * part_pitch(dim) * 4 : 0;
+}
+
+hipError_t launch_ckpt8_wgrad(const void* dy, bool dy_bf16, int64_t ldy, const void* codes, const void* exps,
+                              int64_t rows, int64_t n, int64_t dim, void* dw, bool dw_bf16, int64_t ldw,
+                              bool accumulate, void* workspace, hipStream_t stream) {
+    const Plan p = plan_of(rows, n, dim, dy_bf16);
+    Args g{};
+    g.dy = dy;
+    g.ldy = ldy;
+    g.codes = static_cast<const uint8_t*>(codes);
+    g.exps = static_cast<const uint8_t*>(exps);
+    g.pitch = (dim + 31) / 32 * 32;
+    g.epitch = (dim + 127) / 128 * 4;
+    g.rows = rows;
+    g.n = n;
+    g.dim = dim;
+    g.rows_per_split = p.rows_per_split;
+    g.out = p.splits > 1 ? workspace : dw;
+    g.ldw = p.splits > 1 ? part_pitch(dim) : ldw;
+    g.split_stride = n * part_pitch(dim);
+    g.out_bf16 = p.splits > 1 ? 0 : dw_bf16;
+    g.accumulate = p.splits > 1 ? 0 : accumulate;
+    g.wide = g.ldw % 4 == 0 && reinterpret_cast<uintptr_t>(g.out) % (g.out_bf16 ? 8 : 16) == 0;
+    const bool dma = dy_bf16 && n % 8 == 0 && ldy % 8 == 0 && reinterpret_cast<uintptr_t>(dy) % 16 == 0;
+    hipError_t e;
+    if (!dy_bf16) e = launch_tile<3, false, 128, 2, 2, 64>(g, p, stream);
+    else if (p.tile == 256) e = dma ? launch_tile<1, true, 256, 2, 4, 64>(g, p, stream)
+                                    : launch_tile<1, false, 256, 2, 4, 64>(g, p, stream);
+    else e = dma ? launch_tile<1, true, 128, 2, 2, 64>(g, p, stream) : launch_tile<1, false, 128, 2, 2, 64>(g, p, stream);
+    if (e != hipSuccess || p.splits == 1) return e;
+    const int64_t pieces4 = n * (part_pitch(dim) / 4), blocks = (pieces4 + 255) / 256;
+    hipLaunchKernelGGL(k_ckpt8_wgrad_join, dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), dim3(256), 0,
+                       stream, static_cast<const float*>(workspace), p.splits, n, dim, part_pitch(dim), dw, ldw,
+                       (int32_t)dw_bf16, (int32_t)accumulate);
+    return hipGetLastError();
+}
+
+}  // namespace qc

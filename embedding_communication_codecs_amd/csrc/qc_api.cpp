@@ -493,4 +493,141 @@ int qc_majority_vote(const uint32_t* words, int32_t m, int64_t n, uint32_t* out_
                                              out_words, hs(stream)));
 }
 
+// ------------------------------------------------------ matrix operators
+
+namespace {
+
+// Sizes and strides whose byte offsets stay far below 2^63.
+constexpr int64_t kMaxMatrixElems = int64_t(1) << 56;
+constexpr int64_t kMaxProductStride = int64_t(1) << 23;  // 32-bit offsets inside a tile
+constexpr int64_t kMaxTiles = (int64_t(1) << 31) - 1;
+
+bool bad_type(int32_t t) { return t != QC_F32 && t != QC_BF16; }
+
+// [rows][cols] with row stride ld
+bool bad_matrix(int64_t rows, int64_t cols, int64_t ld) {
+    return rows < 0 || cols < 1 || cols > kMaxMatrixElems || ld < cols ||
+           ld > kMaxMatrixElems / (rows > 0 ? rows : 1);
+}
+
+bool misaligned_for(const void* p, int32_t type) {
+    return (reinterpret_cast<uintptr_t>(p) & (type == QC_BF16 ? 1u : 3u)) != 0;
+}
+
+int64_t up_to(int64_t v, int64_t unit) { return ceil_div(v, unit) * unit; }
+
+// int8 [rows][ld] with k codes a row
+bool bad_codes(int64_t rows, int64_t k, int64_t ld) {
+    return bad_matrix(rows, k, ld) || ld % 16 != 0;  // a multiple of 16 not below k holds k rounded up
+}
+
+}  // namespace
+
+int qc_encode_int8_rowwise(const void* x, int32_t xtype, int64_t rows, int64_t dim, int64_t ldx, int8_t* codes,
+                           int64_t ldq, float* scale, qc_stream_t stream) {
+    if (bad_type(xtype) || bad_matrix(rows, dim, ldx) || bad_codes(rows, dim, ldq)) return QC_ERR_ARG;
+    if (rows == 0) return QC_OK;
+    if (!x || !codes || !scale) return QC_ERR_ARG;
+    if (misaligned_for(x, xtype) || misaligned(codes) || misaligned4(scale)) return QC_ERR_ALIGN;
+    return launched(qc::launch_encode_int8_rowwise(x, xtype == QC_BF16, rows, dim, ldx, codes, ldq, scale, hs(stream)));
+}
+
+int qc_matmul_int8(const int8_t* a, const float* a_scale, int64_t lda, const int8_t* b, const float* b_scale,
+                   int64_t ldb, int64_t m, int64_t n, int64_t k, void* c, int32_t ctype, int64_t ldc,
+                   qc_stream_t stream) {
+    if (bad_type(ctype) || k < 1 || bad_codes(m, k, lda) || bad_codes(n, k, ldb)) return QC_ERR_ARG;
+    if (m == 0 || n == 0) return QC_OK;
+    if (bad_matrix(m, n, ldc) || !a || !a_scale || !b || !b_scale || !c) return QC_ERR_ARG;
+    if (k > 131071 || lda > kMaxProductStride || ldb > kMaxProductStride) return QC_ERR_UNSUPPORTED;
+    if (ceil_div(m, 64) > kMaxTiles / ceil_div(n, 16)) return QC_ERR_ARG;
+    if (misaligned(a) || misaligned(b) || misaligned4(a_scale) || misaligned4(b_scale) || misaligned_for(c, ctype))
+        return QC_ERR_ALIGN;
+    return launched(qc::launch_matmul_int8(a, a_scale, lda, b, b_scale, ldb, m, n, k, c, ctype == QC_BF16, ldc,
+                                           hs(stream)));
+}
+
+int qc_ckpt8_bytes(int64_t rows, int64_t dim, int64_t* code_bytes, int64_t* exp_bytes) {
+    if (!code_bytes || !exp_bytes || rows < 0 || dim < 1 || dim > kMaxMatrixElems / (rows > 0 ? rows : 1))
+        return QC_ERR_ARG;
+    *code_bytes = rows * up_to(dim, QC_CKPT_GROUP);
+    *exp_bytes = rows * (up_to(dim, 4 * QC_CKPT_GROUP) / QC_CKPT_GROUP);
+    return QC_OK;
+}
+
+int qc_encode_ckpt8(const void* x, int32_t xtype, int64_t rows, int64_t dim, int64_t ldx, int8_t* codes,
+                    uint8_t* exps, qc_stream_t stream) {
+    if (bad_type(xtype) || bad_matrix(rows, dim, ldx)) return QC_ERR_ARG;
+    if (rows == 0) return QC_OK;
+    if (!x || !codes || !exps) return QC_ERR_ARG;
+    if (misaligned_for(x, xtype) || misaligned(codes) || misaligned(exps)) return QC_ERR_ALIGN;
+    return launched(qc::launch_encode_ckpt8(x, xtype == QC_BF16, ldx, rows, dim, codes, exps, hs(stream)));
+}
+
+int qc_decode_ckpt8(const int8_t* codes, const uint8_t* exps, int64_t rows, int64_t dim, void* out, int32_t otype,
+                    int64_t ldo, qc_stream_t stream) {
+    if (bad_type(otype) || bad_matrix(rows, dim, ldo)) return QC_ERR_ARG;
+    if (rows == 0) return QC_OK;
+    if (!codes || !exps || !out) return QC_ERR_ARG;
+    if (misaligned(codes) || misaligned(exps) || misaligned_for(out, otype)) return QC_ERR_ALIGN;
+    return launched(qc::launch_decode_ckpt8(codes, exps, rows, dim, out, otype == QC_BF16, ldo, hs(stream)));
+}
+
+namespace {
+
+bool bad_wgrad_sizes(int64_t rows, int64_t n, int64_t dim) {
+    return rows < 0 || n < 0 || dim < 1 || dim > kMaxMatrixElems / (rows > n ? rows : (n > 0 ? n : 1)) ||
+           ceil_div(n, 128) > kMaxTiles / ceil_div(dim, 128) || n > kMaxMatrixElems / (rows > 0 ? rows : 1);
+}
+
+}  // namespace
+
+int64_t qc_ckpt8_wgrad_workspace(int64_t rows, int64_t n, int64_t dim, int32_t dytype) {
+    if (bad_type(dytype) || bad_wgrad_sizes(rows, n, dim)) return -1;
+    return n == 0 ? 0 : qc::ckpt8_wgrad_workspace(rows, n, dim, dytype == QC_BF16);
+}
+
+int qc_ckpt8_wgrad(const void* dy, int32_t dytype, int64_t ldy, const int8_t* codes, const uint8_t* exps,
+                   int64_t rows, int64_t n, int64_t dim, void* dw, int32_t wtype, int64_t ldw, int32_t accumulate,
+                   void* workspace, int64_t workspace_bytes, qc_stream_t stream) {
+    if (bad_type(dytype) || bad_type(wtype) || bad_wgrad_sizes(rows, n, dim)) return QC_ERR_ARG;
+    if (accumulate && wtype != QC_F32) return QC_ERR_UNSUPPORTED;
+    if (n == 0) return QC_OK;
+    if (bad_matrix(rows, n, ldy) || bad_matrix(n, dim, ldw) || !dw) return QC_ERR_ARG;
+    if (rows > 0 && (!dy || !codes || !exps)) return QC_ERR_ARG;
+    if (ldy > kMaxProductStride) return QC_ERR_UNSUPPORTED;
+    const int64_t need = qc_ckpt8_wgrad_workspace(rows, n, dim, dytype);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return QC_ERR_ARG;
+    if (misaligned_for(dy, dytype) || misaligned(codes) || misaligned(exps) || misaligned_for(dw, wtype) ||
+        misaligned(workspace))
+        return QC_ERR_ALIGN;
+    return launched(qc::launch_ckpt8_wgrad(dy, dytype == QC_BF16, ldy, codes, exps, rows, n, dim, dw,
+                                           wtype == QC_BF16, ldw, accumulate != 0, workspace, hs(stream)));
+}
+
+int qc_swiglu_ckpt8(const void* gate, const void* up, int32_t xtype, int64_t ldx, int64_t rows, int64_t dim, void* h,
+                    int64_t ldh, int8_t* gate_codes, uint8_t* gate_exps, int8_t* up_codes, uint8_t* up_exps,
+                    qc_stream_t stream) {
+    if (bad_type(xtype) || bad_matrix(rows, dim, ldx) || bad_matrix(rows, dim, ldh)) return QC_ERR_ARG;
+    if (rows == 0) return QC_OK;
+    if (!gate || !up || !h || !gate_codes || !gate_exps || !up_codes || !up_exps) return QC_ERR_ARG;
+    if (misaligned_for(gate, xtype) || misaligned_for(up, xtype) || misaligned_for(h, xtype) ||
+        misaligned(gate_codes) || misaligned(gate_exps) || misaligned(up_codes) || misaligned(up_exps))
+        return QC_ERR_ALIGN;
+    return launched(qc::launch_swiglu_ckpt8(gate, up, xtype == QC_BF16, ldx, rows, dim, h, ldh, gate_codes, gate_exps,
+                                            up_codes, up_exps, hs(stream)));
+}
+
+int qc_swiglu_ckpt8_backward(const void* dh, int32_t dhtype, int64_t lddh, const int8_t* gate_codes,
+                             const uint8_t* gate_exps, const int8_t* up_codes, const uint8_t* up_exps, int64_t rows,
+                             int64_t dim, void* dgate, void* dup, int64_t ldg, qc_stream_t stream) {
+    if (bad_type(dhtype) || bad_matrix(rows, dim, lddh) || bad_matrix(rows, dim, ldg)) return QC_ERR_ARG;
+    if (rows == 0) return QC_OK;
+    if (!dh || !gate_codes || !gate_exps || !up_codes || !up_exps || !dgate || !dup) return QC_ERR_ARG;
+    if (misaligned_for(dh, dhtype) || misaligned_for(dgate, dhtype) || misaligned_for(dup, dhtype) ||
+        misaligned(gate_codes) || misaligned(gate_exps) || misaligned(up_codes) || misaligned(up_exps))
+        return QC_ERR_ALIGN;
+    return launched(qc::launch_swiglu_ckpt8_backward(dh, dhtype == QC_BF16, lddh, gate_codes, gate_exps, up_codes,
+                                                     up_exps, rows, dim, dgate, dup, ldg, hs(stream)));
+}
+
 }  // extern "C"

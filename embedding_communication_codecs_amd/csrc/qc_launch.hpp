@@ -109,4 +109,34 @@ hipError_t launch_topk_accumulate(const float* values, const uint32_t* indices, 
 hipError_t launch_majority_vote(const uint32_t* words, int32_t m, int64_t n, int64_t payload_bytes,
                                 uint32_t* out_words, hipStream_t stream);
 
+// Matrix operators: types arrive as `bf16` flags (else fp32), strides in
+// elements (bytes for codes), sizes positive, codes 16-byte aligned.
+hipError_t launch_encode_int8_rowwise(const void* x, bool bf16, int64_t rows, int64_t dim, int64_t ldx, void* codes,
+                                      int64_t ldq, float* scale, hipStream_t stream);
+
+hipError_t launch_matmul_int8(const void* a, const float* a_scale, int64_t lda, const void* b, const float* b_scale,
+                              int64_t ldb, int64_t m, int64_t n, int64_t k, void* c, bool bf16, int64_t ldc,
+                              hipStream_t stream);
+
+hipError_t launch_encode_ckpt8(const void* x, bool bf16, int64_t ldx, int64_t rows, int64_t dim, void* codes,
+                               void* exps, hipStream_t stream);
+
+hipError_t launch_decode_ckpt8(const void* codes, const void* exps, int64_t rows, int64_t dim, void* out, bool bf16,
+                               int64_t ldo, hipStream_t stream);
+
+hipError_t launch_swiglu_ckpt8(const void* gate, const void* up, bool bf16, int64_t ldx, int64_t rows, int64_t dim,
+                               void* h, int64_t ldh, void* gate_codes, void* gate_exps, void* up_codes,
+                               void* up_exps, hipStream_t stream);
+
+hipError_t launch_swiglu_ckpt8_backward(const void* dh, bool bf16, int64_t lddh, const void* gate_codes,
+                                        const void* gate_exps, const void* up_codes, const void* up_exps,
+                                        int64_t rows, int64_t dim, void* dgate, void* dup, int64_t ldg,
+                                        hipStream_t stream);
+
+// rows may be 0 (dW becomes zero).
+int64_t ckpt8_wgrad_workspace(int64_t rows, int64_t n, int64_t dim, bool bf16);
+hipError_t launch_ckpt8_wgrad(const void* dy, bool dy_bf16, int64_t ldy, const void* codes, const void* exps,
+                              int64_t rows, int64_t n, int64_t dim, void* dw, bool dw_bf16, int64_t ldw,
+                              bool accumulate, void* workspace, hipStream_t stream);
+
 }  // namespace qc

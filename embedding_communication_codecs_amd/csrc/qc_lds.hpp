@@ -1,0 +1,31 @@
+// qc_lds.hpp -- loads from memory straight into LDS, for the tiled products.
+#pragma once
+#include "qc_matrix.hpp"
+
+namespace qc {
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00020000);
+}
+
+// 16 bytes a lane from rsrc + voff + soff straight into LDS, lane i at lds +
+// 16 i.  Written as asm because the compiler takes every LDS access after
+// the builtin as dependent on it and waits for the load before the next
+// fragment read; it returns nothing in registers, and lds_landed() is the
+// wait that its readers need.
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds, int voff, int soff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(voff), "s"(rsrc), "s"(soff)
+                 : "memory");
+}
+// This wave's loads into LDS have landed and its LDS accesses are done; then
+// every wave's are.
+__device__ __forceinline__ void lds_landed() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+}  // namespace qc

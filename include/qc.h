@@ -54,7 +54,7 @@ typedef struct ihipStream_t* qc_stream_t;
 enum qc_status {
     QC_OK = 0,
     QC_ERR_ARG = 1,          /* NULL pointer, negative size, bad bucket/m/offset */
-    QC_ERR_ALIGN = 2,        /* a device pointer is not 16-byte aligned */
+    QC_ERR_ALIGN = 2,        /* a device pointer is not aligned as required (16 bytes unless stated) */
     QC_ERR_UNSUPPORTED = 3,  /* bits/levels/format/dim this entry point lacks */
     QC_ERR_LAUNCH = 4        /* the HIP runtime refused the kernel launch */
 };
@@ -512,6 +512,139 @@ int64_t qc_payload_bytes(int32_t fmt, int64_t n, int32_t group, int32_t bits);
 
 /* Static string naming a status code. */
 const char* qc_status_str(int32_t status);
+
+/*
+ * ---------------------------------------------------------------------
+ * Computing with 8-bit payloads: INT8 rows and their matrix product, and
+ * activations held in 8 bits ("checkpoints") between the forward and the
+ * backward pass.
+ *
+ * Matrices are row-major with a row stride ("ld") in elements, at least the
+ * number of columns; x, h, out, c, dy, dw and their gradients may start at
+ * any element (4-byte aligned for fp32, 2-byte for bf16), so column ranges
+ * of a wider matrix are passed as they are.  Types are QC_F32 or QC_BF16.
+ * Codes and exponents are 16-byte aligned, scales 4-byte aligned.  A
+ * matrix with rows == 0 is a valid empty call.  Row strides are at most
+ * 2^23 elements in the two products.  Unlike the codecs above, these
+ * accept infinities and NaNs and keep them visible, as stated.
+ * ---------------------------------------------------------------------
+ */
+
+/*
+ * Symmetric INT8 with one scale per row: a row is a token of an activation
+ * matrix or an output channel of a weight matrix.
+ *
+ * Per row: scale = max|x| / 127 in fp32; code = the integer nearest to the
+ * real quotient x / scale, ties to even, within [-127, 127]; all codes 0 when
+ * scale == 0.  A row with an infinity or a NaN gets scale NaN and codes 0.
+ *
+ *   x      [rows][dim], row stride ldx, read.
+ *   codes  int8[rows][ldq], written: dim codes a row and zeros up to the next
+ *          multiple of 16; ldq is a multiple of 16, at least that.
+ *   scale  fp32[rows], written.
+ * Errors: ARG (NULL pointer, bad type, rows < 0, dim < 1, a stride below its
+ *         row), ALIGN.
+ */
+int qc_encode_int8_rowwise(const void* x, int32_t xtype, int64_t rows, int64_t dim, int64_t ldx, int8_t* codes,
+                           int64_t ldq, float* scale, qc_stream_t stream);
+
+/*
+ * Matrix product in INT8 with a scale per token and per output channel:
+ *   c[i][j] = (sum over l of a[i][l] * b[j][l]) * a_scale[i] * b_scale[j].
+ * The sum is exact (int32); it is rounded to fp32 once, and each product with
+ * a scale rounds once more, in the order written.  No bias is added.
+ *
+ *   a, a_scale  int8[m][lda] and fp32[m]: tokens.
+ *   b, b_scale  int8[n][ldb] and fp32[n]: weights, a row per output channel.
+ *               (For the gradient of the input, b holds the codes of the
+ *               transposed weights and a those of the output's gradient.)
+ *   lda, ldb    multiples of 16, at least k rounded up to 16; what lies
+ *               between k and the next multiple of 16 is not used.
+ *   k           1 .. 131071 (codes may be -128: 131071 * 128^2 < 2^31).
+ *   c           [m][n] of type ctype, row stride ldc, written.
+ * Errors: ARG (NULL pointer, bad type, m or n < 0, k < 1, a stride below its
+ *         row or not a multiple of 16), ALIGN, UNSUPPORTED (k or a stride
+ *         above its limit).
+ */
+int qc_matmul_int8(const int8_t* a, const float* a_scale, int64_t lda, const int8_t* b, const float* b_scale,
+                   int64_t ldb, int64_t m, int64_t n, int64_t k, void* c, int32_t ctype, int64_t ldc,
+                   qc_stream_t stream);
+
+/*
+ * Checkpoints: a matrix held in 8 bits with a power-of-two step per group of
+ * QC_CKPT_GROUP = 32 consecutive values of a row (the last group of a row may
+ * be short).
+ *
+ * Per group: E = the smallest integer in [-126, 121] with max|x| <= 127 *
+ * 2^E; code = x * 2^-E rounded to nearest even, within [-127, 127]; the
+ * exponent byte is E + 127.  It stands for code * 2^E, which is exact in
+ * bf16 and in fp32.  A group with an infinity or a NaN has byte 255 and codes
+ * 0 and stands for NaNs.
+ *
+ *   codes  int8, row pitch 32 * ceil(dim / 32) bytes, written entirely (zeros
+ *          past dim).
+ *   exps   uint8, row pitch 4 * ceil(dim / 128) bytes, written entirely
+ *          (zeros past the last group).
+ * qc_ckpt8_bytes gives the bytes of both for a matrix (-1 for bad sizes).
+ * qc_decode_ckpt8 writes the values; bf16 output is exact for what
+ * qc_encode_ckpt8 wrote.
+ * Errors: ARG (NULL pointer, bad type, rows < 0, dim < 1, a stride below its
+ *         row), ALIGN.
+ */
+#define QC_CKPT_GROUP 32
+int qc_ckpt8_bytes(int64_t rows, int64_t dim, int64_t* code_bytes, int64_t* exp_bytes);
+int qc_encode_ckpt8(const void* x, int32_t xtype, int64_t rows, int64_t dim, int64_t ldx, int8_t* codes,
+                    uint8_t* exps, qc_stream_t stream);
+int qc_decode_ckpt8(const int8_t* codes, const uint8_t* exps, int64_t rows, int64_t dim, void* out, int32_t otype,
+                    int64_t ldo, qc_stream_t stream);
+
+/*
+ * Weight gradient of a linear layer whose input was kept as a checkpoint:
+ *   dw[j][d] (+)= sum over tokens t of dy[t][j] * X[t][d],
+ * X the values the checkpoint stands for.  Every product is exact and the
+ * sum is taken in fp32, in an order that depends on the sizes alone (the
+ * same call gives the same bits).
+ *
+ *   dy          [rows][n] of type dytype, row stride ldy.
+ *   codes, exps a checkpoint of [rows][dim].
+ *   dw          [n][dim] of type wtype, row stride ldw, written; with
+ *               accumulate != 0 (QC_F32 only) added to.  With rows == 0 it
+ *               becomes zero, or stays as it is.
+ *   workspace   device memory of at least qc_ckpt8_wgrad_workspace() bytes
+ *               (NULL if that is 0), used during the call: where rows are
+ *               many and n * dim small, the tokens are split over several
+ *               blocks, whose sums are held there until they are joined.
+ * Errors: ARG (NULL pointer, bad type, rows or n < 0, dim < 1, a stride below
+ *         its row, too little workspace), ALIGN, UNSUPPORTED (accumulate with
+ *         a bf16 dw, a stride above its limit).
+ */
+int64_t qc_ckpt8_wgrad_workspace(int64_t rows, int64_t n, int64_t dim, int32_t dytype);
+int qc_ckpt8_wgrad(const void* dy, int32_t dytype, int64_t ldy, const int8_t* codes, const uint8_t* exps,
+                   int64_t rows, int64_t n, int64_t dim, void* dw, int32_t wtype, int64_t ldw, int32_t accumulate,
+                   void* workspace, int64_t workspace_bytes, qc_stream_t stream);
+
+/*
+ * Gated activation h = silu(gate) * up, silu(g) = g / (1 + exp(-g)), keeping
+ * gate and up as checkpoints, and its backward pass from those: with G and U
+ * the values they stand for and s = 1 / (1 + exp(-G)),
+ *   dup = dh * G * s,    dgate = dh * U * s * (1 + G * (1 - s)).
+ * Computed in fp32 and rounded once.
+ *
+ *   gate, up    [rows][dim] of one type, both with row stride ldx (side by
+ *               side in one matrix, or apart).
+ *   h           [rows][dim], the same type, row stride ldh, written.
+ *   *_codes, *_exps   checkpoints of [rows][dim], written / read.
+ *   dh          [rows][dim] of type dhtype, row stride lddh.
+ *   dgate, dup  [rows][dim], the same type, both with row stride ldg, written.
+ * Errors: ARG (NULL pointer, bad type, rows < 0, dim < 1, a stride below its
+ *         row), ALIGN.
+ */
+int qc_swiglu_ckpt8(const void* gate, const void* up, int32_t xtype, int64_t ldx, int64_t rows, int64_t dim, void* h,
+                    int64_t ldh, int8_t* gate_codes, uint8_t* gate_exps, int8_t* up_codes, uint8_t* up_exps,
+                    qc_stream_t stream);
+int qc_swiglu_ckpt8_backward(const void* dh, int32_t dhtype, int64_t lddh, const int8_t* gate_codes,
+                             const uint8_t* gate_exps, const int8_t* up_codes, const uint8_t* up_exps, int64_t rows,
+                             int64_t dim, void* dgate, void* dup, int64_t ldg, qc_stream_t stream);
 
 #ifdef __cplusplus
 }
