@@ -9,6 +9,8 @@
 #include "qc_lds.hpp"
 #include "qc_launch.hpp"
 
+#include <type_traits>
+
 namespace qc {
 namespace {
 
@@ -184,6 +186,198 @@ hipError_t launch_tile(const Args& g, T* c, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// ------------------------------------------------------- pipelined tiles
+// One block computes BN channels x BM tokens with WN x WM waves, in stages of
+// 64 bytes of k.  Four stages lie in LDS: one is read, the next has landed,
+// two are on their way, so a load has two stages' time to arrive.  A wave
+// reads its fragments ahead of their use, into the next stage too: the wait
+// for that one, and the only barrier, stand in the middle of a stage, where
+// the fragments already read keep the matrix cores busy across it.
+//
+// Rows are 64 bytes in LDS, piece c of row r in slot c ^ ((r >> 1) & 3):
+// conflict-free for the fragment reads (16 rows, 4 pieces).
+constexpr int SK = 64;
+
+template <int ROWS, int NW>
+struct StageLoader {
+    static constexpr int N = ROWS / 16 / NW;  // loads per wave: 16 rows each
+    int off[N];
+    __amdgpu_buffer_rsrc_t rsrc;
+    __device__ __forceinline__ void init(const uint8_t* mat, int64_t ld, int64_t row0, int64_t rows, int padded,
+                                         int piece, int wave) {
+        const int64_t left = rows - 1 - row0;
+        const int last = left < ROWS - 1 ? (int)left : ROWS - 1;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            off[i] = min((wave * N + i) * 16 + (lane_id() >> 2), last) * (int)ld + piece * 16;
+        rsrc = buffer_of(mat + row0 * ld, last * (int)ld + padded);
+    }
+    __device__ __forceinline__ void load(int i, uint32_t lds, int wave, int k0, int over) const {
+        load_lds16(rsrc, lds + (wave * N + i) * 1024, off[i] - over, k0);
+    }
+};
+
+template <int ROWS, int THREADS>
+__device__ __forceinline__ void zero_stage_tail(uint8_t* lds, int valid) {
+    for (int i = threadIdx.x; i < ROWS * 4; i += THREADS) {
+        const int r = i >> 2, c = i & 3;
+        uint32_t* p = reinterpret_cast<uint32_t*>(lds + r * SK + ((c ^ ((r >> 1) & 3)) << 4));
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const int keep = valid - (c * 16 + w * 4);  // bytes of this word that stay
+            if (keep <= 0) p[w] = 0u;
+            else if (keep < 4) p[w] &= (1u << (8 * keep)) - 1u;
+        }
+    }
+}
+
+template <class T, int BN, int BM, int WN, int WM>
+__global__ void __launch_bounds__(WN * WM * WAVE)
+k_mm_int8_pipe(Args g, T* __restrict__ c) {
+    constexpr int NW = WN * WM, THREADS = NW * WAVE;
+    constexpr int FN = BN / WN / 16, FM = BM / WM / 16;
+    constexpr int AHEAD = FN >= 8 ? 3 : 2;           // weight fragments read ahead (of a ring of 4)
+    constexpr int TB = BN * SK, STAGE = (BN + BM) * SK;  // weights first, then tokens
+    constexpr int LOADS = (BN + BM) / 16 / NW;
+    static_assert(FN % 4 == 0 && FM % (FN / 2) == 0 && LOADS % (FN / 2) == 0, "fragment schedule");
+    __shared__ __align__(1024) uint8_t lds[4 * STAGE];
+
+    const uint32_t tn = (uint32_t)((g.n + BN - 1) / BN), tm = (uint32_t)((g.m + BM - 1) / BM);
+    const Tile2 tile = tile_of<4>(blockIdx.x, tn, tm);
+    const int64_t n0 = (int64_t)tile.x * BN, m0 = (int64_t)tile.y * BM;
+    const int w = __builtin_amdgcn_readfirstlane(wave_id());
+    const int wn = w % WN, wm = w / WN;
+    const int l = lane_id();
+    const int padded = (g.k + 15) & ~15;
+    const int piece = (l & 3) ^ ((l >> 3) & 3);  // of row l / 4
+    StageLoader<BN, NW> lb;
+    StageLoader<BM, NW> la;
+    lb.init(g.b, g.ldb, n0, g.n, padded, piece, w);
+    la.init(g.a, g.lda, m0, g.m, padded, piece, w);
+
+    const int stages = (g.k + 2 * SK - 1) / (2 * SK) * 2;  // an even number; the last may be all zeros
+    const int whole = g.k / SK;                            // stages from here on hold bytes past k
+    const uint32_t lds0 = lds_addr(lds);
+    // load `part` (of LOADS) of stage s; `over` is how far a lane's piece lies past the last one of its row
+    auto fetch_part = [&](int part, int s, int over) {
+        const uint32_t at = lds0 + (s & 3) * STAGE;
+        if (part < lb.N) lb.load(part, at, w, s * SK, over);
+        else la.load(part - lb.N, at + TB, w, s * SK, over);
+    };
+    auto over_of = [&](int s) { return max(s * SK + piece * 16 - (padded - 16), 0); };
+    auto fetch = [&](int s) {
+#pragma unroll
+        for (int part = 0; part < LOADS; ++part) fetch_part(part, s, over_of(s));
+    };
+    auto cut = [&](int s) {
+        if (s >= whole && s < stages) {  // the weights' bytes past k become zeros (integers: one side is enough)
+            zero_stage_tail<BN, THREADS>(lds + (s & 3) * STAGE, max(g.k - s * SK, 0));
+            __syncthreads();
+        }
+    };
+
+    const int frag = (l & 15) * SK + (((l >> 4) ^ ((l >> 1) & 3)) << 4);
+    const int rb = wn * FN * 1024 + frag, ra = TB + wm * FM * 1024 + frag;
+    // s: the stage's buffer, 0 to 3
+    auto read_b = [&](int s, int i) { return *reinterpret_cast<const i32x4*>(lds + s * STAGE + rb + i * 1024); };
+    auto read_a = [&](int s, int j) { return *reinterpret_cast<const i32x4*>(lds + s * STAGE + ra + j * 1024); };
+
+    i32x4 acc[FN][FM] = {};
+    i32x4 fb[4], fa[2][FM];
+    // Stage s, s = PH modulo 4 (PH modulo 2 where it is not FAST).  FAST: stage
+    // s + 3 exists and s + 1 is whole.  A load is issued with each fragment
+    // after the barrier: all of them at once would hold up the waves.
+    auto stage = [&](auto phase, auto fast, int s) {
+        constexpr int PH = decltype(phase)::value, P = PH & 1;
+        constexpr bool FAST = decltype(fast)::value;
+        const int here = FAST ? PH : s & 3, next = FAST ? (PH + 1) & 3 : (s + 1) & 3;
+#pragma unroll
+        for (int i = 0; i < FN; ++i) {
+            if (i == FN / 2) {
+                if (FAST || s + 2 < stages) lds_landed_but<LOADS>();
+                else lds_landed();
+                if (!FAST) cut(s + 1);
+            }
+            fb[(i + AHEAD) % 4] = i + AHEAD < FN ? read_b(here, i + AHEAD) : read_b(next, i + AHEAD - FN);
+            if (i >= FN / 2) {
+                constexpr int E = FM / (FN / 2), D = LOADS / (FN / 2);
+#pragma unroll
+                for (int e = 0; e < E; ++e) fa[P ^ 1][(i - FN / 2) * E + e] = read_a(next, (i - FN / 2) * E + e);
+                // over the stage that every wave has left
+                if (FAST || s + 3 < stages) {
+#pragma unroll
+                    for (int d = 0; d < D; ++d) fetch_part((i - FN / 2) * D + d, s + 3, FAST ? 0 : over_of(s + 3));
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < FM; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[i % 4], fa[P][j], acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);  // keeps the reads where they stand, ahead of their use
+        }
+    };
+    using std::integral_constant;
+
+    fetch(0);
+    fetch(1);
+    if (stages > 2) {
+        fetch(2);
+        lds_landed_but<2 * LOADS>();
+    } else {
+        lds_landed_but<LOADS>();
+    }
+    cut(0);
+#pragma unroll
+    for (int j = 0; j < FM; ++j) fa[0][j] = read_a(0, j);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) fb[i] = read_b(0, i);
+    int s = 0;
+    for (; s + 6 < min(stages, whole); s += 4) {
+        stage(integral_constant<int, 0>{}, std::true_type{}, s);
+        stage(integral_constant<int, 1>{}, std::true_type{}, s + 1);
+        stage(integral_constant<int, 2>{}, std::true_type{}, s + 2);
+        stage(integral_constant<int, 3>{}, std::true_type{}, s + 3);
+    }
+#pragma unroll 1
+    for (; s < stages; s += 2) {
+        stage(integral_constant<int, 0>{}, std::false_type{}, s);
+        stage(integral_constant<int, 1>{}, std::false_type{}, s + 1);
+    }
+
+    // every scale before the first store: a load after a store would wait for it
+    float sa[FM];
+    f32x4 sb[FN];
+#pragma unroll
+    for (int j = 0; j < FM; ++j) sa[j] = g.sa[min(m0 + (wm * FM + j) * 16 + (l & 15), g.m - 1)];
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+        const int64_t col = n0 + (wn * FN + i) * 16 + 4 * (l >> 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sb[i][e] = g.sb[min(col + e, g.n - 1)];
+    }
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+        const int64_t row = m0 + (wm * FM + j) * 16 + (l & 15);
+        T* cr = c + row * g.ldc;
+#pragma unroll
+        for (int i = 0; i < FN; ++i) {
+            const int64_t col = n0 + (wn * FN + i) * 16 + 4 * (l >> 4);
+            const int64_t left = row < g.m ? g.n - col : 0;
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = scaled(acc[i][j][e], sa[j], sb[i][e]);
+            store4(cr + col, left < 4 ? (int)left : 4, v, g.wide);
+        }
+    }
+}
+
+template <class T, int BN, int BM, int WN, int WM>
+hipError_t launch_pipe(const Args& g, T* c, hipStream_t stream) {
+    const int64_t tiles = ((g.n + BN - 1) / BN) * ((g.m + BM - 1) / BM);
+    hipLaunchKernelGGL((k_mm_int8_pipe<T, BN, BM, WN, WM>), dim3((unsigned)tiles), dim3(WN * WM * WAVE), 0, stream, g,
+                       c);
+    return hipGetLastError();
+}
+
 // ------------------------------------------------------------- few tokens
 // One block: NT * 16 channels x MT * 16 tokens, k split over WS waves in
 // chunks of 128 bytes, joined through LDS.  Bound by the weights' bytes: they
@@ -294,8 +488,8 @@ hipError_t launch(const Args& g, T* c, hipStream_t stream) {
     if (g.m <= 32) return launch_few<T, 1, 2, 8>(g, c, stream);
     if (g.m <= 64) return launch_few<T, 2, 4, 8>(g, c, stream);
     const auto tiles = [&](int64_t bn, int64_t bm) { return ((g.n + bn - 1) / bn) * ((g.m + bm - 1) / bm); };
-    if (tiles(256, 256) >= 192) return launch_tile<T, 256, 256, 2, 4>(g, c, stream);
-    if (tiles(128, 128) >= 192) return launch_tile<T, 128, 128, 2, 2>(g, c, stream);
+    if (tiles(256, 256) >= 192) return launch_pipe<T, 256, 256, 2, 4>(g, c, stream);
+    if (tiles(128, 128) >= 192) return launch_pipe<T, 128, 128, 2, 2>(g, c, stream);
     return launch_tile<T, 64, 64, 2, 2>(g, c, stream);
 }
 

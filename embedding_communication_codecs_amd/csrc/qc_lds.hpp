@@ -24,8 +24,30 @@ __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t rsrc, uint32_t
 __device__ __forceinline__ void lds_landed() {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
+// As lds_landed, but the wave's N newest loads may still be on their way.
+template <int N>
+__device__ __forceinline__ void lds_landed_but() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+}
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+
+// Block b of `blocks` to tile (x, y) of a tx x ty grid.  Consecutive blocks go
+// to the eight XCDs in turn; each XCD gets a contiguous run of tiles, walked in
+// columns of G tiles in y, so that the tiles an XCD works on at one time (32
+// compute units) share rows and columns in its L2.
+struct Tile2 {
+    int x, y;
+};
+template <int G>
+__device__ __forceinline__ Tile2 tile_of(uint32_t b, uint32_t tx, uint32_t ty) {
+    const uint32_t total = tx * ty, q = total / 8, r = total % 8, xcd = b % 8;
+    const uint32_t id = xcd * q + min(xcd, r) + b / 8;
+    const uint32_t band = id / (G * tx), first = band * G, rows = min(ty - first, (uint32_t)G);
+    const uint32_t in = id - band * G * tx;
+    return Tile2{(int)(in / rows), (int)(first + in % rows)};
 }
 
 }  // namespace qc
