@@ -13,6 +13,8 @@
 #include "qc_lds.hpp"
 #include "qc_launch.hpp"
 
+#include <type_traits>
+
 namespace qc {
 namespace {
 
@@ -63,6 +65,52 @@ __device__ __forceinline__ void pieces(float x, uint32_t (&p)[3]) {
     p[0] = b >> 16;
     p[1] = rb >> 16;
     p[2] = __float_as_uint(r - __uint_as_float(rb & 0xFFFF0000u)) >> 16;
+}
+
+// A wave's sums to dW.  Lane l holds output channel l % 16 of each of FN
+// tiles, input channels 4 * (l / 16) .. + 3 of each of FD.
+template <int FN, int FD>
+__device__ __forceinline__ void store_dw(const Args& g, f32x4 (&acc)[FD][FN], int64_t n0, int64_t d0) {
+    const int l = lane_id();
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+        const int64_t n = n0 + j * 16 + (l & 15);
+        if (n >= g.n) continue;
+        const int64_t d = d0 + 4 * (l >> 4);
+        if (g.out_bf16) {
+            BF16* o = static_cast<BF16*>(g.out) + n * g.ldw + d;
+#pragma unroll
+            for (int i = 0; i < FD; ++i) {
+                const int64_t left = g.dim - d - 16 * i;
+                const f32x4 v = acc[i][j];
+                if (g.wide && left >= 4)
+                    *reinterpret_cast<u32x2*>(o + 16 * i) = u32x2{bf16_pair(v.x, v.y), bf16_pair(v.z, v.w)};
+                else
+                    for (int e = 0; e < 4; ++e)
+                        if (e < left) put(o + 16 * i + e, v[e]);
+            }
+            continue;
+        }
+        float* o = static_cast<float*>(g.out) + (int64_t)blockIdx.y * g.split_stride + n * g.ldw + d;
+        if (g.accumulate) {  // what is there, all of it before the first store
+#pragma unroll
+            for (int i = 0; i < FD; ++i) {
+                const int64_t left = g.dim - d - 16 * i;
+                if (g.wide && left >= 4) acc[i][j] += *reinterpret_cast<const f32x4*>(o + 16 * i);
+                else
+                    for (int e = 0; e < 4; ++e)
+                        if (e < left) acc[i][j][e] += o[16 * i + e];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < FD; ++i) {
+            const int64_t left = g.dim - d - 16 * i;
+            if (g.wide && left >= 4) *reinterpret_cast<f32x4*>(o + 16 * i) = acc[i][j];
+            else
+                for (int e = 0; e < 4; ++e)
+                    if (e < left) o[16 * i + e] = acc[i][j][e];
+        }
+    }
 }
 
 // One block: BN output channels (columns of dY) x BD input channels (columns
@@ -248,36 +296,225 @@ k_ckpt8_wgrad(Args g) {
         }
     }
 
-    // ---- lane l: output channel l % 16, input channels 4 * (l / 16) .. + 3
+    store_dw<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16);
+}
+
+// --------------------------------------------------------------- pipelined
+// bf16 gradients whose rows are 16-byte aligned, n a multiple of 8.  One block
+// computes BN output x BD input channels with WN x WD waves, in stages of 32
+// tokens.  Everything is loaded straight into LDS, two stages before its use:
+// dY as it is, X as codes and exponent words.  Each lane's 16 codes and their
+// exponents land in a place of its own, so the lane converts them to bf16 as
+// soon as its own wave's loads have landed and writes them to X's tile, which
+// the next barrier shows to the block.  Load batch b holds dY of stage b and
+// X of stage b + 1: converted X is needed one barrier later than landed dY.
+//
+// As in the INT8 product, fragments are read ahead of their use and into
+// the next stage, and the only barrier of a stage stands in its middle.
+constexpr int ST = 32;  // tokens of a stage
+
+template <int BN, int BD, int WN, int WD>
+__global__ void __launch_bounds__(WN * WD * WAVE)
+k_ckpt8_wgrad_pipe(Args g) {
+    constexpr int NW = WN * WD, THREADS = NW * WAVE;
+    constexpr int FN = BN / WN / 16, FD = BD / WD / 16;
+    constexpr int AHEAD = FN >= 8 ? 3 : 2;
+    constexpr int YB = BN * 2, XB = BD * 2;        // bytes of a token in a tile
+    constexpr int YT = ST * YB, XT = ST * XB;
+    constexpr int YN = YT / 1024 / NW;             // loads of dY a wave and stage
+    constexpr int LOADS = YN + 2;                  // and X's codes and exponents
+    constexpr int TPW = 1024 / BD;                 // tokens of X a wave loads
+    constexpr int RAW = 1024 + 256;                // a wave's codes and exponents of a stage
+    static_assert(TPW * NW == ST && FN % 4 == 0 && FD % (FN / 2) == 0 && YN >= 1, "tile shape");
+    constexpr int XAT = 4 * YT, RAT = XAT + 2 * XT;  // LDS: four dY tiles, two X tiles, four raw stages
+    __shared__ __align__(1024) uint8_t lds[RAT + 4 * NW * RAW];
+
+    const uint32_t tn = (uint32_t)((g.n + BN - 1) / BN), td = (uint32_t)((g.dim + BD - 1) / BD);
+    const Tile2 tile = tile_of<4>(blockIdx.x, tn, td);
+    const int64_t n0 = (int64_t)tile.x * BN, d0 = (int64_t)tile.y * BD;
+    const int64_t t_first = (int64_t)blockIdx.y * g.rows_per_split;
+    const int64_t tokens = min(g.rows - t_first, g.rows_per_split);
+    const int l = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id());
+    const int wn = w % WN, wd = w / WN;
+
+    const int stages = (int)((tokens + 2 * ST - 1) / (2 * ST)) * 2;  // even; the last may have no token
+    const int whole = (int)(tokens / ST);
+    const uint32_t lds0 = lds_addr(lds);
+
+    // ---- loads.  Tokens past the end repeat the last one and are zeroed in
+    // LDS; pieces past a row's end repeat its last piece (their sums are not
+    // stored).
+    const uint8_t* ybase = static_cast<const uint8_t*>(g.dy) + (t_first * g.ldy + n0) * 2;
+    const uint8_t* xbase = g.codes + t_first * g.pitch;
+    const uint8_t* ebase = g.exps + t_first * g.epitch;
+    int ytok[YN], ycol[YN], yoff[YN];
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-        const int64_t n = n0 + (wn * FN + j) * 16 + (l & 15);
-        if (n >= g.n) continue;
+    for (int i = 0; i < YN; ++i) {
+        const int t = (w * YN + i) * (1024 / YB) + l / (YB / 16);
+        const int c = (l % (YB / 16)) ^ (2 * (t & 7));
+        ytok[i] = t;
+        ycol[i] = (int)(min(n0 + c * 8, g.n - 8) - n0) * 2;
+        yoff[i] = t * (int)g.ldy * 2 + ycol[i];
+    }
+    const int xt = w * TPW + l / (BD / 16), xq = l % (BD / 16);  // this lane's token of a stage, and 16 codes of it
+    const int xcol = (int)min(d0 + xq * 16, g.pitch - 16);
+    const int ecol = (int)min((d0 + xq * 16) / 128 * 4, g.epitch - 4);
+    auto y_load = [&](auto fast, int i, int s) {
+        int64_t t0 = (int64_t)s * ST;
+        int off = yoff[i];
+        if (!decltype(fast)::value) {
+            const int64_t t = min(t0 + ytok[i], tokens - 1);
+            t0 = min(t0, tokens - 1);
+            off = (int)(t - t0) * (int)g.ldy * 2 + ycol[i];
+        }
+        load_lds16(buffer_of(ybase + t0 * g.ldy * 2, -1), lds0 + (s & 3) * YT + (w * YN + i) * 1024, off, 0);
+    };
+    auto x_load = [&](auto fast, int part, int s) {
+        int64_t t0 = (int64_t)s * ST;
+        int t = xt;
+        if (!decltype(fast)::value) {
+            const int64_t at = min(t0 + xt, tokens - 1);
+            t0 = min(t0, tokens - 1);
+            t = (int)(at - t0);
+        }
+        const uint32_t at = lds0 + RAT + ((s & 3) * NW + w) * RAW;
+        if (part == 0) load_lds16(buffer_of(xbase + t0 * g.pitch, -1), at, t * (int)g.pitch + xcol, 0);
+        else load_lds4(buffer_of(ebase + t0 * g.epitch, -1), at + 1024, t * (int)g.epitch + ecol, 0);
+    };
+    auto load = [&](auto fast, int part, int batch) {  // one of the LOADS of a batch
+        if (part < YN) y_load(fast, part, batch);
+        else x_load(fast, part - YN, batch + 1);
+    };
+    auto load_all = [&](int batch) {
 #pragma unroll
-        for (int i = 0; i < FD; ++i) {
-            const int64_t d = d0 + (wd * FD + i) * 16 + 4 * (l >> 4);
-            const int64_t left = g.dim - d;
-            if (left <= 0) continue;
-            f32x4 v = acc[i][j];
-            if (g.out_bf16) {
-                BF16* o = static_cast<BF16*>(g.out) + n * g.ldw + d;
-                if (g.wide && left >= 4)
-                    *reinterpret_cast<u32x2*>(o) = u32x2{bf16_pair(v.x, v.y), bf16_pair(v.z, v.w)};
-                else
-                    for (int e = 0; e < 4; ++e)
-                        if (e < left) put(o + e, v[e]);
-            } else {
-                float* o = static_cast<float*>(g.out) + (int64_t)blockIdx.y * g.split_stride + n * g.ldw + d;
-                if (g.wide && left >= 4) {
-                    if (g.accumulate) v += *reinterpret_cast<const f32x4*>(o);
-                    *reinterpret_cast<f32x4*>(o) = v;
-                } else {
-                    for (int e = 0; e < 4; ++e)
-                        if (e < left) o[e] = g.accumulate ? o[e] + v[e] : v[e];
+        for (int part = 0; part < LOADS; ++part) load(std::false_type{}, part, batch);
+    };
+
+    // ---- X: this lane's codes of stage s to bf16
+    u32x4 raw;
+    uint32_t eword;
+    auto x_read = [&](int s) {
+        const uint8_t* at = lds + RAT + ((s & 3) * NW + w) * RAW;
+        raw = *reinterpret_cast<const u32x4*>(at + l * 16);
+        eword = *reinterpret_cast<const uint32_t*>(at + 1024 + l * 4);
+    };
+    // Of eight neighbouring lanes the upper four write their second piece
+    // first: eight pieces of 16 bytes in different banks either time.
+    const bool odd = (l & 4) != 0;
+    const int xplace = place(xt, xq * 2 + odd, XB);
+    auto x_put = [&](auto fast, int s) {
+        float step = ckpt_step((eword >> (8 * ((xq >> 1) & 3))) & 0xFFu);
+        u32x4 q = odd ? u32x4{raw.z, raw.w, raw.x, raw.y} : raw;
+        if (!decltype(fast)::value && (int64_t)s * ST + xt >= tokens) {
+            step = 0.0f;
+            q = u32x4{0, 0, 0, 0};
+        }
+        const float off = -128.0f * step;
+        uint8_t* at = lds + XAT + (s & 1) * XT;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const u32x2 a = held4(q[2 * h], step, off), b = held4(q[2 * h + 1], step, off);
+            *reinterpret_cast<u32x4*>(at + (xplace ^ (16 * h))) = u32x4{a.x, a.y, b.x, b.y};
+        }
+    };
+    auto cut = [&](int s) {
+        if (s >= whole && s < stages) {  // tokens past the end: zeros (X's are too, but an infinity times zero is not)
+            const int first = (int)max(tokens - (int64_t)s * ST, (int64_t)0) * YB;
+            for (int at = first + threadIdx.x * 16; at < YT; at += THREADS * 16)
+                *reinterpret_cast<u32x4*>(lds + (s & 3) * YT + at) = u32x4{0, 0, 0, 0};
+            __syncthreads();
+        }
+    };
+
+    // ---- fragments: lane l reads 8 bytes of token r * 16 + l / 4, and gets
+    // four tokens of channel l % 16
+    auto frag_at = [&](int f, int row_bytes) { return place(l >> 2, f * 2 + ((l & 3) >> 1), row_bytes) + 8 * (l & 1); };
+    int yf[FN], xf[FD];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) yf[j] = frag_at(wn * FN + j, YB);
+#pragma unroll
+    for (int i = 0; i < FD; ++i) xf[i] = XAT + frag_at(wd * FD + i, XB);
+    auto frag = [&](int at, int row_bytes) {
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(lds + at));
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(lds + at + 16 * row_bytes));
+        return __builtin_bit_cast(bf16x8, s16x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w});
+    };
+    auto read_y = [&](int buf, int j) { return frag(buf * YT + yf[j], YB); };
+    auto read_x = [&](int buf, int i) { return frag((buf & 1) * XT + xf[i], XB); };
+
+    f32x4 acc[FD][FN] = {};
+    bf16x8 fy[4], fx[2][FD];
+    // Stage s, s = PH modulo 4 (PH modulo 2 where it is not FAST).  FAST: the
+    // stages up to s + 4 are whole.
+    auto stage = [&](auto phase, auto fast, int s) {
+        constexpr int PH = decltype(phase)::value, P = PH & 1;
+        constexpr bool FAST = decltype(fast)::value;
+        const int here = FAST ? PH : s & 3, next = FAST ? (PH + 1) & 3 : (s + 1) & 3;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            if (j == FN / 2) {
+                if (FAST || s + 2 < stages) lds_landed_but<LOADS>();
+                else lds_landed();
+                if (!FAST) cut(s + 1);
+                if (FAST || s + 2 < stages) x_read(s + 2);
+            }
+            fy[(j + AHEAD) % 4] = j + AHEAD < FN ? read_y(here, j + AHEAD) : read_y(next, j + AHEAD - FN);
+            if (j >= FN / 2) {
+                constexpr int E = FD / (FN / 2), D = (LOADS + FN / 2 - 1) / (FN / 2);
+#pragma unroll
+                for (int e = 0; e < E; ++e) fx[P ^ 1][(j - FN / 2) * E + e] = read_x(next, (j - FN / 2) * E + e);
+                // over what every wave has left
+                if (FAST || s + 3 < stages) {
+#pragma unroll
+                    for (int d = 0; d < D; ++d)
+                        if ((j - FN / 2) * D + d < LOADS) load(fast, (j - FN / 2) * D + d, s + 3);
                 }
             }
+            if (j == FN / 2 + 1 && (FAST || s + 2 < stages)) x_put(fast, s + 2);
+#pragma unroll
+            for (int i = 0; i < FD; ++i)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[P][i], fy[j % 4], acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);  // keeps the reads where they stand, ahead of their use
+        }
+    };
+
+    if (stages > 0) {  // an even number: two at least
+        x_load(std::false_type{}, 0, 0);
+        x_load(std::false_type{}, 1, 0);
+        load_all(0);
+        load_all(1);
+        if (stages > 2) {
+            load_all(2);
+            lds_landed_but<2 * LOADS>();
+        } else {
+            lds_landed_but<LOADS>();
+        }
+        cut(0);
+        x_read(0);
+        x_put(std::false_type{}, 0);
+        x_read(1);
+        x_put(std::false_type{}, 1);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < FD; ++i) fx[0][i] = read_x(0, i);
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) fy[j] = read_y(0, j);
+        using std::integral_constant;
+        int s = 0;
+        for (; s + 7 < whole; s += 4) {
+            stage(integral_constant<int, 0>{}, std::true_type{}, s);
+            stage(integral_constant<int, 1>{}, std::true_type{}, s + 1);
+            stage(integral_constant<int, 2>{}, std::true_type{}, s + 2);
+            stage(integral_constant<int, 3>{}, std::true_type{}, s + 3);
+        }
+#pragma unroll 1
+        for (; s < stages; s += 2) {
+            stage(integral_constant<int, 0>{}, std::false_type{}, s);
+            stage(integral_constant<int, 1>{}, std::false_type{}, s + 1);
         }
     }
+    store_dw<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16);
 }
 
 // dW (+)= the splits' partial sums, added in the splits' order.
@@ -324,6 +561,13 @@ Plan plan_of(int64_t rows, int64_t n, int64_t dim, bool bf16) {
 
 int64_t part_pitch(int64_t dim) { return (dim + 3) & ~int64_t(3); }
 
+template <int B, int WN, int WD>
+hipError_t launch_pipe(const Args& g, const Plan& p, hipStream_t stream) {
+    const dim3 grid((unsigned)(((g.n + B - 1) / B) * ((g.dim + B - 1) / B)), (unsigned)p.splits);
+    hipLaunchKernelGGL((k_ckpt8_wgrad_pipe<B, B, WN, WD>), grid, dim3(WN * WD * WAVE), 0, stream, g);
+    return hipGetLastError();
+}
+
 template <int P, bool DMA, int B, int WN, int WD, int TK>
 hipError_t launch_tile(const Args& g, const Plan& p, hipStream_t stream) {
     const dim3 grid((unsigned)(((g.n + B - 1) / B) * ((g.dim + B - 1) / B)), (unsigned)p.splits);
@@ -362,9 +606,9 @@ hipError_t launch_ckpt8_wgrad(const void* dy, bool dy_bf16, int64_t ldy, const v
     const bool dma = dy_bf16 && n % 8 == 0 && ldy % 8 == 0 && reinterpret_cast<uintptr_t>(dy) % 16 == 0;
     hipError_t e;
     if (!dy_bf16) e = launch_tile<3, false, 128, 2, 2, 64>(g, p, stream);
-    else if (p.tile == 256) e = dma ? launch_tile<1, true, 256, 2, 4, 64>(g, p, stream)
+    else if (p.tile == 256) e = dma ? launch_pipe<256, 2, 4>(g, p, stream)
                                     : launch_tile<1, false, 256, 2, 4, 64>(g, p, stream);
-    else e = dma ? launch_tile<1, true, 128, 2, 2, 64>(g, p, stream) : launch_tile<1, false, 128, 2, 2, 64>(g, p, stream);
+    else e = dma ? launch_pipe<128, 2, 2>(g, p, stream) : launch_tile<1, false, 128, 2, 2, 64>(g, p, stream);
     if (e != hipSuccess || p.splits == 1) return e;
     const int64_t pieces4 = n * (part_pitch(dim) / 4), blocks = (pieces4 + 255) / 256;
     hipLaunchKernelGGL(k_ckpt8_wgrad_join, dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), dim3(256), 0,

@@ -261,10 +261,11 @@ k_mm_int8_pipe(Args g, T* __restrict__ c) {
     // load `part` (of LOADS) of stage s; `over` is how far a lane's piece lies past the last one of its row
     auto fetch_part = [&](int part, int s, int over) {
         const uint32_t at = lds0 + (s & 3) * STAGE;
-        if (part < lb.N) lb.load(part, at, w, s * SK, over);
-        else la.load(part - lb.N, at + TB, w, s * SK, over);
+        const int k0 = min(s * SK, padded - 16);
+        if (part < lb.N) lb.load(part, at, w, k0, over);
+        else la.load(part - lb.N, at + TB, w, k0, over);
     };
-    auto over_of = [&](int s) { return max(s * SK + piece * 16 - (padded - 16), 0); };
+    auto over_of = [&](int s) { return max(min(s * SK, padded - 16) + piece * 16 - (padded - 16), 0); };
     auto fetch = [&](int s) {
 #pragma unroll
         for (int part = 0; part < LOADS; ++part) fetch_part(part, s, over_of(s));

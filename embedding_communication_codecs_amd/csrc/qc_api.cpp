@@ -594,7 +594,7 @@ int qc_ckpt8_wgrad(const void* dy, int32_t dytype, int64_t ldy, const int8_t* co
     if (n == 0) return QC_OK;
     if (bad_matrix(rows, n, ldy) || bad_matrix(n, dim, ldw) || !dw) return QC_ERR_ARG;
     if (rows > 0 && (!dy || !codes || !exps)) return QC_ERR_ARG;
-    if (ldy > kMaxProductStride) return QC_ERR_UNSUPPORTED;
+    if (ldy > kMaxProductStride || dim > kMaxProductStride) return QC_ERR_UNSUPPORTED;
     const int64_t need = qc_ckpt8_wgrad_workspace(rows, n, dim, dytype);
     if (need > 0 && (!workspace || workspace_bytes < need)) return QC_ERR_ARG;
     if (misaligned_for(dy, dytype) || misaligned(codes) || misaligned(exps) || misaligned_for(dw, wtype) ||

@@ -19,6 +19,13 @@ __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t rsrc, uint32_t
                  : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(voff), "s"(rsrc), "s"(soff)
                  : "memory");
 }
+// The same with 4 bytes a lane, lane i at lds + 4 i.
+__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds, int voff, int soff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(voff), "s"(rsrc), "s"(soff)
+                 : "memory");
+}
 // This wave's loads into LDS have landed and its LDS accesses are done; then
 // every wave's are.
 __device__ __forceinline__ void lds_landed() {

@@ -524,8 +524,8 @@ const char* qc_status_str(int32_t status);
  * any element (4-byte aligned for fp32, 2-byte for bf16), so column ranges
  * of a wider matrix are passed as they are.  Types are QC_F32 or QC_BF16.
  * Codes and exponents are 16-byte aligned, scales 4-byte aligned.  A
- * matrix with rows == 0 is a valid empty call.  Row strides are at most
- * 2^23 elements in the two products.  Unlike the codecs above, these
+ * matrix with rows == 0 is a valid empty call.  Rows are at most
+ * 2^23 elements apart in the two products.  Unlike the codecs above, these
  * accept infinities and NaNs and keep them visible, as stated.
  * ---------------------------------------------------------------------
  */
