@@ -137,11 +137,20 @@ def _ptr(t, need_bytes: int | None, name: str):
     return t.data_ptr()
 
 
+_raw_stream = None  # the current stream's handle, by device index
+
+
 def _stream(stream):
     if stream is None:
-        import torch
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
 
-        return torch.cuda.current_stream().cuda_stream
+            # without the Stream object that torch.cuda.current_stream() makes (2.7 us a call)
+            get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            _raw_stream = ((lambda: get(torch.cuda.current_device())) if get else
+                           (lambda: torch.cuda.current_stream().cuda_stream))
+        return _raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -435,6 +444,10 @@ def _mat(t, rows, cols, ld, esize, name):
         raise ValueError(f"{name} must be a GPU tensor")
     if t.element_size() != esize:
         raise ValueError(f"{name} has elements of {t.element_size()} bytes, the call takes {esize}")
+    if t.dim() == 2 and t.stride() == (ld, 1) and t.shape[0] >= rows and t.shape[1] >= cols:
+        return t.data_ptr()  # the common case; the rest finds out what is wrong, or that nothing is
+    if t.dim() > 2 and not t.is_contiguous():
+        raise ValueError(f"{name} must be a matrix, or contiguous")
     if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must have neighbouring elements in a row")
     if t.dim() == 2 and t.shape[0] > 1 and t.stride(0) != ld:
@@ -452,7 +465,8 @@ def _esize(qtype):
 
 
 def _ckpt(codes, exps, rows, dim, name):
-    cb, eb = (ckpt8_bytes(rows, dim) if rows >= 0 and dim > 0 else (None, None))
+    cb = rows * (-(-dim // QC_CKPT_GROUP) * QC_CKPT_GROUP)
+    eb = rows * (-(-dim // (4 * QC_CKPT_GROUP)) * 4)
     return _ptr(codes, cb, name + "codes"), _ptr(exps, eb, name + "exps")
 
 

@@ -325,7 +325,7 @@ k_ckpt8_wgrad_pipe(Args g) {
     constexpr int LOADS = YN + 2;                  // and X's codes and exponents
     constexpr int TPW = 1024 / BD;                 // tokens of X a wave loads
     constexpr int RAW = 1024 + 256;                // a wave's codes and exponents of a stage
-    static_assert(TPW * NW == ST && FN % 4 == 0 && FD % (FN / 2) == 0 && YN >= 1, "tile shape");
+    static_assert(TPW * NW == ST && FN % 4 == 0 && YN >= 1, "tile shape");
     constexpr int XAT = 4 * YT, RAT = XAT + 2 * XT;  // LDS: four dY tiles, two X tiles, four raw stages
     __shared__ __align__(1024) uint8_t lds[RAT + 4 * NW * RAW];
 
@@ -461,14 +461,13 @@ k_ckpt8_wgrad_pipe(Args g) {
             }
             fy[(j + AHEAD) % 4] = j + AHEAD < FN ? read_y(here, j + AHEAD) : read_y(next, j + AHEAD - FN);
             if (j >= FN / 2) {
-                constexpr int E = FD / (FN / 2), D = (LOADS + FN / 2 - 1) / (FN / 2);
+                constexpr int H = FN / 2;  // this iteration's share of X's fragments and of the loads
 #pragma unroll
-                for (int e = 0; e < E; ++e) fx[P ^ 1][(j - FN / 2) * E + e] = read_x(next, (j - FN / 2) * E + e);
+                for (int e = (j - H) * FD / H; e < (j - H + 1) * FD / H; ++e) fx[P ^ 1][e] = read_x(next, e);
                 // over what every wave has left
                 if (FAST || s + 3 < stages) {
 #pragma unroll
-                    for (int d = 0; d < D; ++d)
-                        if ((j - FN / 2) * D + d < LOADS) load(fast, (j - FN / 2) * D + d, s + 3);
+                    for (int d = (j - H) * LOADS / H; d < (j - H + 1) * LOADS / H; ++d) load(fast, d, s + 3);
                 }
             }
             if (j == FN / 2 + 1 && (FAST || s + 2 < stages)) x_put(fast, s + 2);

@@ -65,18 +65,18 @@ struct Loader {
     static constexpr int N = ROWS / 8 / NW;  // loads per wave
     int off[N];
     __amdgpu_buffer_rsrc_t rsrc;
-    __device__ __forceinline__ void init(const uint8_t* mat, int64_t ld, int64_t row0, int64_t rows, int padded) {
+    __device__ __forceinline__ void init(const uint8_t* mat, int64_t ld, int64_t row0, int64_t rows, int padded,
+                                         int wave) {
         const int64_t left = rows - 1 - row0;
         const int last = left < ROWS - 1 ? (int)left : ROWS - 1;
         const int lrow = lane_id() >> 3, piece = (lane_id() & 7) ^ lrow;
 #pragma unroll
-        for (int i = 0; i < N; ++i) off[i] = min((wave_id() * N + i) * 8 + lrow, last) * (int)ld + piece * 16;
+        for (int i = 0; i < N; ++i) off[i] = min((wave * N + i) * 8 + lrow, last) * (int)ld + piece * 16;
         rsrc = buffer_of(mat + row0 * ld, last * (int)ld + padded);
     }
-    // `over`: how far this lane's piece at k0 lies past the last one of the row
-    __device__ __forceinline__ void load(uint32_t lds, int k0, int over) const {
-#pragma unroll
-        for (int i = 0; i < N; ++i) load_lds16(rsrc, lds + (wave_id() * N + i) * 1024, off[i] - over, k0);
+    // load `i` of N; `over`: how far this lane's piece at k0 lies past the last one of the row
+    __device__ __forceinline__ void load(int i, uint32_t lds, int wave, int k0, int over) const {
+        load_lds16(rsrc, lds + (wave * N + i) * 1024, off[i] - over, k0);
     }
 };
 
@@ -106,14 +106,15 @@ k_mm_int8(Args g, T* __restrict__ c) {
     const int64_t tn = (g.n + BN - 1) / BN;
     const int64_t tile = blockIdx.x;
     const int64_t n0 = (tile % tn) * BN, m0 = (tile / tn) * BM;
-    const int wn = wave_id() % WN, wm = wave_id() / WN;
+    const int w = __builtin_amdgcn_readfirstlane(wave_id());
+    const int wn = w % WN, wm = w / WN;
     const int l = lane_id();
 
     const int padded = (g.k + 15) & ~15;
     Loader<BN, NW> lb;
     Loader<BM, NW> la;
-    lb.init(g.b, g.ldb, n0, g.n, padded);
-    la.init(g.a, g.lda, m0, g.m, padded);
+    lb.init(g.b, g.ldb, n0, g.n, padded, w);
+    la.init(g.a, g.lda, m0, g.m, padded, w);
     const int piece16 = ((l & 7) ^ (l >> 3)) * 16;
 
     i32x4 acc[FN][FM] = {};
@@ -143,8 +144,10 @@ k_mm_int8(Args g, T* __restrict__ c) {
     const uint32_t lds0 = lds_addr(lds);
     auto fetch = [&](int buf, int t) {
         const int over = max(t * BK + piece16 - (padded - 16), 0);
-        lb.load(lds0 + buf * TILE, t * BK, over);
-        la.load(lds0 + buf * TILE + TB, t * BK, over);
+#pragma unroll
+        for (int i = 0; i < lb.N; ++i) lb.load(i, lds0 + buf * TILE, w, t * BK, over);
+#pragma unroll
+        for (int i = 0; i < la.N; ++i) la.load(i, lds0 + buf * TILE + TB, w, t * BK, over);
     };
     fetch(0, 0);
     for (int t = 0; t < steps; ++t) {
@@ -188,59 +191,29 @@ hipError_t launch_tile(const Args& g, T* c, hipStream_t stream) {
 
 // ------------------------------------------------------- pipelined tiles
 // One block computes BN channels x BM tokens with WN x WM waves, in stages of
-// 64 bytes of k.  Four stages lie in LDS: one is read, the next has landed,
-// two are on their way, so a load has two stages' time to arrive.  A wave
-// reads its fragments ahead of their use, into the next stage too: the wait
-// for that one, and the only barrier, stand in the middle of a stage, where
-// the fragments already read keep the matrix cores busy across it.
+// 128 bytes of k, two of them in LDS.  A wave reads its fragments ahead of
+// their use, into the next stage too; the wait for that stage, and the only
+// barrier, stand where the last fragments of this one have been read, and the
+// fragments already in registers keep the matrix cores busy across it.  The
+// loads of the stage after next follow at once, over the one just left, and
+// have a whole stage's time to arrive.
 //
-// Rows are 64 bytes in LDS, piece c of row r in slot c ^ ((r >> 1) & 3):
-// conflict-free for the fragment reads (16 rows, 4 pieces).
-constexpr int SK = 64;
-
-template <int ROWS, int NW>
-struct StageLoader {
-    static constexpr int N = ROWS / 16 / NW;  // loads per wave: 16 rows each
-    int off[N];
-    __amdgpu_buffer_rsrc_t rsrc;
-    __device__ __forceinline__ void init(const uint8_t* mat, int64_t ld, int64_t row0, int64_t rows, int padded,
-                                         int piece, int wave) {
-        const int64_t left = rows - 1 - row0;
-        const int last = left < ROWS - 1 ? (int)left : ROWS - 1;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            off[i] = min((wave * N + i) * 16 + (lane_id() >> 2), last) * (int)ld + piece * 16;
-        rsrc = buffer_of(mat + row0 * ld, last * (int)ld + padded);
-    }
-    __device__ __forceinline__ void load(int i, uint32_t lds, int wave, int k0, int over) const {
-        load_lds16(rsrc, lds + (wave * N + i) * 1024, off[i] - over, k0);
-    }
-};
-
-template <int ROWS, int THREADS>
-__device__ __forceinline__ void zero_stage_tail(uint8_t* lds, int valid) {
-    for (int i = threadIdx.x; i < ROWS * 4; i += THREADS) {
-        const int r = i >> 2, c = i & 3;
-        uint32_t* p = reinterpret_cast<uint32_t*>(lds + r * SK + ((c ^ ((r >> 1) & 3)) << 4));
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const int keep = valid - (c * 16 + w * 4);  // bytes of this word that stay
-            if (keep <= 0) p[w] = 0u;
-            else if (keep < 4) p[w] &= (1u << (8 * keep)) - 1u;
-        }
-    }
-}
-
+// 128 bytes of k and not 64: what bounds these kernels is the rate at which a
+// compute unit loads, and that depends on how much of a row a load takes.
+// Measured, from L2, 256 rows 8 KiB apart, all compute units: 16 rows x 64
+// bytes a load 50 bytes/ns a compute unit, 8 x 128 72, 4 x 256 134.
 template <class T, int BN, int BM, int WN, int WM>
 __global__ void __launch_bounds__(WN * WM * WAVE)
 k_mm_int8_pipe(Args g, T* __restrict__ c) {
     constexpr int NW = WN * WM, THREADS = NW * WAVE;
     constexpr int FN = BN / WN / 16, FM = BM / WM / 16;
-    constexpr int AHEAD = FN >= 8 ? 3 : 2;           // weight fragments read ahead (of a ring of 4)
-    constexpr int TB = BN * SK, STAGE = (BN + BM) * SK;  // weights first, then tokens
-    constexpr int LOADS = (BN + BM) / 16 / NW;
-    static_assert(FN % 4 == 0 && FM % (FN / 2) == 0 && LOADS % (FN / 2) == 0, "fragment schedule");
-    __shared__ __align__(1024) uint8_t lds[4 * STAGE];
+    constexpr int AHEAD = FN >= 8 ? 3 : 2;                 // weight fragments read ahead (of a ring of 4)
+    constexpr int STEPS = 2 * FN, TURN = STEPS - FN / 2;   // a step: one weight fragment; the barrier's step
+    constexpr int TB = BN * BK, STAGE = (BN + BM) * BK;    // weights first, then tokens
+    constexpr int LB = BN / 8 / NW, LOADS = (BN + BM) / 8 / NW;
+    static_assert(FN % 4 == 0 && FM >= 1 && (BN / 8) % NW == 0 && (BM / 8) % NW == 0, "tile shape");
+    static_assert(STEPS - 1 - AHEAD <= TURN && STEPS - AHEAD >= TURN, "a stage's last read comes before the barrier, the next one's first after it");
+    __shared__ __align__(1024) uint8_t lds[2 * STAGE];
 
     const uint32_t tn = (uint32_t)((g.n + BN - 1) / BN), tm = (uint32_t)((g.m + BM - 1) / BM);
     const Tile2 tile = tile_of<4>(blockIdx.x, tn, tm);
@@ -249,100 +222,92 @@ k_mm_int8_pipe(Args g, T* __restrict__ c) {
     const int wn = w % WN, wm = w / WN;
     const int l = lane_id();
     const int padded = (g.k + 15) & ~15;
-    const int piece = (l & 3) ^ ((l >> 3) & 3);  // of row l / 4
-    StageLoader<BN, NW> lb;
-    StageLoader<BM, NW> la;
-    lb.init(g.b, g.ldb, n0, g.n, padded, piece, w);
-    la.init(g.a, g.lda, m0, g.m, padded, piece, w);
+    Loader<BN, NW> lb;
+    Loader<BM, NW> la;
+    lb.init(g.b, g.ldb, n0, g.n, padded, w);
+    la.init(g.a, g.lda, m0, g.m, padded, w);
+    const int piece16 = ((l & 7) ^ (l >> 3)) * 16;
 
-    const int stages = (g.k + 2 * SK - 1) / (2 * SK) * 2;  // an even number; the last may be all zeros
-    const int whole = g.k / SK;                            // stages from here on hold bytes past k
+    const int stages = (g.k + BK - 1) / BK;
+    const int whole = g.k / BK;  // a stage from here on (one at most) holds bytes past k
     const uint32_t lds0 = lds_addr(lds);
-    // load `part` (of LOADS) of stage s; `over` is how far a lane's piece lies past the last one of its row
-    auto fetch_part = [&](int part, int s, int over) {
-        const uint32_t at = lds0 + (s & 3) * STAGE;
-        const int k0 = min(s * SK, padded - 16);
-        if (part < lb.N) lb.load(part, at, w, k0, over);
-        else la.load(part - lb.N, at + TB, w, k0, over);
+    auto over_of = [&](int s) { return max(s * BK + piece16 - (padded - 16), 0); };
+    auto fetch_part = [&](int part, int buf, int s, int over) {  // one of LOADS
+        if (part < LB) lb.load(part, lds0 + buf * STAGE, w, s * BK, over);
+        else la.load(part - LB, lds0 + buf * STAGE + TB, w, s * BK, over);
     };
-    auto over_of = [&](int s) { return max(min(s * SK, padded - 16) + piece * 16 - (padded - 16), 0); };
     auto fetch = [&](int s) {
 #pragma unroll
-        for (int part = 0; part < LOADS; ++part) fetch_part(part, s, over_of(s));
+        for (int part = 0; part < LOADS; ++part) fetch_part(part, s & 1, s, over_of(s));
     };
     auto cut = [&](int s) {
-        if (s >= whole && s < stages) {  // the weights' bytes past k become zeros (integers: one side is enough)
-            zero_stage_tail<BN, THREADS>(lds + (s & 3) * STAGE, max(g.k - s * SK, 0));
+        if (s >= whole) {  // the weights' bytes past k become zeros (integers: one side is enough)
+            zero_tail<BN, THREADS>(lds + (s & 1) * STAGE, g.k - s * BK);
             __syncthreads();
         }
     };
 
-    const int frag = (l & 15) * SK + (((l >> 4) ^ ((l >> 1) & 3)) << 4);
-    const int rb = wn * FN * 1024 + frag, ra = TB + wm * FM * 1024 + frag;
-    // s: the stage's buffer, 0 to 3
-    auto read_b = [&](int s, int i) { return *reinterpret_cast<const i32x4*>(lds + s * STAGE + rb + i * 1024); };
-    auto read_a = [&](int s, int j) { return *reinterpret_cast<const i32x4*>(lds + s * STAGE + ra + j * 1024); };
+    // fragment addresses: row l % 16, piece kk * 4 + l / 16
+    const int frag = (l & 15) * BK + (((l >> 4) ^ (l & 7)) << 4);
+    const int rb = wn * FN * 2048 + frag, ra = TB + wm * FM * 2048 + frag;
+    auto read_b = [&](int buf, int q) {
+        return *reinterpret_cast<const i32x4*>(lds + buf * STAGE + (rb ^ (q / FN * 64)) + q % FN * 2048);
+    };
+    auto read_a = [&](int buf, int kk, int j) {
+        return *reinterpret_cast<const i32x4*>(lds + buf * STAGE + (ra ^ (kk * 64)) + j * 2048);
+    };
 
     i32x4 acc[FN][FM] = {};
     i32x4 fb[4], fa[2][FM];
-    // Stage s, s = PH modulo 4 (PH modulo 2 where it is not FAST).  FAST: stage
-    // s + 3 exists and s + 1 is whole.  A load is issued with each fragment
-    // after the barrier: all of them at once would hold up the waves.
-    auto stage = [&](auto phase, auto fast, int s) {
-        constexpr int PH = decltype(phase)::value, P = PH & 1;
+    // Stage s in buffer `buf`.  FAST: stages s + 1 and s + 2 exist and are whole.
+    auto stage = [&](int buf, auto fast, int s) {
         constexpr bool FAST = decltype(fast)::value;
-        const int here = FAST ? PH : s & 3, next = FAST ? (PH + 1) & 3 : (s + 1) & 3;
 #pragma unroll
-        for (int i = 0; i < FN; ++i) {
-            if (i == FN / 2) {
-                if (FAST || s + 2 < stages) lds_landed_but<LOADS>();
-                else lds_landed();
+        for (int q = 0; q < STEPS; ++q) {
+            const int kk = q / FN, i = q % FN;
+            if (q + AHEAD < STEPS) fb[(q + AHEAD) % 4] = read_b(buf, q + AHEAD);
+            if (q == TURN && (FAST || s + 1 < stages)) {
+                lds_landed();
                 if (!FAST) cut(s + 1);
             }
-            fb[(i + AHEAD) % 4] = i + AHEAD < FN ? read_b(here, i + AHEAD) : read_b(next, i + AHEAD - FN);
+            if (q + AHEAD >= STEPS) fb[(q + AHEAD) % 4] = read_b(buf ^ 1, q + AHEAD - STEPS);
             if (i >= FN / 2) {
-                constexpr int E = FM / (FN / 2), D = LOADS / (FN / 2);
+                constexpr int H = FN / 2;  // this step's share of the token fragments and of the loads
 #pragma unroll
-                for (int e = 0; e < E; ++e) fa[P ^ 1][(i - FN / 2) * E + e] = read_a(next, (i - FN / 2) * E + e);
-                // over the stage that every wave has left
-                if (FAST || s + 3 < stages) {
+                for (int e = (i - H) * FM / H; e < (i - H + 1) * FM / H; ++e)
+                    fa[kk ^ 1][e] = kk == 0 ? read_a(buf, 1, e) : read_a(buf ^ 1, 0, e);
+                if (kk == 1 && (FAST || s + 2 < stages)) {
 #pragma unroll
-                    for (int d = 0; d < D; ++d) fetch_part((i - FN / 2) * D + d, s + 3, FAST ? 0 : over_of(s + 3));
+                    for (int d = (i - H) * LOADS / H; d < (i - H + 1) * LOADS / H; ++d)
+                        fetch_part(d, buf, s + 2, FAST ? 0 : over_of(s + 2));
                 }
             }
 #pragma unroll
             for (int j = 0; j < FM; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[i % 4], fa[P][j], acc[i][j], 0, 0, 0);
+                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[q % 4], fa[kk][j], acc[i][j], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);  // keeps the reads where they stand, ahead of their use
         }
     };
-    using std::integral_constant;
 
     fetch(0);
-    fetch(1);
-    if (stages > 2) {
-        fetch(2);
-        lds_landed_but<2 * LOADS>();
-    } else {
+    if (stages > 1) {
+        fetch(1);
         lds_landed_but<LOADS>();
+    } else {
+        lds_landed();
     }
     cut(0);
 #pragma unroll
-    for (int j = 0; j < FM; ++j) fa[0][j] = read_a(0, j);
+    for (int j = 0; j < FM; ++j) fa[0][j] = read_a(0, 0, j);
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) fb[i] = read_b(0, i);
+    for (int q = 0; q < AHEAD; ++q) fb[q] = read_b(0, q);
     int s = 0;
-    for (; s + 6 < min(stages, whole); s += 4) {
-        stage(integral_constant<int, 0>{}, std::true_type{}, s);
-        stage(integral_constant<int, 1>{}, std::true_type{}, s + 1);
-        stage(integral_constant<int, 2>{}, std::true_type{}, s + 2);
-        stage(integral_constant<int, 3>{}, std::true_type{}, s + 3);
+    for (; s + 3 < whole; s += 2) {
+        stage(0, std::true_type{}, s);
+        stage(1, std::true_type{}, s + 1);
     }
 #pragma unroll 1
-    for (; s < stages; s += 2) {
-        stage(integral_constant<int, 0>{}, std::false_type{}, s);
-        stage(integral_constant<int, 1>{}, std::false_type{}, s + 1);
-    }
+    for (; s < stages; ++s) stage(s & 1, std::false_type{}, s);
 
     // every scale before the first store: a load after a store would wait for it
     float sa[FM];
@@ -413,7 +378,7 @@ k_mm_int8_few(Args g, T* __restrict__ c) {
     auto get = [&](Chunk& f, int ch) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int at = ch * BK + (l >> 4) * 32 + h * 16;
+            const int at = ch * BK + h * 64 + (l >> 4) * 16;
             const int in = min(at, padded - 16);  // pieces past the row repeat its last one
 #pragma unroll
             for (int i = 0; i < NT; ++i) f.b[i][h] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(pb[i] + in));
@@ -427,7 +392,7 @@ k_mm_int8_few(Args g, T* __restrict__ c) {
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int keep = g.k - (ch * BK + (l >> 4) * 32 + h * 16 + e * 4);
+                    const int keep = g.k - (ch * BK + h * 64 + (l >> 4) * 16 + e * 4);
                     const uint32_t mask = keep <= 0 ? 0u : (keep >= 4 ? ~0u : (1u << (8 * keep)) - 1u);
 #pragma unroll
                     for (int i = 0; i < NT; ++i) f.b[i][h][e] &= (int)mask;

@@ -187,6 +187,21 @@ def test_matmul_large_tiles(qc, m, n, k, dtype):
     assert torch.equal(c.get(), want)
 
 
+@pytest.mark.parametrize("m,n,k", [(3700, 3400, 1500), (2000, 1900, 1024), (1500, 2100, 641), (3584, 3840, 448)])
+def test_matmul_large_tiles_long_k(qc, m, n, k):
+    """The same over enough k for the steady state of the pipeline; codes small
+    enough that every sum is below 2^24 and fp32 on the host exact."""
+    a, b = codes_of(m, k, 21) // 2, codes_of(n, k, 22) // 2
+    c = Buf(m, n, n, BF16)
+    kp = ref.up(k, 16)
+    sa, sb = torch.full((m,), 0.5), torch.full((n,), 2.0 ** -7)
+    qc.qc_matmul_int8(strided(a, kp), sa.cuda(), kp, strided(b, kp), sb.cuda(), kp, m, n, k, c.t, qc.QC_BF16, n)
+    torch.cuda.synchronize()
+    c.check()
+    want = (torch.from_numpy(a.numpy().astype(np.float32) @ b.numpy().astype(np.float32).T) * 2.0 ** -8).to(BF16)
+    assert torch.equal(c.get(), want)
+
+
 @pytest.mark.parametrize("m,n,k,lda,ldb,ldc,skip", [(5, 40, 100, 128, 160, 43, 1), (40, 70, 333, 352, 336, 71, 3),
                                                      (200, 130, 77, 96, 80, 132, 2), (300, 300, 300, 320, 304, 304, 0)])
 def test_matmul_strides(qc, m, n, k, lda, ldb, ldc, skip):
@@ -307,7 +322,7 @@ def check_wgrad(got, dy, v, wtype, start=None):
     assert rel <= (4e-3 if wtype is BF16 else 1e-5), rel
 
 
-WG = [(1, 8, 16), (1, 1, 1), (5, 33, 70), (63, 16, 32), (64, 128, 128), (65, 130, 127), (130, 250, 500), (200, 64, 257),
+WG = [(2049, 64, 130), (4500, 264, 200), (1, 8, 16), (1, 1, 1), (5, 33, 70), (63, 16, 32), (64, 128, 128), (65, 130, 127), (130, 250, 500), (200, 64, 257),
       (257, 384, 129), (1000, 40, 72), (3000, 64, 100), (515, 8, 300)]
 
 
@@ -321,7 +336,8 @@ def test_wgrad(qc, rows, n, dim, dtype):
     assert torch.equal(got, again)
 
 
-@pytest.mark.parametrize("rows,n,dim", [(70, 3600, 3700), (129, 3504, 3425), (64, 4095, 3300)])
+@pytest.mark.parametrize("rows,n,dim", [(70, 3600, 3700), (129, 3504, 3425), (64, 4095, 3300), (609, 3600, 3601),
+                                        (512, 3584, 3840), (289, 3592, 3500)])
 def test_wgrad_large_tiles(qc, rows, n, dim):
     dy, x = ref.matrix(rows, n, 1, BF16), ref.matrix(rows, dim, 2, BF16)
     got, v = run_wgrad(qc, dy, x)
