@@ -50,169 +50,92 @@ __device__ __forceinline__ void store4(float* p, int left, const float (&v)[4], 
     }
 }
 
-constexpr int BK = 128;  // bytes of k per step: one LDS row, eight 16-byte pieces
+// Rows of a matrix lie in LDS as K bytes (128 or 256), their 16-byte pieces
+// permuted so that the fragment reads are free of bank conflicts: a
+// ds_read_b128 takes, in one go, a piece of eight neighbouring rows and the
+// piece beside it of eight others; these 16 have to differ modulo 256 bytes.
+template <int K>
+__device__ __forceinline__ int slot_of(int row, int piece) {
+    static_assert(K == 128 || K == 256, "row bytes");
+    return piece ^ (K == 128 ? row & 7 : (2 * row) & 15);
+}
 
-// Rows [row0, row0 + ROWS) of a matrix, bytes [k0, k0 + 128) of each, into
-// LDS.  A wave's load writes 1,024 consecutive LDS bytes, eight rows; piece
-// c of row r goes to slot c ^ (r & 7), so that the fragment reads (16 rows,
-// one piece each) spread over all banks.  Rows past the matrix repeat its
-// last row (their results are not stored) and pieces past the row's padded
-// end repeat its last piece (zeroed in LDS before use), so every address is
-// inside the matrix.  Buffer addressing: a lane's offset inside the tile in a
-// VGPR, k0 in an SGPR.
-template <int ROWS, int NW>
+// Rows [row0, row0 + ROWS) of a matrix, K bytes from k0 of each, into LDS by
+// NW waves; a load takes 1,024 / K rows.  Rows past the matrix repeat its
+// last row (their results are not stored) and pieces past a row's padded end
+// repeat its last piece (made zeros before use), so every address is inside
+// the matrix.  Buffer addressing: a lane's offset inside the tile in a VGPR,
+// k0 in an SGPR.
+//
+// What bounds these kernels is the rate at which a compute unit loads, and
+// that depends on how much of a row a load takes.  Measured from L2, 256
+// rows 8 KiB apart, all compute units at work: 16 rows x 64 bytes a load 50
+// bytes/ns a compute unit, 8 x 128 72, 4 x 256 134, 1 x 1,024 148.
+template <int ROWS, int K, int NW>
 struct Loader {
-    static constexpr int N = ROWS / 8 / NW;  // loads per wave
+    static constexpr int RPL = 1024 / K, N = ROWS / RPL / NW;  // rows a load, loads a wave
+    static_assert(N >= 1 && N * RPL * NW == ROWS, "every wave loads alike");
     int off[N];
     __amdgpu_buffer_rsrc_t rsrc;
     __device__ __forceinline__ void init(const uint8_t* mat, int64_t ld, int64_t row0, int64_t rows, int padded,
                                          int wave) {
         const int64_t left = rows - 1 - row0;
         const int last = left < ROWS - 1 ? (int)left : ROWS - 1;
-        const int lrow = lane_id() >> 3, piece = (lane_id() & 7) ^ lrow;
 #pragma unroll
-        for (int i = 0; i < N; ++i) off[i] = min((wave * N + i) * 8 + lrow, last) * (int)ld + piece * 16;
+        for (int i = 0; i < N; ++i) off[i] = min(row(wave, i), last) * (int)ld + piece(wave, i) * 16;
         rsrc = buffer_of(mat + row0 * ld, last * (int)ld + padded);
     }
-    // load `i` of N; `over`: how far this lane's piece at k0 lies past the last one of the row
-    __device__ __forceinline__ void load(int i, uint32_t lds, int wave, int k0, int over) const {
+    __device__ __forceinline__ static int row(int wave, int i) { return (wave * N + i) * RPL + lane_id() / (K / 16); }
+    __device__ __forceinline__ static int piece(int wave, int i) {
+        return slot_of<K>(row(wave, i), lane_id() % (K / 16));
+    }
+    // load `i` of N at k0.  WHOLE: the rows reach k0 + K.
+    template <bool WHOLE>
+    __device__ __forceinline__ void load(int i, uint32_t lds, int wave, int k0, int padded) const {
+        const int over = WHOLE ? 0 : max(k0 + piece(wave, i) * 16 - (padded - 16), 0);
         load_lds16(rsrc, lds + (wave * N + i) * 1024, off[i] - over, k0);
     }
 };
 
-// Zeroes the bytes from `valid` (of 128) on in every row of an LDS tile.
-template <int ROWS, int THREADS>
+// Of four neighbouring codes, those at k and after become zeros; `at`: where the first is.
+__device__ __forceinline__ uint32_t cut_word(uint32_t word, int at, int k) {
+    const int keep = k - at;
+    return keep <= 0 ? 0u : (keep >= 4 ? word : word & ((1u << (8 * keep)) - 1u));
+}
+
+// The same for a tile of ROWS rows in LDS, `valid` of K bytes of which exist.
+template <int ROWS, int K, int THREADS>
 __device__ __forceinline__ void zero_tail(uint8_t* lds, int valid) {
-    for (int i = threadIdx.x; i < ROWS * 8; i += THREADS) {
-        const int r = i >> 3, c = i & 7;
-        uint32_t* p = reinterpret_cast<uint32_t*>(lds + r * 128 + ((c ^ (r & 7)) << 4));
+    for (int i = threadIdx.x; i < ROWS * (K / 16); i += THREADS) {
+        const int r = i / (K / 16), c = i % (K / 16);
+        u32x4* p = reinterpret_cast<u32x4*>(lds + r * K + (slot_of<K>(r, c) << 4));
+        if (c * 16 + 16 > valid) {
+            u32x4 v = *p;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const int keep = valid - (c * 16 + w * 4);  // bytes of this word that stay
-            if (keep <= 0) p[w] = 0u;
-            else if (keep < 4) p[w] &= (1u << (8 * keep)) - 1u;
+            for (int w = 0; w < 4; ++w) v[w] = cut_word(v[w], c * 16 + w * 4, valid);
+            *p = v;
         }
     }
-}
-
-// One block computes BN channels x BM tokens with WN x WM waves.
-template <class T, int BN, int BM, int WN, int WM>
-__global__ void __launch_bounds__(WN * WM * WAVE)
-k_mm_int8(Args g, T* __restrict__ c) {
-    constexpr int NW = WN * WM, THREADS = NW * WAVE;
-    constexpr int FN = BN / WN / 16, FM = BM / WM / 16;
-    constexpr int TB = BN * BK, TILE = (BN + BM) * BK;  // weights first, then tokens
-    __shared__ __align__(1024) uint8_t lds[2 * TILE];
-    const int64_t tn = (g.n + BN - 1) / BN;
-    const int64_t tile = blockIdx.x;
-    const int64_t n0 = (tile % tn) * BN, m0 = (tile / tn) * BM;
-    const int w = __builtin_amdgcn_readfirstlane(wave_id());
-    const int wn = w % WN, wm = w / WN;
-    const int l = lane_id();
-
-    const int padded = (g.k + 15) & ~15;
-    Loader<BN, NW> lb;
-    Loader<BM, NW> la;
-    lb.init(g.b, g.ldb, n0, g.n, padded, w);
-    la.init(g.a, g.lda, m0, g.m, padded, w);
-    const int piece16 = ((l & 7) ^ (l >> 3)) * 16;
-
-    i32x4 acc[FN][FM] = {};
-    // fragment addresses: row l%16, piece kk*4 + l/16
-    const int slot = ((l >> 4) ^ (l & 7)) << 4;
-    const int rb = (wn * FN * 16 + (l & 15)) * 128 + slot;
-    const int ra = (wm * FM * 16 + (l & 15)) * 128 + slot;
-
-    auto step = [&](const uint8_t* tb, const uint8_t* ta) {
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            i32x4 fb[FN], fa[FM];
-#pragma unroll
-            for (int i = 0; i < FN; ++i) fb[i] = *reinterpret_cast<const i32x4*>(tb + (rb ^ (kk * 64)) + i * 2048);
-#pragma unroll
-            for (int j = 0; j < FM; ++j) fa[j] = *reinterpret_cast<const i32x4*>(ta + (ra ^ (kk * 64)) + j * 2048);
-#pragma unroll
-            for (int i = 0; i < FN; ++i)
-#pragma unroll
-                for (int j = 0; j < FM; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[i], fa[j], acc[i][j], 0, 0, 0);
-        }
-    };
-
-    const int steps = (g.k + BK - 1) / BK;
-    const int tail = g.k - (steps - 1) * BK;
-    const uint32_t lds0 = lds_addr(lds);
-    auto fetch = [&](int buf, int t) {
-        const int over = max(t * BK + piece16 - (padded - 16), 0);
-#pragma unroll
-        for (int i = 0; i < lb.N; ++i) lb.load(i, lds0 + buf * TILE, w, t * BK, over);
-#pragma unroll
-        for (int i = 0; i < la.N; ++i) la.load(i, lds0 + buf * TILE + TB, w, t * BK, over);
-    };
-    fetch(0, 0);
-    for (int t = 0; t < steps; ++t) {
-        const int buf = t & 1;
-        lds_landed();
-        if (t + 1 < steps) fetch(buf ^ 1, t + 1);
-        if (t == steps - 1 && tail < BK) {
-            // the weights' bytes past k become zeros (integers: one side is enough)
-            zero_tail<BN, THREADS>(lds + buf * TILE, tail);
-            __syncthreads();
-        }
-        step(lds + buf * TILE, lds + buf * TILE + TB);
-    }
-
-#pragma unroll
-    for (int j = 0; j < FM; ++j) {
-        const int64_t row = m0 + (wm * FM + j) * 16 + (l & 15);
-        if (row < g.m) {
-            const float sa = g.sa[row];
-#pragma unroll
-            for (int i = 0; i < FN; ++i) {
-                const int64_t col = n0 + (wn * FN + i) * 16 + 4 * (l >> 4);
-                const int64_t left = g.n - col;
-                if (left > 0) {
-                    float v[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = scaled(acc[i][j][e], sa, e < left ? g.sb[col + e] : 0.0f);
-                    store4(c + row * g.ldc + col, left < 4 ? (int)left : 4, v, g.wide);
-                }
-            }
-        }
-    }
-}
-
-template <class T, int BN, int BM, int WN, int WM>
-hipError_t launch_tile(const Args& g, T* c, hipStream_t stream) {
-    const int64_t tiles = ((g.n + BN - 1) / BN) * ((g.m + BM - 1) / BM);
-    hipLaunchKernelGGL((k_mm_int8<T, BN, BM, WN, WM>), dim3((unsigned)tiles), dim3(WN * WM * WAVE), 0, stream, g, c);
-    return hipGetLastError();
 }
 
 // ------------------------------------------------------- pipelined tiles
 // One block computes BN channels x BM tokens with WN x WM waves, in stages of
-// 128 bytes of k, two of them in LDS.  A wave reads its fragments ahead of
+// K bytes of k, two of them in LDS.  A wave reads its fragments ahead of
 // their use, into the next stage too; the wait for that stage, and the only
 // barrier, stand where the last fragments of this one have been read, and the
 // fragments already in registers keep the matrix cores busy across it.  The
 // loads of the stage after next follow at once, over the one just left, and
 // have a whole stage's time to arrive.
-//
-// 128 bytes of k and not 64: what bounds these kernels is the rate at which a
-// compute unit loads, and that depends on how much of a row a load takes.
-// Measured, from L2, 256 rows 8 KiB apart, all compute units: 16 rows x 64
-// bytes a load 50 bytes/ns a compute unit, 8 x 128 72, 4 x 256 134.
-template <class T, int BN, int BM, int WN, int WM>
+template <class T, int BN, int BM, int WN, int WM, int K>
 __global__ void __launch_bounds__(WN * WM * WAVE)
 k_mm_int8_pipe(Args g, T* __restrict__ c) {
     constexpr int NW = WN * WM, THREADS = NW * WAVE;
     constexpr int FN = BN / WN / 16, FM = BM / WM / 16;
     constexpr int AHEAD = FN >= 8 ? 3 : 2;                 // weight fragments read ahead (of a ring of 4)
-    constexpr int STEPS = 2 * FN, TURN = STEPS - FN / 2;   // a step: one weight fragment; the barrier's step
-    constexpr int TB = BN * BK, STAGE = (BN + BM) * BK;    // weights first, then tokens
-    constexpr int LB = BN / 8 / NW, LOADS = (BN + BM) / 8 / NW;
-    static_assert(FN % 4 == 0 && FM >= 1 && (BN / 8) % NW == 0 && (BM / 8) % NW == 0, "tile shape");
-    static_assert(STEPS - 1 - AHEAD <= TURN && STEPS - AHEAD >= TURN, "a stage's last read comes before the barrier, the next one's first after it");
+    constexpr int KK = K / 64, STEPS = KK * FN, TURN = STEPS - FN / 2;   // a step: one weight fragment; the barrier's step
+    constexpr int TB = BN * K, STAGE = (BN + BM) * K;      // weights first, then tokens
+    // a stage's last read comes before the barrier, the next one's first after it
+    static_assert(FN % 4 == 0 && FM >= 1 && STEPS - 1 - AHEAD <= TURN && STEPS - AHEAD >= TURN, "tile shape");
     __shared__ __align__(1024) uint8_t lds[2 * STAGE];
 
     const uint32_t tn = (uint32_t)((g.n + BN - 1) / BN), tm = (uint32_t)((g.m + BM - 1) / BM);
@@ -222,39 +145,39 @@ k_mm_int8_pipe(Args g, T* __restrict__ c) {
     const int wn = w % WN, wm = w / WN;
     const int l = lane_id();
     const int padded = (g.k + 15) & ~15;
-    Loader<BN, NW> lb;
-    Loader<BM, NW> la;
+    Loader<BN, K, NW> lb;
+    Loader<BM, K, NW> la;
+    constexpr int LOADS = lb.N + la.N;
     lb.init(g.b, g.ldb, n0, g.n, padded, w);
     la.init(g.a, g.lda, m0, g.m, padded, w);
-    const int piece16 = ((l & 7) ^ (l >> 3)) * 16;
 
-    const int stages = (g.k + BK - 1) / BK;
-    const int whole = g.k / BK;  // a stage from here on (one at most) holds bytes past k
+    const int stages = (g.k + K - 1) / K;
+    const int whole = g.k / K;  // a stage from here on (one at most) holds bytes past k
     const uint32_t lds0 = lds_addr(lds);
-    auto over_of = [&](int s) { return max(s * BK + piece16 - (padded - 16), 0); };
-    auto fetch_part = [&](int part, int buf, int s, int over) {  // one of LOADS
-        if (part < LB) lb.load(part, lds0 + buf * STAGE, w, s * BK, over);
-        else la.load(part - LB, lds0 + buf * STAGE + TB, w, s * BK, over);
+    auto fetch_part = [&](auto fast, int part, int buf, int s) {  // one of LOADS
+        constexpr bool FAST = decltype(fast)::value;
+        if (part < lb.N) lb.template load<FAST>(part, lds0 + buf * STAGE, w, s * K, padded);
+        else la.template load<FAST>(part - lb.N, lds0 + buf * STAGE + TB, w, s * K, padded);
     };
     auto fetch = [&](int s) {
 #pragma unroll
-        for (int part = 0; part < LOADS; ++part) fetch_part(part, s & 1, s, over_of(s));
+        for (int part = 0; part < LOADS; ++part) fetch_part(std::false_type{}, part, s & 1, s);
     };
     auto cut = [&](int s) {
         if (s >= whole) {  // the weights' bytes past k become zeros (integers: one side is enough)
-            zero_tail<BN, THREADS>(lds + (s & 1) * STAGE, g.k - s * BK);
+            zero_tail<BN, K, THREADS>(lds + (s & 1) * STAGE, g.k - s * K);
             __syncthreads();
         }
     };
 
-    // fragment addresses: row l % 16, piece kk * 4 + l / 16
-    const int frag = (l & 15) * BK + (((l >> 4) ^ (l & 7)) << 4);
-    const int rb = wn * FN * 2048 + frag, ra = TB + wm * FM * 2048 + frag;
+    // fragments: row l % 16, piece kk * 4 + l / 16 (an xor of kk * 64 in the address)
+    const int frag = (l & 15) * K + (slot_of<K>(l & 15, l >> 4) << 4);
+    const int rb = wn * FN * 16 * K + frag, ra = TB + wm * FM * 16 * K + frag;
     auto read_b = [&](int buf, int q) {
-        return *reinterpret_cast<const i32x4*>(lds + buf * STAGE + (rb ^ (q / FN * 64)) + q % FN * 2048);
+        return *reinterpret_cast<const i32x4*>(lds + buf * STAGE + (rb ^ (q / FN * 64)) + q % FN * (16 * K));
     };
     auto read_a = [&](int buf, int kk, int j) {
-        return *reinterpret_cast<const i32x4*>(lds + buf * STAGE + (ra ^ (kk * 64)) + j * 2048);
+        return *reinterpret_cast<const i32x4*>(lds + buf * STAGE + (ra ^ (kk * 64)) + j * (16 * K));
     };
 
     i32x4 acc[FN][FM] = {};
@@ -275,16 +198,16 @@ k_mm_int8_pipe(Args g, T* __restrict__ c) {
                 constexpr int H = FN / 2;  // this step's share of the token fragments and of the loads
 #pragma unroll
                 for (int e = (i - H) * FM / H; e < (i - H + 1) * FM / H; ++e)
-                    fa[kk ^ 1][e] = kk == 0 ? read_a(buf, 1, e) : read_a(buf ^ 1, 0, e);
-                if (kk == 1 && (FAST || s + 2 < stages)) {
+                    fa[(kk + 1) & 1][e] = kk + 1 < KK ? read_a(buf, kk + 1, e) : read_a(buf ^ 1, 0, e);
+                if (kk + 1 == KK && (FAST || s + 2 < stages)) {
 #pragma unroll
                     for (int d = (i - H) * LOADS / H; d < (i - H + 1) * LOADS / H; ++d)
-                        fetch_part(d, buf, s + 2, FAST ? 0 : over_of(s + 2));
+                        fetch_part(fast, d, buf, s + 2);
                 }
             }
 #pragma unroll
             for (int j = 0; j < FM; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[q % 4], fa[kk][j], acc[i][j], 0, 0, 0);
+                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[q % 4], fa[kk & 1][j], acc[i][j], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);  // keeps the reads where they stand, ahead of their use
         }
     };
@@ -336,98 +259,93 @@ k_mm_int8_pipe(Args g, T* __restrict__ c) {
     }
 }
 
-template <class T, int BN, int BM, int WN, int WM>
+template <class T, int BN, int BM, int WN, int WM, int K>
 hipError_t launch_pipe(const Args& g, T* c, hipStream_t stream) {
     const int64_t tiles = ((g.n + BN - 1) / BN) * ((g.m + BM - 1) / BM);
-    hipLaunchKernelGGL((k_mm_int8_pipe<T, BN, BM, WN, WM>), dim3((unsigned)tiles), dim3(WN * WM * WAVE), 0, stream, g,
+    hipLaunchKernelGGL((k_mm_int8_pipe<T, BN, BM, WN, WM, K>), dim3((unsigned)tiles), dim3(WN * WM * WAVE), 0, stream, g,
                        c);
     return hipGetLastError();
 }
 
 // ------------------------------------------------------------- few tokens
 // One block: NT * 16 channels x MT * 16 tokens, k split over WS waves in
-// chunks of 128 bytes, joined through LDS.  Bound by the weights' bytes: they
-// go from memory to the matrix instruction without LDS, two chunks of every
-// row in flight a wave; the tokens come from L2.  The four lanes that hold
-// a row take 32 bytes of the chunk each, half of it per instruction: the
-// order of k inside a chunk is the same for both operands, and any will do.
-template <class T, int NT, int MT, int WS>
+// slabs of 256 bytes, joined through LDS.  A wave loads the rows of its slab
+// into a part of LDS of its own (no barrier until the waves join), up to NB
+// slabs at a time, as 4 rows x 256 bytes a load; that pattern is what makes
+// this fast: with the fragments loaded straight into registers, 16 rows x 64
+// bytes a load, 61 tokens x 4096 x 4096 took 13.5 us instead of 8.5.
+template <class T, int NT, int MT, int WS, int NB>
 __global__ void __launch_bounds__(WS * WAVE)
 k_mm_int8_few(Args g, T* __restrict__ c) {
-    __shared__ i32x4 part[WS * NT * MT * WAVE];
-    const int l = lane_id(), w = wave_id();
+    constexpr int K = 256, ROWS = (NT + MT) * 16, SLAB = ROWS * K;
+    constexpr int OWN = NB * SLAB > NT * MT * 1024 ? NB * SLAB : NT * MT * 1024;  // a wave's LDS: slabs, then sums
+    __shared__ __align__(1024) uint8_t lds[WS * OWN];
+    const int l = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id());
     const int64_t n0 = (int64_t)blockIdx.x * (NT * 16), m0 = (int64_t)blockIdx.y * (MT * 16);
     const int padded = (g.k + 15) & ~15;
-    const int chunks = (g.k + BK - 1) / BK;
-    const uint8_t* pb[NT];
-    const uint8_t* pa[MT];
+    Loader<NT * 16, K, 1> lb;
+    Loader<MT * 16, K, 1> la;
+    constexpr int LOADS = lb.N + la.N;
+    lb.init(g.b, g.ldb, n0, g.n, padded, 0);
+    la.init(g.a, g.lda, m0, g.m, padded, 0);
+    uint8_t* own = lds + w * OWN;
+    auto fetch = [&](int slab, int buf) {
+        const uint32_t at = lds_addr(own) + buf * SLAB;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int64_t r = n0 + i * 16 + (l & 15);
-        pb[i] = g.b + (r < g.n ? r : g.n - 1) * g.ldb;
-    }
+        for (int i = 0; i < lb.N; ++i) lb.template load<false>(i, at, 0, slab * K, padded);
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-        const int64_t r = m0 + j * 16 + (l & 15);
-        pa[j] = g.a + (r < g.m ? r : g.m - 1) * g.lda;
-    }
+        for (int i = 0; i < la.N; ++i) la.template load<false>(i, at + NT * 16 * K, 0, slab * K, padded);
+    };
+
     i32x4 acc[NT][MT] = {};
-    struct Chunk {
-        i32x4 b[NT][2], a[MT][2];
-    };
-    auto get = [&](Chunk& f, int ch) {
+    const int slabs = (g.k + K - 1) / K;
+    const int mine = (slabs - w + WS - 1) / WS;  // slabs w, w + WS, ...
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int at = ch * BK + h * 64 + (l >> 4) * 16;
-            const int in = min(at, padded - 16);  // pieces past the row repeat its last one
+    for (int b = 0; b < NB; ++b)
+        if (b < mine) fetch(w + b * WS, b);
+    for (int it = 0; it < mine; ++it) {
+        const int slab = w + it * WS, buf = NB == 1 ? 0 : it % NB;
+        if (NB > 1 && it + NB <= mine) asm volatile("s_waitcnt vmcnt(%0)" : : "n"((NB - 1) * LOADS) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+        const uint8_t* at = own + buf * SLAB + (l & 15) * K;
 #pragma unroll
-            for (int i = 0; i < NT; ++i) f.b[i][h] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(pb[i] + in));
+        for (int kk = 0; kk < K / 64; ++kk) {
+            const int slot = slot_of<K>(l & 15, kk * 4 + (l >> 4)) << 4;
+            i32x4 fb[NT], fa[MT];
 #pragma unroll
-            for (int j = 0; j < MT; ++j) f.a[j][h] = *reinterpret_cast<const i32x4*>(pa[j] + in);
-        }
-    };
-    auto use = [&](Chunk& f, int ch) {
-        if ((ch + 1) * BK > g.k) {  // the weights' bytes past k become zeros
+            for (int i = 0; i < NT; ++i) fb[i] = *reinterpret_cast<const i32x4*>(at + i * (16 * K) + slot);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int j = 0; j < MT; ++j) fa[j] = *reinterpret_cast<const i32x4*>(at + (NT + j) * (16 * K) + slot);
+            if ((slab + 1) * K > g.k) {  // the weights' bytes past k become zeros
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int keep = g.k - (ch * BK + h * 64 + (l >> 4) * 16 + e * 4);
-                    const uint32_t mask = keep <= 0 ? 0u : (keep >= 4 ? ~0u : (1u << (8 * keep)) - 1u);
+                for (int i = 0; i < NT; ++i)
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) f.b[i][h][e] &= (int)mask;
-                }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
+                    for (int e = 0; e < 4; ++e)
+                        fb[i][e] = (int)cut_word(fb[i][e], slab * K + kk * 64 + (l >> 4) * 16 + e * 4, g.k);
+            }
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int j = 0; j < MT; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.b[i][h], f.a[j][h], acc[i][j], 0, 0, 0);
-    };
-    int ch = w;
-    for (; ch + WS < chunks; ch += 2 * WS) {
-        Chunk f0, f1;
-        get(f0, ch);
-        get(f1, ch + WS);
-        use(f0, ch);
-        use(f1, ch + WS);
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[i], fa[j], acc[i][j], 0, 0, 0);
+        }
+        if (it + NB < mine) {
+            asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");  // this slab has been read
+            fetch(slab + NB * WS, buf);
+        }
     }
-    if (ch < chunks) {
-        Chunk f;
-        get(f, ch);
-        use(f, ch);
-    }
+
+    // all of a wave's loads have landed and been read; its part of LDS takes its sums
+    i32x4* sums = reinterpret_cast<i32x4*>(own);
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int j = 0; j < MT; ++j) part[(w * NT * MT + i * MT + j) * WAVE + l] = acc[i][j];
+        for (int j = 0; j < MT; ++j) sums[(i * MT + j) * WAVE + l] = acc[i][j];
     __syncthreads();
     for (int f = w; f < NT * MT; f += WS) {
-        i32x4 sum = part[f * WAVE + l];
+        i32x4 sum = {};
 #pragma unroll
-        for (int s = 1; s < WS; ++s) sum += part[(s * NT * MT + f) * WAVE + l];
+        for (int s = 0; s < WS; ++s) sum += *reinterpret_cast<const i32x4*>(lds + s * OWN + (f * WAVE + l) * 16);
         const int64_t row = m0 + (f % MT) * 16 + (l & 15);
         const int64_t col = n0 + (f / MT) * 16 + 4 * (l >> 4);
         const int64_t left = g.n - col;
@@ -441,22 +359,60 @@ k_mm_int8_few(Args g, T* __restrict__ c) {
     }
 }
 
-template <class T, int NT, int MT, int WS>
+template <class T, int NT, int MT, int WS, int NB>
 hipError_t launch_few(const Args& g, T* c, hipStream_t stream) {
     const dim3 grid((unsigned)((g.n + NT * 16 - 1) / (NT * 16)), (unsigned)((g.m + MT * 16 - 1) / (MT * 16)));
-    hipLaunchKernelGGL((k_mm_int8_few<T, NT, MT, WS>), grid, dim3(WS * WAVE), 0, stream, g, c);
+    hipLaunchKernelGGL((k_mm_int8_few<T, NT, MT, WS, NB>), grid, dim3(WS * WAVE), 0, stream, g, c);
     return hipGetLastError();
+}
+
+// Which tile: the one whose rounds of blocks over the 256 compute units take
+// the least time.  `round_us` is the measured time of one full round at k =
+// 4096 without the launch itself (2 us); all grow with k alike.  Against the
+// next best shape, whole calls, weights from HBM, at n = k = 4096:
+//   m    1: 16 x 16 5.5 us (32 x 16 8.7)     m  16 (n 16384): 32 x 16 16.1 (16 x 16 18.5)
+//   m   32: 16 x 32 7.6 (32 x 32 9.0)        m  61: 32 x 32 8.5 (16 x 64 9.5)
+//   m  128: 32 x 64 9.7 (32 x 32 13.3)       m 256: 64 x 64 14.4 (32 x 64 15.5)
+//   m  512: 128 x 64 19.5 (128 x 128 24.7)   m 1024: 128 x 128, 256 bytes of k 25.0 (128 bytes 30.1)
+//   m 2048: 128 x 128, 128 bytes of k 45.3 (256 x 256 53.5)  m 4096: 256 x 256 58.7 (128 x 128 79.7)
+struct Shape {
+    int bn, bm, slots;  // channels, tokens, blocks at work at one time
+    float round_us;
+};
+constexpr Shape kShapes[] = {
+    {16, 16, 256, 4.0f},  {32, 16, 256, 6.8f},   {16, 32, 256, 5.4f},   {32, 32, 256, 6.5f},    {32, 64, 256, 7.2f},
+    {64, 64, 256, 12.0f}, {128, 64, 256, 17.6f}, {128, 128, 256, 22.8f}, {128, 128, 512, 43.0f}, {256, 256, 256, 51.0f},
+};
+
+int shape_of(int64_t m, int64_t n) {
+    int best = 0;
+    double least = 0;
+    for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); ++i) {
+        const Shape& s = kShapes[i];
+        const int64_t blocks = ((n + s.bn - 1) / s.bn) * ((m + s.bm - 1) / s.bm);
+        const double us = (double)((blocks + s.slots - 1) / s.slots) * s.round_us;
+        if (i == 0 || us < least) {
+            best = i;
+            least = us;
+        }
+    }
+    return best;
 }
 
 template <class T>
 hipError_t launch(const Args& g, T* c, hipStream_t stream) {
-    if (g.m <= 16) return launch_few<T, 1, 1, 16>(g, c, stream);
-    if (g.m <= 32) return launch_few<T, 1, 2, 8>(g, c, stream);
-    if (g.m <= 64) return launch_few<T, 2, 4, 8>(g, c, stream);
-    const auto tiles = [&](int64_t bn, int64_t bm) { return ((g.n + bn - 1) / bn) * ((g.m + bm - 1) / bm); };
-    if (tiles(256, 256) >= 192) return launch_pipe<T, 256, 256, 2, 4>(g, c, stream);
-    if (tiles(128, 128) >= 192) return launch_pipe<T, 128, 128, 2, 2>(g, c, stream);
-    return launch_tile<T, 64, 64, 2, 2>(g, c, stream);
+    switch (shape_of(g.m, g.n)) {
+        case 0: return launch_few<T, 1, 1, 8, 2>(g, c, stream);
+        case 1: return launch_few<T, 2, 1, 6, 2>(g, c, stream);
+        case 2: return launch_few<T, 1, 2, 8, 1>(g, c, stream);
+        case 3: return launch_few<T, 2, 2, 8, 1>(g, c, stream);
+        case 4: return launch_few<T, 2, 4, 6, 1>(g, c, stream);
+        case 5: return launch_few<T, 4, 4, 4, 1>(g, c, stream);
+        case 6: return launch_pipe<T, 128, 64, 2, 2, 256>(g, c, stream);
+        case 7: return launch_pipe<T, 128, 128, 2, 2, 256>(g, c, stream);
+        case 8: return launch_pipe<T, 128, 128, 2, 2, 128>(g, c, stream);
+        default: return launch_pipe<T, 256, 256, 2, 4, 128>(g, c, stream);
+    }
 }
 
 }  // namespace

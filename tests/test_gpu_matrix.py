@@ -187,7 +187,9 @@ def test_matmul_large_tiles(qc, m, n, k, dtype):
     assert torch.equal(c.get(), want)
 
 
-@pytest.mark.parametrize("m,n,k", [(3700, 3400, 1500), (2000, 1900, 1024), (1500, 2100, 641), (3584, 3840, 448)])
+@pytest.mark.parametrize("m,n,k", [(3700, 3400, 1500), (2000, 1900, 1024), (1500, 2100, 641), (3584, 3840, 448),
+                                   (9, 5000, 1333), (30, 4001, 2700), (60, 3900, 1100), (120, 4002, 2900),
+                                   (250, 3907, 1300), (500, 4000, 1601), (1000, 4003, 1700), (2000, 4000, 1111)])
 def test_matmul_large_tiles_long_k(qc, m, n, k):
     """The same over enough k for the steady state of the pipeline; codes small
     enough that every sum is below 2^24 and fp32 on the host exact."""
