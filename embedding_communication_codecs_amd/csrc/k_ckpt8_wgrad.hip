@@ -113,11 +113,12 @@ __device__ __forceinline__ void store_dw(const Args& g, f32x4 (&acc)[FD][FN], in
     }
 }
 
-// One block: BN output channels (columns of dY) x BD input channels (columns
-// of X), WN x WD waves, TK tokens a step.  P: pieces of dY (1: bf16, 3:
-// fp32).  DMA: dY's rows are 16-byte aligned and n a multiple of 8: they are
-// loaded straight into LDS (P = 1 only).
-template <int P, bool DMA, int BN, int BD, int WN, int WD, int TK>
+// ------------------------------------------------------------------- simple
+// Gradients of very few channels (n below 8 in bf16, below 4 in fp32).  One
+// block: BN output channels (columns of dY) x BD input channels (columns of
+// X), WN x WD waves, TK tokens a step, two steps in LDS; both operands pass
+// through registers.  P: pieces of dY (1: bf16, 3: fp32).
+template <int P, int BN, int BD, int WN, int WD, int TK>
 __global__ void __launch_bounds__(WN * WD * WAVE)
 k_ckpt8_wgrad(Args g) {
     constexpr int NW = WN * WD, THREADS = NW * WAVE;
@@ -174,28 +175,8 @@ k_ckpt8_wgrad(Args g) {
     };
 
     // ---- dY
-    const uint32_t lds0 = lds_addr(lds);
-    constexpr int YN = TK * YB / 1024 / NW;  // loads a wave (DMA)
-    constexpr int TPL = 1024 / YB;           // tokens a load
-    int yoff[YN > 0 ? YN : 1];
-    auto y_offsets = [&](int last) {
-#pragma unroll
-        for (int i = 0; i < YN; ++i) {
-            const int t = (w * YN + i) * TPL + l / (YB / 16);
-            const int c = (l % (YB / 16)) ^ (2 * (t & 7));
-            const int64_t col = min(n0 + c * 8, g.n - 8);  // pieces past n repeat its last one
-            yoff[i] = (int)(min(t, last) * g.ldy + (col - n0)) * 2;
-        }
-    };
-    auto y_dma = [&](int buf, int64_t t0) {
-        const int64_t left = t_end - t0;
-        if (left < TK) y_offsets((int)left - 1);  // tokens past the end repeat the last one
-        const auto rsrc = buffer_of(static_cast<const uint8_t*>(g.dy) + (t0 * g.ldy + n0) * 2, -1);
-#pragma unroll
-        for (int i = 0; i < YN; ++i) load_lds16(rsrc, lds0 + buf * TILE + (w * YN + i) * 1024, yoff[i], 0);
-    };
     constexpr int YC = TK * BN / 8 / THREADS;  // pieces of 8 values a thread stages
-    float yv[DMA ? 1 : YC][8];
+    float yv[YC][8];
     auto y_get = [&](int64_t t0) {
 #pragma unroll
         for (int i = 0; i < YC; ++i) {
@@ -262,36 +243,22 @@ k_ckpt8_wgrad(Args g) {
     };
 
     if (t_first < t_end) {
-        if constexpr (DMA) {
-            y_offsets(TK - 1);
-            y_dma(0, t_first);
-        } else {
-            y_get(t_first);
-            y_put(lds);
-        }
+        y_get(t_first);
+        y_put(lds);
         x_get(t_first);
         x_put(lds + P * YT);
         int buf = 0;
         for (int64_t t0 = t_first; t0 < t_end; t0 += TK, buf ^= 1) {
-            lds_landed();
+            __syncthreads();
             const bool more = t0 + TK < t_end;
             if (more) {
                 x_get(t0 + TK);
-                if constexpr (DMA) y_dma(buf ^ 1, t0 + TK);
-                else y_get(t0 + TK);
-            }
-            if constexpr (DMA) {
-                if (t_end - t0 < TK) {  // tokens past the end: zeros (X's are zeros too; an infinity times zero is not)
-                    const int first = (int)(t_end - t0) * YB;
-                    for (int at = first + threadIdx.x * 16; at < YT; at += THREADS * 16)
-                        *reinterpret_cast<u32x4*>(lds + buf * TILE + at) = u32x4{0, 0, 0, 0};
-                    __syncthreads();
-                }
+                y_get(t0 + TK);
             }
             compute(lds + buf * TILE);
             if (more) {
                 x_put(lds + (buf ^ 1) * TILE + P * YT);
-                if constexpr (!DMA) y_put(lds + (buf ^ 1) * TILE);
+                y_put(lds + (buf ^ 1) * TILE);
             }
         }
     }
@@ -299,9 +266,36 @@ k_ckpt8_wgrad(Args g) {
     store_dw<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16);
 }
 
+// The same of four neighbours, packed: word 0 holds values 0 and 1.
+__device__ __forceinline__ void pieces4(f32x4 x, u32x2 (&q)[3]) {
+    uint32_t b[4], most = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        b[e] = __float_as_uint(x[e]);
+        most = umax(most, b[e] & 0x7FFFFFFFu);
+    }
+    if (__builtin_expect(__any(most >= kInfBits), 0)) {
+        uint32_t p[4][3];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pieces(x[e], p[e]);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) q[i] = u32x2{p[0][i] | (p[1][i] << 16), p[2][i] | (p[3][i] << 16)};
+        return;
+    }
+    auto upper = [](uint32_t lo, uint32_t hi) { return __builtin_amdgcn_perm(hi, lo, 0x07060302u); };
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        q[i] = u32x2{upper(b[0], b[1]), upper(b[2], b[3])};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[e] = x[e] - __uint_as_float(b[e] & 0xFFFF0000u);
+            b[e] = __float_as_uint(x[e]);
+        }
+    }
+}
+
 // --------------------------------------------------------------- pipelined
-// bf16 gradients whose rows are 16-byte aligned, n a multiple of 8.  One block
-// computes BN output x BD input channels with WN x WD waves, in stages of 32
+// bf16 gradients, n at least 8.  One block computes BN output x BD input channels with WN x WD waves, in stages of 32
 // tokens.  Everything is loaded straight into LDS, two stages before its use:
 // dY as it is, X as codes and exponent words.  Each lane's 16 codes and their
 // exponents land in a place of its own, so the lane converts them to bf16 as
@@ -341,21 +335,26 @@ k_ckpt8_wgrad_pipe(Args g) {
     const int whole = (int)(tokens / ST);
     const uint32_t lds0 = lds_addr(lds);
 
-    // ---- loads.  Tokens past the end repeat the last one and are zeroed in
-    // LDS; pieces past a row's end repeat its last piece (their sums are not
-    // stored).
-    const uint8_t* ybase = static_cast<const uint8_t*>(g.dy) + (t_first * g.ldy + n0) * 2;
+    // ---- loads, of 16 bytes a lane at any alignment of dY's rows.  Tokens past
+    // the end repeat the last one and are zeroed in LDS; pieces past a row's
+    // end repeat its last piece (their sums are not stored).  A row's last
+    // piece may reach past n: into the next row, whose values fall on columns
+    // that are not stored.  The matrix's last row has no next one: there the
+    // piece is taken from n - 8, and cut() puts its values in their places.
+    const uint8_t* ybase = static_cast<const uint8_t*>(g.dy) + t_first * g.ldy * 2;  // column 0: offsets stay positive
     const uint8_t* xbase = g.codes + t_first * g.pitch;
     const uint8_t* ebase = g.exps + t_first * g.epitch;
-    int ytok[YN], ycol[YN], yoff[YN];
+    const int64_t last_piece = (g.n - 1) / 8 * 8;
+    const bool patch = t_first + tokens == g.rows && g.n % 8 != 0;
+    const int first_col = (int)n0, last_col = (int)last_piece;
+    auto ytok = [&](int i) { return (w * YN + i) * (1024 / YB) + l / (YB / 16); };
+    auto ycol = [&](int i) {
+        const int c = (l % (YB / 16)) ^ (2 * (ytok(i) & 7));
+        return min(first_col + c * 8, last_col);
+    };
+    int yoff[YN];
 #pragma unroll
-    for (int i = 0; i < YN; ++i) {
-        const int t = (w * YN + i) * (1024 / YB) + l / (YB / 16);
-        const int c = (l % (YB / 16)) ^ (2 * (t & 7));
-        ytok[i] = t;
-        ycol[i] = (int)(min(n0 + c * 8, g.n - 8) - n0) * 2;
-        yoff[i] = t * (int)g.ldy * 2 + ycol[i];
-    }
+    for (int i = 0; i < YN; ++i) yoff[i] = (ytok(i) * (int)g.ldy + ycol(i)) * 2;
     const int xt = w * TPW + l / (BD / 16), xq = l % (BD / 16);  // this lane's token of a stage, and 16 codes of it
     const int xcol = (int)min(d0 + xq * 16, g.pitch - 16);
     const int ecol = (int)min((d0 + xq * 16) / 128 * 4, g.epitch - 4);
@@ -363,9 +362,10 @@ k_ckpt8_wgrad_pipe(Args g) {
         int64_t t0 = (int64_t)s * ST;
         int off = yoff[i];
         if (!decltype(fast)::value) {
-            const int64_t t = min(t0 + ytok[i], tokens - 1);
             t0 = min(t0, tokens - 1);
-            off = (int)(t - t0) * (int)g.ldy * 2 + ycol[i];
+            const int last = (int)min(tokens - 1 - t0, (int64_t)ST), t = min(ytok(i), last);
+            const int col = ycol(i);
+            off = (t * (int)g.ldy + (patch && t == last && col == last_col ? (int)g.n - 8 : col)) * 2;
         }
         load_lds16(buffer_of(ybase + t0 * g.ldy * 2, -1), lds0 + (s & 3) * YT + (w * YN + i) * 1024, off, 0);
     };
@@ -373,9 +373,8 @@ k_ckpt8_wgrad_pipe(Args g) {
         int64_t t0 = (int64_t)s * ST;
         int t = xt;
         if (!decltype(fast)::value) {
-            const int64_t at = min(t0 + xt, tokens - 1);
             t0 = min(t0, tokens - 1);
-            t = (int)(at - t0);
+            t = min(xt, (int)min(tokens - 1 - t0, (int64_t)ST));
         }
         const uint32_t at = lds0 + RAT + ((s & 3) * NW + w) * RAW;
         if (part == 0) load_lds16(buffer_of(xbase + t0 * g.pitch, -1), at, t * (int)g.pitch + xcol, 0);
@@ -405,7 +404,7 @@ k_ckpt8_wgrad_pipe(Args g) {
     auto x_put = [&](auto fast, int s) {
         float step = ckpt_step((eword >> (8 * ((xq >> 1) & 3))) & 0xFFu);
         u32x4 q = odd ? u32x4{raw.z, raw.w, raw.x, raw.y} : raw;
-        if (!decltype(fast)::value && (int64_t)s * ST + xt >= tokens) {
+        if (!decltype(fast)::value && xt >= (int)min(tokens - (int64_t)s * ST, (int64_t)ST)) {
             step = 0.0f;
             q = u32x4{0, 0, 0, 0};
         }
@@ -418,30 +417,36 @@ k_ckpt8_wgrad_pipe(Args g) {
         }
     };
     auto cut = [&](int s) {
-        if (s >= whole && s < stages) {  // tokens past the end: zeros (X's are too, but an infinity times zero is not)
-            const int first = (int)max(tokens - (int64_t)s * ST, (int64_t)0) * YB;
-            for (int at = first + threadIdx.x * 16; at < YT; at += THREADS * 16)
-                *reinterpret_cast<u32x4*>(lds + (s & 3) * YT + at) = u32x4{0, 0, 0, 0};
-            __syncthreads();
+        const bool last = patch && s == (int)((tokens - 1) / ST);
+        if (!last && (s < whole || s >= stages)) return;
+        // tokens past the end: zeros (X's are too, but an infinity times zero is not)
+        uint8_t* at = lds + (s & 3) * YT;
+        for (int i = (int)max(min(tokens - (int64_t)s * ST, (int64_t)ST), (int64_t)0) * YB + threadIdx.x * 16; i < YT;
+             i += THREADS * 16)
+            *reinterpret_cast<u32x4*>(at + i) = u32x4{0, 0, 0, 0};
+        if (last && threadIdx.x < 8 && last_piece >= n0 && last_piece < n0 + BN) {
+            const int64_t col = last_piece + threadIdx.x;
+            const uint16_t v = col < g.n ? static_cast<const uint16_t*>(g.dy)[(g.rows - 1) * g.ldy + col] : 0;
+            *reinterpret_cast<uint16_t*>(at + place((int)((tokens - 1) % ST), (int)(last_piece - n0) / 8, YB) +
+                                         2 * threadIdx.x) = v;
         }
+        __syncthreads();
     };
 
     // ---- fragments: lane l reads 8 bytes of token r * 16 + l / 4, and gets
     // four tokens of channel l % 16
     auto frag_at = [&](int f, int row_bytes) { return place(l >> 2, f * 2 + ((l & 3) >> 1), row_bytes) + 8 * (l & 1); };
-    int yf[FN], xf[FD];
-#pragma unroll
-    for (int j = 0; j < FN; ++j) yf[j] = frag_at(wn * FN + j, YB);
-#pragma unroll
-    for (int i = 0; i < FD; ++i) xf[i] = XAT + frag_at(wd * FD + i, XB);
+    // FN and FD are powers of two up to 8: the other fragments are an xor away
+    const int yf = frag_at(wn * FN, YB), xf = frag_at(wd * FD, XB);
+    static_assert((FN & (FN - 1)) == 0 && FN <= 8 && (FD & (FD - 1)) == 0 && FD <= 8, "fragments");
     auto frag = [&](int at, int row_bytes) {
         typedef short s16x8 __attribute__((ext_vector_type(8)));
         const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(lds + at));
         const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(lds + at + 16 * row_bytes));
         return __builtin_bit_cast(bf16x8, s16x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w});
     };
-    auto read_y = [&](int buf, int j) { return frag(buf * YT + yf[j], YB); };
-    auto read_x = [&](int buf, int i) { return frag((buf & 1) * XT + xf[i], XB); };
+    auto read_y = [&](int buf, int j) { return frag(buf * YT + (yf ^ (j << 5)), YB); };
+    auto read_x = [&](int buf, int i) { return frag(XAT + (buf & 1) * XT + (xf ^ (i << 5)), XB); };
 
     f32x4 acc[FD][FN] = {};
     bf16x8 fy[4], fx[2][FD];
@@ -516,6 +521,167 @@ k_ckpt8_wgrad_pipe(Args g) {
     store_dw<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16);
 }
 
+// The same for fp32 gradients, n at least 4: each wave's part of dY lands in
+// a place of its own too, and is taken apart into its three bf16 pieces, a
+// tile each, when X is converted.  The three products of a step share X's
+// fragments.  A batch holds dY and X of one stage.
+template <int BN, int BD, int WN, int WD>
+__global__ void __launch_bounds__(WN * WD * WAVE)
+k_ckpt8_wgrad_pipe_f32(Args g) {
+    constexpr int NW = WN * WD;
+    constexpr int FN = BN / WN / 16, FD = BD / WD / 16;
+    constexpr int YB = BN * 2, XB = BD * 2, YT = ST * YB, XT = ST * XB;
+    constexpr int YN = ST * BN * 4 / 1024 / NW;    // loads of dY a wave and stage
+    constexpr int XL = ST * BD / 16 / NW;          // lanes of a wave that load 16 codes of X
+    constexpr int TPW = ST / NW;                   // tokens of X a wave converts
+    constexpr int LOADS = YN + 2;
+    constexpr int RAW = YN * 1024 + XL * 16 + 256;  // a wave's loads of a stage
+    static_assert(BN == 128 && BD == 128 && XL == 32 && TPW * NW == ST && YN >= 1, "tile shape");
+    constexpr int BUF = 3 * YT + XT, RAT = 2 * BUF;  // LDS: two buffers of tiles, four raw stages
+    __shared__ __align__(1024) uint8_t lds[RAT + 4 * NW * RAW];
+
+    const uint32_t tn = (uint32_t)((g.n + BN - 1) / BN), td = (uint32_t)((g.dim + BD - 1) / BD);
+    const Tile2 tile = tile_of<4>(blockIdx.x, tn, td);
+    const int64_t n0 = (int64_t)tile.x * BN, d0 = (int64_t)tile.y * BD;
+    const int64_t t_first = (int64_t)blockIdx.y * g.rows_per_split;
+    const int64_t tokens = min(g.rows - t_first, g.rows_per_split);
+    const int l = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id());
+    const int wn = w % WN, wd = w / WN;
+    const int stages = (int)((tokens + ST - 1) / ST);
+    const uint32_t lds0 = lds_addr(lds);
+
+    // ---- loads: as above, with pieces of four values; the last row's short
+    // piece is taken from n - 4 and moved up in registers
+    const uint8_t* ybase = static_cast<const uint8_t*>(g.dy) + t_first * g.ldy * 4;
+    const uint8_t* xbase = g.codes + t_first * g.pitch;
+    const uint8_t* ebase = g.exps + t_first * g.epitch;
+    const int64_t last_piece = (g.n - 1) / 4 * 4;
+    const int yc = l & 31;                          // this lane's piece of a token
+    const int ycol = (int)min(n0 + yc * 4, last_piece);
+    const int yover = max(ycol + 4 - (int)g.n, 0);  // values of it past n
+    const int lxt = w * TPW + l / (BD / 16);        // the token of X this lane loads (lanes below XL)
+    const int xcol = (int)min(d0 + (l % (BD / 16)) * 16, g.pitch - 16);
+    const int ext = w * TPW + l / (WAVE / TPW);     // and the token whose exponents it loads
+    const int ecol = (int)min(d0 / 32, g.epitch - 4);
+    auto token_y = [&](int i) { return (w * YN + i) * 2 + (l >> 5); };
+    int yoff[YN];
+#pragma unroll
+    for (int i = 0; i < YN; ++i) yoff[i] = (token_y(i) * (int)g.ldy + ycol) * 4;
+    const int xoff = lxt * (int)g.pitch + xcol, eoff = ext * (int)g.epitch + ecol;
+    // how many tokens a stage has (all of them but in the last one)
+    auto tokens_of = [&](int s) { return (int)min(tokens - (int64_t)s * ST, (int64_t)ST); };
+    auto load = [&](int part, int s) {  // one of the LOADS of a stage
+        const int64_t t0 = (int64_t)s * ST;
+        const int have = tokens_of(s);
+        const bool all = have == ST && t_first + t0 + ST < g.rows;
+        const uint32_t at = lds0 + RAT + ((s & 3) * NW + w) * RAW;
+        if (part < YN) {
+            int off = yoff[part];
+            if (!all) {
+                const int t = min(token_y(part), have - 1);
+                off = (t * (int)g.ldy + ycol - (t_first + t0 + t == g.rows - 1 ? yover : 0)) * 4;
+            }
+            load_lds16(buffer_of(ybase + t0 * g.ldy * 4, -1), at + part * 1024, off, 0);
+        } else if (part == YN) {
+            const int off = all ? xoff : min(lxt, have - 1) * (int)g.pitch + xcol;
+            if (l < XL) load_lds16(buffer_of(xbase + t0 * g.pitch, -1), at + YN * 1024, off, 0);
+        } else {
+            const int off = all ? eoff : min(ext, have - 1) * (int)g.epitch + ecol;
+            load_lds4(buffer_of(ebase + t0 * g.epitch, -1), at + YN * 1024 + XL * 16, off, 0);
+        }
+    };
+    auto load_all = [&](int s) {
+#pragma unroll
+        for (int part = 0; part < LOADS; ++part) load(part, s);
+    };
+
+    // ---- conversion of a stage by the wave that loaded it; every lane has a
+    // piece of dY a load, and 8 codes of X
+    const int cxt = l / (BD / 8), cxp = l % (BD / 8);
+    auto convert = [&](int part, int s) {
+        const uint8_t* at = lds + RAT + ((s & 3) * NW + w) * RAW;
+        uint8_t* to = lds + (s & 1) * BUF;
+        if (part < YN) {
+            f32x4 r = *reinterpret_cast<const f32x4*>(at + part * 1024 + l * 16);
+            const int t = token_y(part);
+            if (s == stages - 1) {  // tokens past the end, and the last row's short piece
+                const int have = tokens_of(s), up = t_first + tokens == g.rows && t == have - 1 ? yover : 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float v = 0.0f;
+#pragma unroll
+                    for (int f = e; f < 4; ++f)
+                        if (f == e + up) v = r[f];
+                    r[e] = t < have ? v : 0.0f;
+                }
+            }
+            u32x2 q[3];
+            pieces4(r, q);
+            uint8_t* o = to + place(t, yc >> 1, YB) + 8 * (yc & 1);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x2*>(o + p * YT) = q[p];
+        } else {
+            const u32x2 codes = *reinterpret_cast<const u32x2*>(at + YN * 1024 + l * 8);
+            const uint32_t e = *reinterpret_cast<const uint32_t*>(at + YN * 1024 + XL * 16 + l * 4);
+            const int t = w * TPW + cxt;
+            const bool live = t < tokens_of(s);
+            const float step = live ? ckpt_step((e >> (8 * (cxp >> 2))) & 0xFFu) : 0.0f;
+            const u32x2 a = held4(live ? codes.x : 0u, step, -128.0f * step), b = held4(live ? codes.y : 0u, step, -128.0f * step);
+            *reinterpret_cast<u32x4*>(to + 3 * YT + place(t, cxp, XB)) = u32x4{a.x, a.y, b.x, b.y};
+        }
+    };
+
+    const int fbase = (l >> 2) * YB + 8 * (l & 1);
+    auto frag = [&](int at, int f) {
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
+        const int o = at + fbase + (((f * 2 + ((l & 3) >> 1)) ^ (2 * ((l >> 2) & 7))) << 4);
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(lds + o));
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(lds + o + 16 * YB));
+        return __builtin_bit_cast(bf16x8, s16x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w});
+    };
+
+    f32x4 acc[FD][FN] = {};
+    if (stages > 0) {
+        load_all(0);
+        if (stages > 1) load_all(1);
+        if (stages > 2) load_all(2);
+        if (stages > 2) lds_landed_but<2 * LOADS>();
+        else lds_landed();
+#pragma unroll
+        for (int part = 0; part <= YN; ++part) convert(part, 0);
+        for (int s = 0; s < stages; ++s) {
+            // stage s is converted and this wave's loads of stage s + 1 have
+            // landed; stage s - 1 has been read by every wave
+            if (s + 2 < stages) lds_landed_but<LOADS>();
+            else lds_landed();
+            const int at = (s & 1) * BUF;
+            bf16x8 fx[FD], fy[2][FN];
+#pragma unroll
+            for (int i = 0; i < FD; ++i) fx[i] = frag(at + 3 * YT, wd * FD + i);
+#pragma unroll
+            for (int j = 0; j < FN; ++j) fy[0][j] = frag(at, wn * FN + j);
+            if (s + 3 < stages) load_all(s + 3);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
+                if (p < 2) {
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) fy[(p + 1) & 1][j] = frag(at + (p + 1) * YT, wn * FN + j);
+                }
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+#pragma unroll
+                    for (int i = 0; i < FD; ++i)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[i], fy[p & 1][j], acc[i][j], 0, 0, 0);
+                if (s + 1 < stages) {  // beside the products
+#pragma unroll
+                    for (int part = p * (YN + 1) / 3; part < (p + 1) * (YN + 1) / 3; ++part) convert(part, s + 1);
+                }
+            }
+        }
+    }
+    store_dw<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16);
+}
+
 // dW (+)= the splits' partial sums, added in the splits' order.
 __global__ void __launch_bounds__(256)
 k_ckpt8_wgrad_join(const float* __restrict__ part, int32_t splits, int64_t n, int64_t dim, int64_t ldp,
@@ -538,39 +704,82 @@ k_ckpt8_wgrad_join(const float* __restrict__ part, int32_t splits, int64_t n, in
     }
 }
 
+// ------------------------------------------------------------------ plan
+// Tile and number of token splits: the pair whose measured parts add up to
+// the least time.  A round is what all 256 compute units do at one time
+// (`slots` blocks); it takes `stage_us` for each 32 tokens and `store_us` at
+// its end; joining splits takes a launch and the traffic of their sums.
+// Measured against each other: 4096 x 4096 x 4096 (tokens, n, dim) 256 x 256
+// 118 us, 128 x 128 181 us; 2048^3 128 x 128 35 us, 256 x 256 58 us; 4096 x
+// 1024 x 1024 in 1 split 58 us, 2 39 us, 4 28 us, 16 37 us; 16384 x 1024 x
+// 1024 256 x 256 in 16 splits 55 us, 128 x 128 in 8 62 us.
+struct Shape {
+    int tile, slots;
+    float stage_us, store_us;
+    float alone_us;  // stage_us when at most 256 blocks run, one a compute unit
+};
+constexpr Shape kBf16Shapes[] = {{128, 512, 0.75f, 4.0f, 0.45f}, {256, 256, 0.83f, 8.0f, 0.83f}};
+constexpr Shape kF32Shapes[] = {{128, 256, 1.2f, 4.0f, 1.2f}};
+
 struct Plan {
-    int tile;  // 256 or 128
+    int tile;
     int32_t splits;
     int64_t rows_per_split;
 };
 
 Plan plan_of(int64_t rows, int64_t n, int64_t dim, bool bf16) {
-    const auto tiles = [&](int64_t b) { return ((n + b - 1) / b) * ((dim + b - 1) / b); };
-    Plan p{128, 1, 0};
-    if (bf16 && tiles(256) >= 192) p.tile = 256;
-    const int64_t steps = (rows + 63) / 64, t = tiles(p.tile);
-    int64_t s = t >= 256 ? 1 : (512 + t - 1) / t;
-    s = s < steps / 4 ? s : steps / 4;  // at least four steps a split
-    if (s < 1) s = 1;
-    p.rows_per_split = ((steps + s - 1) / s) * 64;
-    if (p.rows_per_split < 64) p.rows_per_split = 64;
-    p.splits = (int32_t)(rows > 0 ? (rows + p.rows_per_split - 1) / p.rows_per_split : 1);
-    return p;
+    Plan best{128, 1, 64};
+    double least = 0;
+    const int64_t units = rows > 0 ? (rows + 63) / 64 : 1;  // splits are whole pairs of stages
+    for (const Shape& s : kBf16Shapes) {
+        const Shape& shape = bf16 ? s : kF32Shapes[0];
+        const int64_t tiles = ((n + shape.tile - 1) / shape.tile) * ((dim + shape.tile - 1) / shape.tile);
+        for (int64_t want = 1; want <= 64 && want <= units; ++want) {
+            const int64_t per = (units + want - 1) / want, splits = (units + per - 1) / per;
+            if (splits != want) continue;
+            const int64_t blocks = tiles * splits, rounds = (blocks + shape.slots - 1) / shape.slots;
+            double us = (double)rounds * (2.0 * (double)per * (blocks <= 256 ? shape.alone_us : shape.stage_us) + shape.store_us);
+            if (splits > 1) us += 2.5 + (double)(splits + 1) * (double)n * (double)dim * (4.0 / 6e6);
+            if (least == 0 || us < least) {
+                least = us;
+                best = Plan{shape.tile, (int32_t)splits, per * 64};
+            }
+        }
+        if (!bf16) break;
+    }
+    return best;
 }
 
 int64_t part_pitch(int64_t dim) { return (dim + 3) & ~int64_t(3); }
 
-template <int B, int WN, int WD>
-hipError_t launch_pipe(const Args& g, const Plan& p, hipStream_t stream) {
-    const dim3 grid((unsigned)(((g.n + B - 1) / B) * ((g.dim + B - 1) / B)), (unsigned)p.splits);
-    hipLaunchKernelGGL((k_ckpt8_wgrad_pipe<B, B, WN, WD>), grid, dim3(WN * WD * WAVE), 0, stream, g);
+template <int BN, int BD, int WN, int WD>
+hipError_t launch_pipe_f32(const Args& g, int32_t splits, hipStream_t stream) {
+    const dim3 grid((unsigned)(((g.n + BN - 1) / BN) * ((g.dim + BD - 1) / BD)), (unsigned)splits);
+    hipLaunchKernelGGL((k_ckpt8_wgrad_pipe_f32<BN, BD, WN, WD>), grid, dim3(WN * WD * WAVE), 0, stream, g);
     return hipGetLastError();
 }
 
-template <int P, bool DMA, int B, int WN, int WD, int TK>
-hipError_t launch_tile(const Args& g, const Plan& p, hipStream_t stream) {
-    const dim3 grid((unsigned)(((g.n + B - 1) / B) * ((g.dim + B - 1) / B)), (unsigned)p.splits);
-    hipLaunchKernelGGL((k_ckpt8_wgrad<P, DMA, B, B, WN, WD, TK>), grid, dim3(WN * WD * WAVE), 0, stream, g);
+template <int BN, int BD, int WN, int WD>
+hipError_t launch_pipe(const Args& g, int32_t splits, hipStream_t stream) {
+    const dim3 grid((unsigned)(((g.n + BN - 1) / BN) * ((g.dim + BD - 1) / BD)), (unsigned)splits);
+    hipLaunchKernelGGL((k_ckpt8_wgrad_pipe<BN, BD, WN, WD>), grid, dim3(WN * WD * WAVE), 0, stream, g);
+    return hipGetLastError();
+}
+
+template <int P, int B, int WN, int WD, int TK>
+hipError_t launch_tile(const Args& g, int32_t splits, hipStream_t stream) {
+    const dim3 grid((unsigned)(((g.n + B - 1) / B) * ((g.dim + B - 1) / B)), (unsigned)splits);
+    hipLaunchKernelGGL((k_ckpt8_wgrad<P, B, B, WN, WD, TK>), grid, dim3(WN * WD * WAVE), 0, stream, g);
+    return hipGetLastError();
+}
+
+// g.out, g.ldw: the partial sums of launch_pipe or launch_tile
+hipError_t launch_join(const Args& g, int32_t splits, void* dw, bool dw_bf16, int64_t ldw, bool accumulate,
+                       hipStream_t stream) {
+    const int64_t pieces = g.n * (g.ldw / 4), blocks = (pieces + 255) / 256;
+    hipLaunchKernelGGL(k_ckpt8_wgrad_join, dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), dim3(256), 0,
+                       stream, static_cast<const float*>(g.out), splits, g.n, g.dim, g.ldw, dw, ldw, (int32_t)dw_bf16,
+                       (int32_t)accumulate);
     return hipGetLastError();
 }
 
@@ -602,18 +811,14 @@ hipError_t launch_ckpt8_wgrad(const void* dy, bool dy_bf16, int64_t ldy, const v
     g.out_bf16 = p.splits > 1 ? 0 : dw_bf16;
     g.accumulate = p.splits > 1 ? 0 : accumulate;
     g.wide = g.ldw % 4 == 0 && reinterpret_cast<uintptr_t>(g.out) % (g.out_bf16 ? 8 : 16) == 0;
-    const bool dma = dy_bf16 && n % 8 == 0 && ldy % 8 == 0 && reinterpret_cast<uintptr_t>(dy) % 16 == 0;
     hipError_t e;
-    if (!dy_bf16) e = launch_tile<3, false, 128, 2, 2, 64>(g, p, stream);
-    else if (p.tile == 256) e = dma ? launch_pipe<256, 2, 4>(g, p, stream)
-                                    : launch_tile<1, false, 256, 2, 4, 64>(g, p, stream);
-    else e = dma ? launch_pipe<128, 2, 2>(g, p, stream) : launch_tile<1, false, 128, 2, 2, 64>(g, p, stream);
+    if (!dy_bf16) e = n < 4 ? launch_tile<3, 128, 2, 2, 64>(g, p.splits, stream)
+                            : launch_pipe_f32<128, 128, 2, 4>(g, p.splits, stream);
+    else if (n < 8) e = launch_tile<1, 128, 2, 2, 64>(g, p.splits, stream);
+    else if (p.tile == 256) e = launch_pipe<256, 256, 2, 4>(g, p.splits, stream);
+    else e = launch_pipe<128, 128, 2, 2>(g, p.splits, stream);
     if (e != hipSuccess || p.splits == 1) return e;
-    const int64_t pieces4 = n * (part_pitch(dim) / 4), blocks = (pieces4 + 255) / 256;
-    hipLaunchKernelGGL(k_ckpt8_wgrad_join, dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), dim3(256), 0,
-                       stream, static_cast<const float*>(workspace), p.splits, n, dim, part_pitch(dim), dw, ldw,
-                       (int32_t)dw_bf16, (int32_t)accumulate);
-    return hipGetLastError();
+    return launch_join(g, p.splits, dw, dw_bf16, ldw, accumulate, stream);
 }
 
 }  // namespace qc
