@@ -27,18 +27,28 @@ struct KeptIn {
 
 // Where a thread works: 16 lanes are a unit of 128 columns, a block of 256
 // threads holds 16 units, 2^lx of them side by side and the others in rows
-// below, so narrow matrices fill blocks too.
+// below, so narrow matrices fill blocks too.  Grid: x the tiles of a row, y
+// the tiles of rows.  Saving and restoring take two of the latter at a time,
+// with the loads of both before the first use (8192 x 8192 bf16: save 34.3
+// us against 38.4 with one and 34.4 with four, restore 34.6 against 35.3 and
+// 35.7); the gated activation, which holds more, takes one (backward 87 us
+// against 92 with two).
+constexpr int kUnroll = 2;
 struct Place {
     int64_t row, col;
     bool live;  // the unit has values (its lanes may still be past dim)
 };
 
-__device__ __forceinline__ Place place_of(int64_t tile, int64_t rows, int64_t dim, int lx, int64_t col_tiles) {
+struct Sizes {
+    int64_t rows, dim, pitch, epitch, row_tiles;
+    int lx;
+};
+
+__device__ __forceinline__ Place place_of(int64_t rt, const Sizes& z) {
     const int unit = threadIdx.x >> 4, l = threadIdx.x & 15;
-    const int64_t rt = tile / col_tiles, ct = tile - rt * col_tiles;
-    const int64_t row = (rt << (4 - lx)) + (unit >> lx);
-    const int64_t u = (ct << lx) + (unit & ((1 << lx) - 1));
-    return Place{row, u * 128 + 8 * l, row < rows && u * 128 < dim};
+    const int64_t row = (rt << (4 - z.lx)) + (unit >> z.lx);
+    const int64_t u = ((int64_t)blockIdx.x << z.lx) + (unit & ((1 << z.lx) - 1));
+    return Place{row, u * 128 + 8 * l, row < z.rows && u * 128 < z.dim};
 }
 
 // The exponent bytes of a unit's four groups, gathered into lane 0 of its 16
@@ -51,77 +61,110 @@ __device__ __forceinline__ uint32_t gather_bytes(uint32_t b) {
 }
 
 // Every lane of the wave calls this (lanes without values hold zeros).
-__device__ __forceinline__ void keep8(const float (&v)[8], const Place& p, int64_t dim, const Kept& k,
-                                      int64_t pitch, int64_t epitch) {
+__device__ __forceinline__ void keep8(const float (&v)[8], const Place& p, const Sizes& z, const Kept& k) {
     uint32_t amax = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) amax = umax(amax, abs_bits(v[i]));
     amax = quad_max(amax);
-    const bool group = p.live && (p.col & ~int64_t(31)) < dim;  // else: padding, byte 0
+    const bool group = p.live && (p.col & ~int64_t(31)) < z.dim;  // else: padding, byte 0
     const uint32_t byte = group ? ckpt_byte(amax) : 0u;
     const uint32_t word = gather_bytes(byte);
-    if (p.live && (threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t*>(k.exps + p.row * epitch + p.col / 32) = word;
+    if (p.live && (threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t*>(k.exps + p.row * z.epitch + p.col / 32) = word;
     if (group) {
-        const float inv = __uint_as_float((254u - min(byte, 254u)) << 23);
-        float q[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = byte == kCkptNaN ? 0.0f : ckpt_code(v[i], inv);
-        const u32x2 w = {pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7])};
-        __builtin_nontemporal_store(w, reinterpret_cast<u32x2*>(k.codes + p.row * pitch + p.col));
+        const u32x2 w = ckpt_codes(v, byte);
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x2*>(k.codes + p.row * z.pitch + p.col));
     }
 }
 
-__device__ __forceinline__ void held8(const KeptIn& k, const Place& p, int64_t pitch, int64_t epitch, float (&v)[8]) {
-    const u32x2 w = ld_stream_u2(k.codes + p.row * pitch + p.col);
-    const float step = ckpt_step(k.exps[p.row * epitch + p.col / 32]);
+struct Raw8 {  // 8 codes and their step's byte
+    u32x2 codes;
+    uint32_t byte;
+};
+__device__ __forceinline__ Raw8 held_raw8(const KeptIn& k, const Place& p, const Sizes& z) {
+    if (!(p.live && p.col < z.dim)) return Raw8{u32x2{0, 0}, 0};
+    return Raw8{ld_stream_u2(k.codes + p.row * z.pitch + p.col), k.exps[p.row * z.epitch + p.col / 32]};
+}
+__device__ __forceinline__ int64_t left_of(const Place& p, const Sizes& z) { return p.live ? z.dim - p.col : 0; }
+
+template <class T>
+__global__ void __launch_bounds__(256)
+k_enc_ckpt8(const T* __restrict__ x, int64_t ldx, Sizes z, Kept k) {
+    constexpr int U = kUnroll;
+    for (int64_t rt = (int64_t)blockIdx.y * U; rt < z.row_tiles; rt += (int64_t)gridDim.y * U) {
+        float v[U][8];
+        Place p[U];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (float)(int8_t)(w[i >> 2] >> (8 * (i & 3))) * step;
+        for (int u = 0; u < U; ++u) {
+            p[u] = place_of(rt + u, z);
+            load8(x + p[u].row * ldx + p[u].col, left_of(p[u], z), v[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) keep8(v[u], p[u], z, k);
+    }
 }
 
 template <class T>
 __global__ void __launch_bounds__(256)
-k_enc_ckpt8(const T* __restrict__ x, int64_t ldx, int64_t rows, int64_t dim, int lx, int64_t col_tiles, int64_t tiles,
-            Kept k, int64_t pitch, int64_t epitch) {
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const Place p = place_of(tile, rows, dim, lx, col_tiles);
-        float v[8];
-        load8(x + p.row * ldx + p.col, p.live ? dim - p.col : 0, v);
-        keep8(v, p, dim, k, pitch, epitch);
-    }
-}
-
-template <class T>
-__global__ void __launch_bounds__(256)
-k_dec_ckpt8(KeptIn k, int64_t pitch, int64_t epitch, int64_t rows, int64_t dim, int lx, int64_t col_tiles,
-            int64_t tiles, T* __restrict__ out, int64_t ldo) {
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const Place p = place_of(tile, rows, dim, lx, col_tiles);
-        if (p.live && p.col < dim) {
+k_dec_ckpt8(KeptIn k, Sizes z, T* __restrict__ out, int64_t ldo) {
+    constexpr int U = kUnroll;
+    for (int64_t rt = (int64_t)blockIdx.y * U; rt < z.row_tiles; rt += (int64_t)gridDim.y * U) {
+        Raw8 r[U];
+        Place p[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            p[u] = place_of(rt + u, z);
+            r[u] = held_raw8(k, p[u], z);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
             float v[8];
-            held8(k, p, pitch, epitch, v);
-            store8(out + p.row * ldo + p.col, dim - p.col, v);
+            ckpt_values(r[u].codes, r[u].byte, v);
+            store8(out + p[u].row * ldo + p[u].col, left_of(p[u], z), v);
         }
     }
+}
+
+// s = 1 / (1 + exp(-x)) and c = 1 - s.  With a = exp(-|x|), in (0, 1], r =
+// 1 / (1 + a): r and a * r are the two of them, the larger first, neither
+// from a difference.  a = 2^t (1 + d ln 2) with t = fl(-|x| log2 e) and d what
+// its rounding left, so that a's relative error does not grow with |x|;
+// below 2^-126 it becomes 0.  r takes one Newton step from the hardware's
+// reciprocal.  About 20 issue slots against 45 with expf and divisions,
+// which the forward pass was bound by (8192 x 8192: 106 us).
+__device__ __forceinline__ void sigmoid(float x, float& s, float& c) {
+    constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0c0p-26f, kLn2 = 0x1.62e430p-1f;
+    const float m = fminf(fabsf(x), 200.0f);  // an infinity has no such d
+    const float t = m * -kLog2e;
+    const float d = __builtin_fmaf(m, -kLog2eLow, __builtin_fmaf(m, -kLog2e, -t));
+    const float e = __builtin_amdgcn_exp2f(t);
+    const float a = __builtin_fmaf(e, d * kLn2, e);
+    const float q = 1.0f + a, r0 = __builtin_amdgcn_rcpf(q);
+    const float r = __builtin_fmaf(__builtin_fmaf(-q, r0, 1.0f), r0, r0);
+    const float ar = a * r;
+    s = x < 0.0f ? ar : r;
+    c = x < 0.0f ? r : ar;
 }
 
 // h = silu(g) * u, and the checkpoints of g and u.
 template <class T>
 __global__ void __launch_bounds__(256)
-k_swiglu_ckpt8(const T* __restrict__ gate, const T* __restrict__ up, int64_t ldx, int64_t rows, int64_t dim, int lx,
-               int64_t col_tiles, int64_t tiles, T* __restrict__ h, int64_t ldh, Kept kg, Kept ku, int64_t pitch,
-               int64_t epitch) {
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const Place p = place_of(tile, rows, dim, lx, col_tiles);
-        const int64_t left = p.live ? dim - p.col : 0;
+k_swiglu_ckpt8(const T* __restrict__ gate, const T* __restrict__ up, int64_t ldx, Sizes z, T* __restrict__ h,
+               int64_t ldh, Kept kg, Kept ku) {
+    for (int64_t rt = blockIdx.y; rt < z.row_tiles; rt += gridDim.y) {
+        const Place p = place_of(rt, z);
         float g[8], u[8];
-        load8(gate + p.row * ldx + p.col, left, g);
-        load8(up + p.row * ldx + p.col, left, u);
-        keep8(g, p, dim, kg, pitch, epitch);
-        keep8(u, p, dim, ku, pitch, epitch);
+        load8(gate + p.row * ldx + p.col, left_of(p, z), g);
+        load8(up + p.row * ldx + p.col, left_of(p, z), u);
+        keep8(g, p, z, kg);
+        keep8(u, p, z, ku);
         float o[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = g[i] / (1.0f + expf(-g[i])) * u[i];
-        store8(h + p.row * ldh + p.col, left, o);
+        for (int e = 0; e < 8; ++e) {
+            float s, c;
+            sigmoid(g[e], s, c);
+            o[e] = g[e] * s * u[e];
+        }
+        store8(h + p.row * ldh + p.col, left_of(p, z), o);
     }
 }
 
@@ -129,81 +172,78 @@ k_swiglu_ckpt8(const T* __restrict__ gate, const T* __restrict__ up, int64_t ldx
 //   dU = dh * G * s,  dG = dh * U * s * (1 + G * (1 - s)).
 template <class T>
 __global__ void __launch_bounds__(256)
-k_swiglu_ckpt8_bwd(const T* __restrict__ dh, int64_t lddh, KeptIn kg, KeptIn ku, int64_t pitch, int64_t epitch,
-                   int64_t rows, int64_t dim, int lx, int64_t col_tiles, int64_t tiles, T* __restrict__ dgate,
+k_swiglu_ckpt8_bwd(const T* __restrict__ dh, int64_t lddh, KeptIn kg, KeptIn ku, Sizes z, T* __restrict__ dgate,
                    T* __restrict__ dup, int64_t ldg) {
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const Place p = place_of(tile, rows, dim, lx, col_tiles);
-        if (p.live && p.col < dim) {
-            const int64_t left = dim - p.col;
-            float d[8], g[8], u[8];
-            load8(dh + p.row * lddh + p.col, left, d);
-            held8(kg, p, pitch, epitch, g);
-            held8(ku, p, pitch, epitch, u);
+    for (int64_t rt = blockIdx.y; rt < z.row_tiles; rt += gridDim.y) {
+        const Place p = place_of(rt, z);
+        float d[8], g[8], u[8];
+        load8(dh + p.row * lddh + p.col, left_of(p, z), d);
+        const Raw8 rg = held_raw8(kg, p, z), ru = held_raw8(ku, p, z);
+        ckpt_values(rg.codes, rg.byte, g);
+        ckpt_values(ru.codes, ru.byte, u);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float s = 1.0f / (1.0f + expf(-g[i]));
-                const float a = d[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
-                u[i] = d[i] * g[i] * s;
-                g[i] = a;
-            }
-            store8(dgate + p.row * ldg + p.col, left, g);
-            store8(dup + p.row * ldg + p.col, left, u);
+        for (int e = 0; e < 8; ++e) {
+            float s, c;
+            sigmoid(g[e], s, c);
+            const float ds = d[e] * s;
+            const float a = ds * u[e] * (1.0f + g[e] * c);
+            u[e] = ds * g[e];
+            g[e] = a;
         }
+        store8(dgate + p.row * ldg + p.col, left_of(p, z), g);
+        store8(dup + p.row * ldg + p.col, left_of(p, z), u);
     }
 }
 
-struct Tiling {
-    int lx;
-    int64_t col_tiles, tiles, pitch, epitch;
-    dim3 grid() const { return dim3((unsigned)(tiles < kMaxBlocks ? tiles : kMaxBlocks)); }
+struct Launch {
+    Sizes z;
+    dim3 grid;
 };
 
-Tiling tiling(int64_t rows, int64_t dim) {
-    Tiling t;
+// `unroll`: tiles of rows that a thread takes at a time
+Launch launch_of(int64_t rows, int64_t dim, int unroll) {
+    Launch n;
     const int64_t units = (dim + 127) / 128;
-    t.lx = units >= 16 ? 4 : log2_exact(units);
-    t.col_tiles = (units + (1 << t.lx) - 1) >> t.lx;
-    const int64_t rpb = 16 >> t.lx;
-    t.tiles = (rows + rpb - 1) / rpb * t.col_tiles;
-    t.pitch = (dim + 31) / 32 * 32;
-    t.epitch = units * 4;
-    return t;
+    n.z.rows = rows;
+    n.z.dim = dim;
+    n.z.lx = units >= 16 ? 4 : log2_exact(units);
+    n.z.pitch = (dim + 31) / 32 * 32;
+    n.z.epitch = units * 4;
+    n.z.row_tiles = (rows + (16 >> n.z.lx) - 1) >> (4 - n.z.lx);
+    const int64_t y = (n.z.row_tiles + unroll - 1) / unroll;
+    n.grid = dim3((unsigned)((units + (1 << n.z.lx) - 1) >> n.z.lx), (unsigned)(y < 65535 ? y : 65535));
+    return n;
 }
 
 template <class T>
 hipError_t enc(const void* x, int64_t ldx, int64_t rows, int64_t dim, Kept k, hipStream_t stream) {
-    const Tiling t = tiling(rows, dim);
-    hipLaunchKernelGGL(k_enc_ckpt8<T>, t.grid(), dim3(256), 0, stream, static_cast<const T*>(x), ldx, rows, dim, t.lx,
-                       t.col_tiles, t.tiles, k, t.pitch, t.epitch);
+    const Launch n = launch_of(rows, dim, kUnroll);
+    hipLaunchKernelGGL((k_enc_ckpt8<T>), n.grid, dim3(256), 0, stream, static_cast<const T*>(x), ldx, n.z, k);
     return hipGetLastError();
 }
 
 template <class T>
 hipError_t dec(KeptIn k, int64_t rows, int64_t dim, void* out, int64_t ldo, hipStream_t stream) {
-    const Tiling t = tiling(rows, dim);
-    hipLaunchKernelGGL(k_dec_ckpt8<T>, t.grid(), dim3(256), 0, stream, k, t.pitch, t.epitch, rows, dim, t.lx,
-                       t.col_tiles, t.tiles, static_cast<T*>(out), ldo);
+    const Launch n = launch_of(rows, dim, kUnroll);
+    hipLaunchKernelGGL((k_dec_ckpt8<T>), n.grid, dim3(256), 0, stream, k, n.z, static_cast<T*>(out), ldo);
     return hipGetLastError();
 }
 
 template <class T>
 hipError_t swiglu(const void* gate, const void* up, int64_t ldx, int64_t rows, int64_t dim, void* h, int64_t ldh,
                   Kept kg, Kept ku, hipStream_t stream) {
-    const Tiling t = tiling(rows, dim);
-    hipLaunchKernelGGL(k_swiglu_ckpt8<T>, t.grid(), dim3(256), 0, stream, static_cast<const T*>(gate),
-                       static_cast<const T*>(up), ldx, rows, dim, t.lx, t.col_tiles, t.tiles, static_cast<T*>(h), ldh,
-                       kg, ku, t.pitch, t.epitch);
+    const Launch n = launch_of(rows, dim, 1);
+    hipLaunchKernelGGL((k_swiglu_ckpt8<T>), n.grid, dim3(256), 0, stream, static_cast<const T*>(gate),
+                       static_cast<const T*>(up), ldx, n.z, static_cast<T*>(h), ldh, kg, ku);
     return hipGetLastError();
 }
 
 template <class T>
 hipError_t swiglu_bwd(const void* dh, int64_t lddh, KeptIn kg, KeptIn ku, int64_t rows, int64_t dim, void* dgate,
                       void* dup, int64_t ldg, hipStream_t stream) {
-    const Tiling t = tiling(rows, dim);
-    hipLaunchKernelGGL(k_swiglu_ckpt8_bwd<T>, t.grid(), dim3(256), 0, stream, static_cast<const T*>(dh), lddh, kg, ku,
-                       t.pitch, t.epitch, rows, dim, t.lx, t.col_tiles, t.tiles, static_cast<T*>(dgate),
-                       static_cast<T*>(dup), ldg);
+    const Launch n = launch_of(rows, dim, 1);
+    hipLaunchKernelGGL((k_swiglu_ckpt8_bwd<T>), n.grid, dim3(256), 0, stream, static_cast<const T*>(dh), lddh, kg,
+                       ku, n.z, static_cast<T*>(dgate), static_cast<T*>(dup), ldg);
     return hipGetLastError();
 }
 

@@ -39,16 +39,13 @@ struct Args {
 // eight neighbouring tokens on different banks.
 __device__ __forceinline__ int place(int t, int c, int row_bytes) { return t * row_bytes + ((c ^ (2 * (t & 7))) << 4); }
 
-// Four bf16 values from four codes: code * step is exact, so its upper half
-// is the bf16 value.  (c + 128) is read from a byte of the word xor 0x80..,
-// and 128 * step taken off again in the multiply-add, exactly.
-__device__ __forceinline__ u32x2 held4(uint32_t word, float step, float off) {
-    const uint32_t w = word ^ 0x80808080u;
-    const uint32_t a = __float_as_uint(__builtin_fmaf((float)(w & 0xFFu), step, off));
-    const uint32_t b = __float_as_uint(__builtin_fmaf((float)((w >> 8) & 0xFFu), step, off));
-    const uint32_t c = __float_as_uint(__builtin_fmaf((float)((w >> 16) & 0xFFu), step, off));
-    const uint32_t d = __float_as_uint(__builtin_fmaf((float)(w >> 24), step, off));
-    return u32x2{__builtin_amdgcn_perm(b, a, 0x07060302u), __builtin_amdgcn_perm(d, c, 0x07060302u)};
+// Four bf16 values from four codes: code * step is exact and its upper half
+// is the bf16 value.
+__device__ __forceinline__ u32x2 held4(uint32_t word, float step) {
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(code_of(word, i) * step);
+    return u32x2{__builtin_amdgcn_perm(v[1], v[0], 0x07060302u), __builtin_amdgcn_perm(v[3], v[2], 0x07060302u)};
 }
 
 // The three pieces of an fp32 value (8 mantissa bits each, cut off, so their
@@ -164,11 +161,10 @@ k_ckpt8_wgrad(Args g) {
         for (int i = 0; i < XG; ++i) {
             const int id = i * THREADS + threadIdx.x;
             const int t = id / (BD / 32), c = (id % (BD / 32)) * 4;
-            const float off = -128.0f * xstep[i];
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
-                const u32x2 a = held4(xw[i][h >> 1][2 * (h & 1)], xstep[i], off);
-                const u32x2 b = held4(xw[i][h >> 1][2 * (h & 1) + 1], xstep[i], off);
+                const u32x2 a = held4(xw[i][h >> 1][2 * (h & 1)], xstep[i]);
+                const u32x2 b = held4(xw[i][h >> 1][2 * (h & 1) + 1], xstep[i]);
                 *reinterpret_cast<u32x4*>(tile + place(t, c + h, XB)) = u32x4{a.x, a.y, b.x, b.y};
             }
         }
@@ -312,7 +308,7 @@ __global__ void __launch_bounds__(WN * WD * WAVE)
 k_ckpt8_wgrad_pipe(Args g) {
     constexpr int NW = WN * WD, THREADS = NW * WAVE;
     constexpr int FN = BN / WN / 16, FD = BD / WD / 16;
-    constexpr int AHEAD = FN >= 8 ? 3 : 2;
+    constexpr int AHEAD = 2;  // fragments of dY read ahead (of a ring of 4)
     constexpr int YB = BN * 2, XB = BD * 2;        // bytes of a token in a tile
     constexpr int YT = ST * YB, XT = ST * XB;
     constexpr int YN = YT / 1024 / NW;             // loads of dY a wave and stage
@@ -347,14 +343,14 @@ k_ckpt8_wgrad_pipe(Args g) {
     const int64_t last_piece = (g.n - 1) / 8 * 8;
     const bool patch = t_first + tokens == g.rows && g.n % 8 != 0;
     const int first_col = (int)n0, last_col = (int)last_piece;
-    auto ytok = [&](int i) { return (w * YN + i) * (1024 / YB) + l / (YB / 16); };
-    auto ycol = [&](int i) {
-        const int c = (l % (YB / 16)) ^ (2 * (ytok(i) & 7));
+    auto ytok = [&](int i, int lane) { return (w * YN + i) * (1024 / YB) + lane / (YB / 16); };
+    auto ycol = [&](int i, int lane) {
+        const int c = (lane % (YB / 16)) ^ (2 * (ytok(i, lane) & 7));
         return min(first_col + c * 8, last_col);
     };
     int yoff[YN];
 #pragma unroll
-    for (int i = 0; i < YN; ++i) yoff[i] = (ytok(i) * (int)g.ldy + ycol(i)) * 2;
+    for (int i = 0; i < YN; ++i) yoff[i] = (ytok(i, l) * (int)g.ldy + ycol(i, l)) * 2;
     const int xt = w * TPW + l / (BD / 16), xq = l % (BD / 16);  // this lane's token of a stage, and 16 codes of it
     const int xcol = (int)min(d0 + xq * 16, g.pitch - 16);
     const int ecol = (int)min((d0 + xq * 16) / 128 * 4, g.epitch - 4);
@@ -363,8 +359,10 @@ k_ckpt8_wgrad_pipe(Args g) {
         int off = yoff[i];
         if (!decltype(fast)::value) {
             t0 = min(t0, tokens - 1);
-            const int last = (int)min(tokens - 1 - t0, (int64_t)ST), t = min(ytok(i), last);
-            const int col = ycol(i);
+            int lane = l;
+            asm("" : "+v"(lane));  // computed anew: held through the main loop, these would not fit the registers
+            const int last = (int)min(tokens - 1 - t0, (int64_t)ST), t = min(ytok(i, lane), last);
+            const int col = ycol(i, lane);
             off = (t * (int)g.ldy + (patch && t == last && col == last_col ? (int)g.n - 8 : col)) * 2;
         }
         load_lds16(buffer_of(ybase + t0 * g.ldy * 2, -1), lds0 + (s & 3) * YT + (w * YN + i) * 1024, off, 0);
@@ -408,11 +406,10 @@ k_ckpt8_wgrad_pipe(Args g) {
             step = 0.0f;
             q = u32x4{0, 0, 0, 0};
         }
-        const float off = -128.0f * step;
         uint8_t* at = lds + XAT + (s & 1) * XT;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const u32x2 a = held4(q[2 * h], step, off), b = held4(q[2 * h + 1], step, off);
+            const u32x2 a = held4(q[2 * h], step), b = held4(q[2 * h + 1], step);
             *reinterpret_cast<u32x4*>(at + (xplace ^ (16 * h))) = u32x4{a.x, a.y, b.x, b.y};
         }
     };
@@ -626,7 +623,7 @@ k_ckpt8_wgrad_pipe_f32(Args g) {
             const int t = w * TPW + cxt;
             const bool live = t < tokens_of(s);
             const float step = live ? ckpt_step((e >> (8 * (cxp >> 2))) & 0xFFu) : 0.0f;
-            const u32x2 a = held4(live ? codes.x : 0u, step, -128.0f * step), b = held4(live ? codes.y : 0u, step, -128.0f * step);
+            const u32x2 a = held4(live ? codes.x : 0u, step), b = held4(live ? codes.y : 0u, step);
             *reinterpret_cast<u32x4*>(to + 3 * YT + place(t, cxp, XB)) = u32x4{a.x, a.y, b.x, b.y};
         }
     };

@@ -16,14 +16,15 @@
 namespace qc {
 namespace {
 
-// Code of v for the row's scale s and r = fl(1/s).  v * r is within 127 *
-// 2^-23 (1.6e-5) of the real quotient, so unless it lies closer than 2e-5 to
-// the middle between two integers its nearest integer is the right one;
-// `near` collects the exceptions, which the caller decides in 64 bits.
-__device__ __forceinline__ float code_fast(float v, float r, bool& near) {
-    const float q = __builtin_rintf(v * r);
-    near |= !(fabsf(__builtin_fmaf(v, r, -q)) < 0.49998f);
-    return q;
+// Sum (see kWhole) whose low byte is the code of v, for r = fl(1/s) of the
+// row's scale s.  v * r is within 127 * 2^-23 (1.6e-5) of the real quotient,
+// so unless it lies closer than 2e-5 to the middle between two whole
+// numbers its nearest one is the right one; `far` gathers the distance from
+// it, and the caller decides the exceptions in 64 bits.
+__device__ __forceinline__ float code_fast(float v, float r, float& far) {
+    const float sum = __builtin_fmaf(v, r, kWhole);
+    far = fmaxf(far, fabsf(__builtin_fmaf(v, r, kWhole - sum)));
+    return sum;
 }
 
 // In 64 bits the quotient of two fp32 numbers is a half-integer only if the
@@ -31,21 +32,21 @@ __device__ __forceinline__ float code_fast(float v, float r, bool& near) {
 // 2^-32 of it.
 __device__ __forceinline__ float code_exact(float v, float s) {
     const double q = __builtin_rint((double)v / (double)s);
-    return (float)fmin(fmax(q, -127.0), 127.0);
+    return (float)fmin(fmax(q, -127.0), 127.0) + kWhole;
 }
 
 __device__ __forceinline__ uint64_t encode8(const float (&v)[8], float s, float r, bool fast) {
-    float q[8];
-    bool near = !fast;
+    float q[8], far = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = code_fast(v[i], r, near);
+    for (int i = 0; i < 8; ++i) q[i] = code_fast(v[i], r, far);
+    const bool near = !fast || far >= 0.49998f;
     if (__any(near)) {
         if (near) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = s > 0.0f ? code_exact(v[i], s) : 0.0f;
+            for (int i = 0; i < 8; ++i) q[i] = s > 0.0f ? code_exact(v[i], s) : kWhole;
         }
     }
-    return (uint64_t)pack4(q[0], q[1], q[2], q[3]) | ((uint64_t)pack4(q[4], q[5], q[6], q[7]) << 32);
+    return (uint64_t)low_bytes(q[0], q[1], q[2], q[3]) | ((uint64_t)low_bytes(q[4], q[5], q[6], q[7]) << 32);
 }
 
 __device__ __forceinline__ uint32_t amax8(const float (&v)[8]) {

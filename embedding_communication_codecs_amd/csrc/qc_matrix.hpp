@@ -88,10 +88,16 @@ __device__ __forceinline__ void store8(float* p, int64_t left, const float (&v)[
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-// Four small whole floats as the bytes of a word, first value lowest.
-__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
-    return ((uint32_t)(int)a & 0xFFu) | (((uint32_t)(int)b & 0xFFu) << 8) | (((uint32_t)(int)c & 0xFFu) << 16) |
-           ((uint32_t)(int)d << 24);
+// 1.5 * 2^23: a number of magnitude up to 2^22 added to it is rounded to a
+// whole number, to nearest even, whose two's complement low bits are those
+// of the sum's bit pattern.
+constexpr float kWhole = 12582912.0f;
+
+// The low bytes of four such sums as a word, the first lowest.
+__device__ __forceinline__ uint32_t low_bytes(float a, float b, float c, float d) {
+    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(d), __float_as_uint(c), 0x04000C0Cu);
+    return lo | hi;
 }
 
 constexpr uint32_t kInfBits = 0x7F800000u;
@@ -111,10 +117,28 @@ __device__ __forceinline__ uint32_t ckpt_byte(uint32_t amax_bits) {
     return amax_bits >= kInfBits ? kCkptNaN : (uint32_t)min(max(e, 1), 248);
 }
 __device__ __forceinline__ float ckpt_step(uint32_t byte) { return __uint_as_float(byte << 23); }
-// x * 2^-E is exact but where it underflows (code 0 either way), so the
-// code is the nearest integer of the real quotient, ties to even.
-__device__ __forceinline__ float ckpt_code(float x, float inv) {
-    return fminf(fmaxf(__builtin_rintf(x * inv), -127.0f), 127.0f);
+// Codes of eight values of a group with exponent byte `byte`.  The
+// multiply-add rounds the exact x * 2^-E once, to a whole number; a byte of
+// 248 may stand for a group beyond 127 steps.
+__device__ __forceinline__ u32x2 ckpt_codes(const float (&v)[8], uint32_t byte) {
+    const float inv = __uint_as_float((254u - min(byte, 253u)) << 23);
+    const float most = 127.0f * ckpt_step(min(byte, 248u));
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = __builtin_fmaf(fminf(fmaxf(v[i], -most), most), inv, kWhole);
+    const bool nan = byte == kCkptNaN;
+    return u32x2{nan ? 0u : low_bytes(s[0], s[1], s[2], s[3]), nan ? 0u : low_bytes(s[4], s[5], s[6], s[7])};
+}
+
+// Byte i of a word as a signed code (one conversion instruction).
+__device__ __forceinline__ float code_of(uint32_t word, int i) { return (float)(int8_t)(word >> (8 * i)); }
+
+// Eight codes times their step, exactly.  A step of infinity (byte 255) with
+// its codes 0 gives NaN.
+__device__ __forceinline__ void ckpt_values(u32x2 codes, uint32_t byte, float (&v)[8]) {
+    const float step = ckpt_step(byte);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = code_of(codes[i >> 2], i & 3) * step;
 }
 
 // Maximum over aligned groups of four lanes (8 values each: one group).

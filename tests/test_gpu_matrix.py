@@ -406,6 +406,24 @@ def test_wgrad_fp32_pieces(qc, rows, n, dim):
     assert np.all(np.abs(got.double().numpy() - want) <= 4 * U32 * np.abs(want) + 2.0 ** -126)
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("n", [3, 16])
+def test_wgrad_every_step(qc, n, dtype):
+    """One token a channel and a power of two: dW holds what the checkpoint
+    stands for, from the largest step to the smallest, exactly (results below
+    the smallest normal number may come out as zero)."""
+    x = ref.hard_rows(96, dtype)[:14]  # the finite ones
+    dy = torch.zeros((14, n), dtype=dtype)
+    for first in range(0, 14, n):
+        dy.zero_()
+        k = min(n, 14 - first)
+        dy[torch.arange(first, first + k), torch.arange(k)] = 2.0 ** -3
+        got, v = run_wgrad(qc, dy, x)
+        want = v[first: first + k] / 8
+        off = np.abs(got[:k].double().numpy() - want)
+        assert np.all(off <= np.where(np.abs(want) < 2.0 ** -125, np.abs(want), 0.0)), off.max()
+
+
 def test_wgrad_is_the_gradient(qc):
     """Against differences of sum(dy * (X W^T)), X as held."""
     rows, n, dim = 90, 12, 40
