@@ -147,8 +147,9 @@ def _stream(stream):
             import torch
 
             # without the Stream object that torch.cuda.current_stream() makes (2.7 us a call)
-            get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-            _raw_stream = ((lambda: get(torch.cuda.current_device())) if get else
+            get, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+            torch.cuda.init()
+            _raw_stream = ((lambda: get(device())) if get and device else
                            (lambda: torch.cuda.current_stream().cuda_stream))
         return _raw_stream()
     if isinstance(stream, int):
@@ -440,12 +441,14 @@ def _mat(t, rows, cols, ld, esize, name):
         return None
     if isinstance(t, int):
         return t
+    s = t.shape
+    if (len(s) == 2 and t.is_cuda and t.stride() == (ld, 1) and s[0] >= rows and s[1] >= cols
+            and t.element_size() == esize):
+        return t.data_ptr()  # the common case; what follows finds out what is wrong, or that nothing is
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if t.element_size() != esize:
         raise ValueError(f"{name} has elements of {t.element_size()} bytes, the call takes {esize}")
-    if t.dim() == 2 and t.stride() == (ld, 1) and t.shape[0] >= rows and t.shape[1] >= cols:
-        return t.data_ptr()  # the common case; the rest finds out what is wrong, or that nothing is
     if t.dim() > 2 and not t.is_contiguous():
         raise ValueError(f"{name} must be a matrix, or contiguous")
     if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:

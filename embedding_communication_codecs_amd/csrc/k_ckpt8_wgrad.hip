@@ -262,31 +262,24 @@ k_ckpt8_wgrad(Args g) {
     store_dw<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16);
 }
 
-// The same of four neighbours, packed: word 0 holds values 0 and 1.
+// The same of four neighbours, packed (word 0 holds values 0 and 1), without
+// a branch.
 __device__ __forceinline__ void pieces4(f32x4 x, u32x2 (&q)[3]) {
-    uint32_t b[4], most = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        b[e] = __float_as_uint(x[e]);
-        most = umax(most, b[e] & 0x7FFFFFFFu);
-    }
-    if (__builtin_expect(__any(most >= kInfBits), 0)) {
-        uint32_t p[4][3];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) pieces(x[e], p[e]);
-#pragma unroll
-        for (int i = 0; i < 3; ++i) q[i] = u32x2{p[0][i] | (p[1][i] << 16), p[2][i] | (p[3][i] << 16)};
-        return;
-    }
     auto upper = [](uint32_t lo, uint32_t hi) { return __builtin_amdgcn_perm(hi, lo, 0x07060302u); };
+    uint32_t b[4];
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-        q[i] = u32x2{upper(b[0], b[1]), upper(b[2], b[3])};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            x[e] = x[e] - __uint_as_float(b[e] & 0xFFFF0000u);
+            if (i == 0) {
+                x[e] = __builtin_canonicalizef(x[e]);  // a NaN's upper half is a NaN then
+            } else {
+                const float r = x[e] - __uint_as_float(b[e] & 0xFFFF0000u);
+                x[e] = i > 1 || __builtin_isfinite(x[e]) ? r : 0.0f;  // an infinity is its first piece alone
+            }
             b[e] = __float_as_uint(x[e]);
         }
+        q[i] = u32x2{upper(b[0], b[1]), upper(b[2], b[3])};
     }
 }
 
@@ -529,11 +522,11 @@ k_ckpt8_wgrad_pipe_f32(Args g) {
     constexpr int FN = BN / WN / 16, FD = BD / WD / 16;
     constexpr int YB = BN * 2, XB = BD * 2, YT = ST * YB, XT = ST * XB;
     constexpr int YN = ST * BN * 4 / 1024 / NW;    // loads of dY a wave and stage
-    constexpr int XL = ST * BD / 16 / NW;          // lanes of a wave that load 16 codes of X
+    constexpr int XN = ST * BD / 256 / NW;         // and of X's codes (4 a lane)
     constexpr int TPW = ST / NW;                   // tokens of X a wave converts
-    constexpr int LOADS = YN + 2;
-    constexpr int RAW = YN * 1024 + XL * 16 + 256;  // a wave's loads of a stage
-    static_assert(BN == 128 && BD == 128 && XL == 32 && TPW * NW == ST && YN >= 1, "tile shape");
+    constexpr int LOADS = YN + XN + 1;
+    constexpr int RAW = YN * 1024 + XN * 256 + 256;  // a wave's loads of a stage: dY, codes, exponents
+    static_assert(BN == 128 && BD == 128 && XN == 2 && TPW * NW == ST && YN == 2 && FN == 4, "tile shape");
     constexpr int BUF = 3 * YT + XT, RAT = 2 * BUF;  // LDS: two buffers of tiles, four raw stages
     __shared__ __align__(1024) uint8_t lds[RAT + 4 * NW * RAW];
 
@@ -556,79 +549,94 @@ k_ckpt8_wgrad_pipe_f32(Args g) {
     const int yc = l & 31;                          // this lane's piece of a token
     const int ycol = (int)min(n0 + yc * 4, last_piece);
     const int yover = max(ycol + 4 - (int)g.n, 0);  // values of it past n
-    const int lxt = w * TPW + l / (BD / 16);        // the token of X this lane loads (lanes below XL)
-    const int xcol = (int)min(d0 + (l % (BD / 16)) * 16, g.pitch - 16);
-    const int ext = w * TPW + l / (WAVE / TPW);     // and the token whose exponents it loads
+    const int xd = l % 32 * 4, xcol = (int)min(d0 + xd, g.pitch - 4);  // this lane's codes of X, in each load
     const int ecol = (int)min(d0 / 32, g.epitch - 4);
     auto token_y = [&](int i) { return (w * YN + i) * 2 + (l >> 5); };
-    int yoff[YN];
+    auto token_x = [&](int i) { return w * TPW + i * 2 + (l >> 5); };
+    const int token_e = w * TPW + (l >> 4);  // the token whose exponents this lane loads
+    int yoff[YN], xoff[XN];
 #pragma unroll
     for (int i = 0; i < YN; ++i) yoff[i] = (token_y(i) * (int)g.ldy + ycol) * 4;
-    const int xoff = lxt * (int)g.pitch + xcol, eoff = ext * (int)g.epitch + ecol;
+#pragma unroll
+    for (int i = 0; i < XN; ++i) xoff[i] = token_x(i) * (int)g.pitch + xcol;
+    const int eoff = token_e * (int)g.epitch + ecol;
     // how many tokens a stage has (all of them but in the last one)
     auto tokens_of = [&](int s) { return (int)min(tokens - (int64_t)s * ST, (int64_t)ST); };
-    auto load = [&](int part, int s) {  // one of the LOADS of a stage
+    // FAST, here and below: the stage is whole and not the matrix's last rows
+    auto load = [&](auto fast, int part, int s) {  // one of the LOADS of a stage
+        constexpr bool FAST = decltype(fast)::value;
         const int64_t t0 = (int64_t)s * ST;
-        const int have = tokens_of(s);
-        const bool all = have == ST && t_first + t0 + ST < g.rows;
+        const int have = FAST ? ST : tokens_of(s);
         const uint32_t at = lds0 + RAT + ((s & 3) * NW + w) * RAW;
         if (part < YN) {
             int off = yoff[part];
-            if (!all) {
+            if (!FAST) {
                 const int t = min(token_y(part), have - 1);
                 off = (t * (int)g.ldy + ycol - (t_first + t0 + t == g.rows - 1 ? yover : 0)) * 4;
             }
             load_lds16(buffer_of(ybase + t0 * g.ldy * 4, -1), at + part * 1024, off, 0);
-        } else if (part == YN) {
-            const int off = all ? xoff : min(lxt, have - 1) * (int)g.pitch + xcol;
-            if (l < XL) load_lds16(buffer_of(xbase + t0 * g.pitch, -1), at + YN * 1024, off, 0);
+        } else if (part < YN + XN) {
+            const int i = part - YN, off = FAST ? xoff[i] : min(token_x(i), have - 1) * (int)g.pitch + xcol;
+            load_lds4(buffer_of(xbase + t0 * g.pitch, -1), at + YN * 1024 + i * 256, off, 0);
         } else {
-            const int off = all ? eoff : min(ext, have - 1) * (int)g.epitch + ecol;
-            load_lds4(buffer_of(ebase + t0 * g.epitch, -1), at + YN * 1024 + XL * 16, off, 0);
+            const int off = FAST ? eoff : min(token_e, have - 1) * (int)g.epitch + ecol;
+            load_lds4(buffer_of(ebase + t0 * g.epitch, -1), at + YN * 1024 + XN * 256, off, 0);
         }
     };
-    auto load_all = [&](int s) {
+    auto load_all = [&](auto fast, int s) {
 #pragma unroll
-        for (int part = 0; part < LOADS; ++part) load(part, s);
+        for (int part = 0; part < LOADS; ++part) load(fast, part, s);
     };
 
-    // ---- conversion of a stage by the wave that loaded it; every lane has a
-    // piece of dY a load, and 8 codes of X
-    const int cxt = l / (BD / 8), cxp = l % (BD / 8);
-    auto convert = [&](int part, int s) {
+    // ---- conversion of a stage by the wave that loaded it: of each load of
+    // dY four values a lane, of each of X four codes
+    f32x4 raw_y[YN];
+    uint32_t raw_x[XN], raw_e[XN];
+    auto read_raw = [&](int s) {
         const uint8_t* at = lds + RAT + ((s & 3) * NW + w) * RAW;
-        uint8_t* to = lds + (s & 1) * BUF;
-        if (part < YN) {
-            f32x4 r = *reinterpret_cast<const f32x4*>(at + part * 1024 + l * 16);
-            const int t = token_y(part);
-            if (s == stages - 1) {  // tokens past the end, and the last row's short piece
-                const int have = tokens_of(s), up = t_first + tokens == g.rows && t == have - 1 ? yover : 0;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float v = 0.0f;
+        for (int i = 0; i < YN; ++i) raw_y[i] = *reinterpret_cast<const f32x4*>(at + i * 1024 + l * 16);
 #pragma unroll
-                    for (int f = e; f < 4; ++f)
-                        if (f == e + up) v = r[f];
-                    r[e] = t < have ? v : 0.0f;
-                }
-            }
-            u32x2 q[3];
-            pieces4(r, q);
-            uint8_t* o = to + place(t, yc >> 1, YB) + 8 * (yc & 1);
-#pragma unroll
-            for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x2*>(o + p * YT) = q[p];
-        } else {
-            const u32x2 codes = *reinterpret_cast<const u32x2*>(at + YN * 1024 + l * 8);
-            const uint32_t e = *reinterpret_cast<const uint32_t*>(at + YN * 1024 + XL * 16 + l * 4);
-            const int t = w * TPW + cxt;
-            const bool live = t < tokens_of(s);
-            const float step = live ? ckpt_step((e >> (8 * (cxp >> 2))) & 0xFFu) : 0.0f;
-            const u32x2 a = held4(live ? codes.x : 0u, step), b = held4(live ? codes.y : 0u, step);
-            *reinterpret_cast<u32x4*>(to + 3 * YT + place(t, cxp, XB)) = u32x4{a.x, a.y, b.x, b.y};
+        for (int i = 0; i < XN; ++i) {
+            raw_x[i] = *reinterpret_cast<const uint32_t*>(at + YN * 1024 + i * 256 + l * 4);
+            // the exponents of this token's four groups are the lane's that loaded them
+            raw_e[i] = *reinterpret_cast<const uint32_t*>(at + YN * 1024 + XN * 256 + (token_x(i) - w * TPW) * 64);
         }
     };
+    auto convert_y = [&](auto fast, int i, int s) {
+        f32x4 r = raw_y[i];
+        const int t = token_y(i);
+        if (!decltype(fast)::value) {  // tokens past the end, and the last row's short piece
+            const int have = tokens_of(s);
+            const int up = t_first + (int64_t)s * ST + t == g.rows - 1 ? yover : 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float v = 0.0f;
+#pragma unroll
+                for (int f = e; f < 4; ++f)
+                    if (f == e + up) v = r[f];
+                r[e] = t < have ? v : 0.0f;
+            }
+        }
+        u32x2 q[3];
+        pieces4(r, q);
+        uint8_t* o = lds + (s & 1) * BUF + place(t, yc >> 1, YB) + 8 * (yc & 1);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x2*>(o + p * YT) = q[p];
+    };
+    auto convert_x = [&](auto fast, int i, int s) {
+        uint32_t codes = raw_x[i];
+        const int t = token_x(i);
+        float step = ckpt_step((raw_e[i] >> (8 * (xd >> 5))) & 0xFFu);
+        if (!decltype(fast)::value && t >= tokens_of(s)) {
+            codes = 0;
+            step = 0.0f;
+        }
+        *reinterpret_cast<u32x2*>(lds + (s & 1) * BUF + 3 * YT + place(t, xd >> 3, XB) + 2 * (xd & 4)) =
+            held4(codes, step);
+    };
 
-    const int fbase = (l >> 2) * YB + 8 * (l & 1);
+    const int fbase = (l >> 2) * YB + 8 * (l & 1), fx0 = 3 * YT;
     auto frag = [&](int at, int f) {
         typedef short s16x8 __attribute__((ext_vector_type(8)));
         const int o = at + fbase + (((f * 2 + ((l & 3) >> 1)) ^ (2 * ((l >> 2) & 7))) << 4);
@@ -638,43 +646,56 @@ k_ckpt8_wgrad_pipe_f32(Args g) {
     };
 
     f32x4 acc[FD][FN] = {};
-    if (stages > 0) {
-        load_all(0);
-        if (stages > 1) load_all(1);
-        if (stages > 2) load_all(2);
-        if (stages > 2) lds_landed_but<2 * LOADS>();
+    // Stage s is converted and this wave's loads of stage s + 1 have landed;
+    // every wave has read stage s - 1.  FAST: stages up to s + 3 are.
+    auto stage = [&](auto fast, int s) {
+        constexpr bool FAST = decltype(fast)::value;
+        if (FAST || s + 2 < stages) lds_landed_but<LOADS>();
         else lds_landed();
+        const int at = (s & 1) * BUF;
+        bf16x8 fx[FD], fy[2][FN];
+        if (FAST || s + 1 < stages) read_raw(s + 1);
 #pragma unroll
-        for (int part = 0; part <= YN; ++part) convert(part, 0);
-        for (int s = 0; s < stages; ++s) {
-            // stage s is converted and this wave's loads of stage s + 1 have
-            // landed; stage s - 1 has been read by every wave
-            if (s + 2 < stages) lds_landed_but<LOADS>();
-            else lds_landed();
-            const int at = (s & 1) * BUF;
-            bf16x8 fx[FD], fy[2][FN];
+        for (int i = 0; i < FD; ++i) fx[i] = frag(at + fx0, wd * FD + i);
 #pragma unroll
-            for (int i = 0; i < FD; ++i) fx[i] = frag(at + 3 * YT, wd * FD + i);
+        for (int j = 0; j < FN; ++j) fy[0][j] = frag(at, wn * FN + j);
+        if (FAST || s + 3 < stages) load_all(fast, s + 3);
 #pragma unroll
-            for (int j = 0; j < FN; ++j) fy[0][j] = frag(at, wn * FN + j);
-            if (s + 3 < stages) load_all(s + 3);
+        for (int p = 0; p < 3; ++p) {
+            if (p < 2) {
 #pragma unroll
-            for (int p = 0; p < 3; ++p) {
-                if (p < 2) {
+                for (int j = 0; j < FN; ++j) fy[(p + 1) & 1][j] = frag(at + (p + 1) * YT, wn * FN + j);
+            }
+            if (FAST || s + 1 < stages) {  // beside the products
+                if (p < YN) convert_y(fast, p, s + 1);
+                else {
 #pragma unroll
-                    for (int j = 0; j < FN; ++j) fy[(p + 1) & 1][j] = frag(at + (p + 1) * YT, wn * FN + j);
-                }
-#pragma unroll
-                for (int j = 0; j < FN; ++j)
-#pragma unroll
-                    for (int i = 0; i < FD; ++i)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[i], fy[p & 1][j], acc[i][j], 0, 0, 0);
-                if (s + 1 < stages) {  // beside the products
-#pragma unroll
-                    for (int part = p * (YN + 1) / 3; part < (p + 1) * (YN + 1) / 3; ++part) convert(part, s + 1);
+                    for (int i = 0; i < XN; ++i) convert_x(fast, i, s + 1);
                 }
             }
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int i = 0; i < FD; ++i)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[i], fy[p & 1][j], acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    if (stages > 0) {
+        load_all(std::false_type{}, 0);
+        if (stages > 1) load_all(std::false_type{}, 1);
+        if (stages > 2) load_all(std::false_type{}, 2);
+        if (stages > 2) lds_landed_but<2 * LOADS>();
+        else lds_landed();
+        read_raw(0);
+#pragma unroll
+        for (int i = 0; i < YN; ++i) convert_y(std::false_type{}, i, 0);
+#pragma unroll
+        for (int i = 0; i < XN; ++i) convert_x(std::false_type{}, i, 0);
+        int s = 0;
+        for (; s + 4 < stages; ++s) stage(std::true_type{}, s);
+#pragma unroll 1
+        for (; s < stages; ++s) stage(std::false_type{}, s);
     }
     store_dw<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16);
 }
@@ -716,7 +737,7 @@ struct Shape {
     float alone_us;  // stage_us when at most 256 blocks run, one a compute unit
 };
 constexpr Shape kBf16Shapes[] = {{128, 512, 0.75f, 4.0f, 0.45f}, {256, 256, 0.83f, 8.0f, 0.83f}};
-constexpr Shape kF32Shapes[] = {{128, 256, 1.2f, 4.0f, 1.2f}};
+constexpr Shape kF32Shapes[] = {{128, 256, 1.05f, 4.0f, 1.05f}};
 
 struct Plan {
     int tile;
