@@ -313,7 +313,7 @@ k_ckpt8_wgrad_pipe(Args g) {
     __shared__ __align__(1024) uint8_t lds[RAT + 4 * NW * RAW];
 
     const uint32_t tn = (uint32_t)((g.n + BN - 1) / BN), td = (uint32_t)((g.dim + BD - 1) / BD);
-    const Tile2 tile = tile_of<4>(blockIdx.x, tn, td);
+    const Tile2 tile = tile_of<8>(blockIdx.x, tn, td);
     const int64_t n0 = (int64_t)tile.x * BN, d0 = (int64_t)tile.y * BD;
     const int64_t t_first = (int64_t)blockIdx.y * g.rows_per_split;
     const int64_t tokens = min(g.rows - t_first, g.rows_per_split);
@@ -531,7 +531,7 @@ k_ckpt8_wgrad_pipe_f32(Args g) {
     __shared__ __align__(1024) uint8_t lds[RAT + 4 * NW * RAW];
 
     const uint32_t tn = (uint32_t)((g.n + BN - 1) / BN), td = (uint32_t)((g.dim + BD - 1) / BD);
-    const Tile2 tile = tile_of<4>(blockIdx.x, tn, td);
+    const Tile2 tile = tile_of<8>(blockIdx.x, tn, td);
     const int64_t n0 = (int64_t)tile.x * BN, d0 = (int64_t)tile.y * BD;
     const int64_t t_first = (int64_t)blockIdx.y * g.rows_per_split;
     const int64_t tokens = min(g.rows - t_first, g.rows_per_split);
@@ -752,9 +752,9 @@ Plan plan_of(int64_t rows, int64_t n, int64_t dim, bool bf16) {
     for (const Shape& s : kBf16Shapes) {
         const Shape& shape = bf16 ? s : kF32Shapes[0];
         const int64_t tiles = ((n + shape.tile - 1) / shape.tile) * ((dim + shape.tile - 1) / shape.tile);
-        for (int64_t want = 1; want <= 64 && want <= units; ++want) {
+        for (const int64_t want : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+            if (want > units) break;
             const int64_t per = (units + want - 1) / want, splits = (units + per - 1) / per;
-            if (splits != want) continue;
             const int64_t blocks = tiles * splits, rounds = (blocks + shape.slots - 1) / shape.slots;
             double us = (double)rounds * (2.0 * (double)per * (blocks <= 256 ? shape.alone_us : shape.stage_us) + shape.store_us);
             if (splits > 1) us += 2.5 + (double)(splits + 1) * (double)n * (double)dim * (4.0 / 6e6);

@@ -281,7 +281,8 @@ k_mm_int8_few(Args g, T* __restrict__ c) {
     constexpr int OWN = NB * SLAB > NT * MT * 1024 ? NB * SLAB : NT * MT * 1024;  // a wave's LDS: slabs, then sums
     __shared__ __align__(1024) uint8_t lds[WS * OWN];
     const int l = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id());
-    const int64_t n0 = (int64_t)blockIdx.x * (NT * 16), m0 = (int64_t)blockIdx.y * (MT * 16);
+    const uint32_t tn = (uint32_t)((g.n + NT * 16 - 1) / (NT * 16));
+    const int64_t n0 = (int64_t)(blockIdx.x % tn) * (NT * 16), m0 = (int64_t)(blockIdx.x / tn) * (MT * 16);
     const int padded = (g.k + 15) & ~15;
     Loader<NT * 16, K, 1> lb;
     Loader<MT * 16, K, 1> la;
@@ -361,8 +362,8 @@ k_mm_int8_few(Args g, T* __restrict__ c) {
 
 template <class T, int NT, int MT, int WS, int NB>
 hipError_t launch_few(const Args& g, T* c, hipStream_t stream) {
-    const dim3 grid((unsigned)((g.n + NT * 16 - 1) / (NT * 16)), (unsigned)((g.m + MT * 16 - 1) / (MT * 16)));
-    hipLaunchKernelGGL((k_mm_int8_few<T, NT, MT, WS, NB>), grid, dim3(WS * WAVE), 0, stream, g, c);
+    const int64_t tiles = ((g.n + NT * 16 - 1) / (NT * 16)) * ((g.m + MT * 16 - 1) / (MT * 16));
+    hipLaunchKernelGGL((k_mm_int8_few<T, NT, MT, WS, NB>), dim3((unsigned)tiles), dim3(WS * WAVE), 0, stream, g, c);
     return hipGetLastError();
 }
 

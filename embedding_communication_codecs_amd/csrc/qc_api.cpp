@@ -539,7 +539,7 @@ int qc_matmul_int8(const int8_t* a, const float* a_scale, int64_t lda, const int
     if (m == 0 || n == 0) return QC_OK;
     if (bad_matrix(m, n, ldc) || !a || !a_scale || !b || !b_scale || !c) return QC_ERR_ARG;
     if (k > 131071 || lda > kMaxProductStride || ldb > kMaxProductStride) return QC_ERR_UNSUPPORTED;
-    if (ceil_div(m, 64) > kMaxTiles / ceil_div(n, 16)) return QC_ERR_ARG;
+    if (ceil_div(m, 16) > kMaxTiles / ceil_div(n, 16)) return QC_ERR_ARG;
     if (misaligned(a) || misaligned(b) || misaligned4(a_scale) || misaligned4(b_scale) || misaligned_for(c, ctype))
         return QC_ERR_ALIGN;
     return launched(qc::launch_matmul_int8(a, a_scale, lda, b, b_scale, ldb, m, n, k, c, ctype == QC_BF16, ldc,

@@ -12,7 +12,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, in
 // 16 i.  Written as asm because the compiler takes every LDS access after
 // the builtin as dependent on it and waits for the load before the next
 // fragment read; it returns nothing in registers, and lds_landed() is the
-// wait that its readers need.
+// wait that its readers need.  (m0 is a reserved register: the compiler sets it
+// right before each use of its own.)
 __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds, int voff, int soff) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :

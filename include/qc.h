@@ -616,7 +616,7 @@ int qc_decode_ckpt8(const int8_t* codes, const uint8_t* exps, int64_t rows, int6
  *               blocks, whose sums are held there until they are joined.
  * Errors: ARG (NULL pointer, bad type, rows or n < 0, dim < 1, a stride below
  *         its row, too little workspace), ALIGN, UNSUPPORTED (accumulate with
- *         a bf16 dw, a stride above its limit).
+ *         a bf16 dw, ldy or dim above 2^23).
  */
 int64_t qc_ckpt8_wgrad_workspace(int64_t rows, int64_t n, int64_t dim, int32_t dytype);
 int qc_ckpt8_wgrad(const void* dy, int32_t dytype, int64_t ldy, const int8_t* codes, const uint8_t* exps,

@@ -586,6 +586,38 @@ def test_streams_and_graph(qc, m, n, k):
         assert all(torch.equal(s[o].view(torch.uint8), eager[o].view(torch.uint8)) for o in OUT)
 
 
+@pytest.mark.parametrize("m,n", [(4200000, 3), (3, 1100000)])
+def test_matmul_many_tiles(qc, m, n):
+    """More tiles one way than a grid has in its second dimension."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    a = torch.randint(-127, 128, (m, 16), device="cuda", generator=g, dtype=torch.int8)
+    b = torch.randint(-127, 128, (n, 16), device="cuda", generator=g, dtype=torch.int8)
+    c = torch.empty((m, n), device="cuda")
+    one = torch.ones(max(m, n), device="cuda")
+    qc.qc_matmul_int8(a, one, 16, b, one, 16, m, n, 16, c, qc.QC_F32, n)
+    assert torch.equal(c, a.float() @ b.float().t())  # sums below 2^24: exact
+
+
+def test_rows_past_the_grid(qc):
+    """More rows than blocks of one launch."""
+    rows = 4400000
+    x = torch.randn((rows, 8), device="cuda").to(BF16)
+    q, s = torch.empty((rows, 16), dtype=torch.int8, device="cuda"), torch.empty(rows, device="cuda")
+    c, e = torch.empty((rows, 32), dtype=torch.int8, device="cuda"), torch.empty((rows, 4), dtype=torch.uint8, device="cuda")
+    y = torch.empty_like(x)
+    qc.qc_encode_int8_rowwise(x, qc.QC_BF16, rows, 8, 8, q, 16, s)
+    qc.qc_encode_ckpt8(x, qc.QC_BF16, rows, 8, 8, c, e)
+    qc.qc_decode_ckpt8(c, e, rows, 8, y, qc.QC_BF16, 8)
+    torch.cuda.synchronize()
+    for at in (0, 1048570, 4194300, rows - 50):
+        part = x[at: at + 50].cpu()
+        wq, ws = ref.int8_rows(part)
+        wc, we = ref.ckpt8(part)
+        assert np.array_equal(q[at: at + 50, :8].cpu().numpy(), wq) and same(s[at: at + 50].cpu().numpy(), ws)
+        assert np.array_equal(c[at: at + 50].cpu().numpy(), wc) and np.array_equal(e[at: at + 50].cpu().numpy(), we)
+        assert same(y[at: at + 50].cpu().double().numpy(), ref.held(wc, we, 8))
+
+
 def test_offsets_past_32_bits(qc):
     """Row strides that put the last rows past 2^31 elements."""
     rows, ld, cols = 70000, 32768, 40

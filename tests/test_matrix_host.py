@@ -86,7 +86,7 @@ REFUSED = [
     *[("qc_matmul_int8", matmul, kw, st) for kw, st in [
         (dict(a=None), ARG), (dict(sa=None), ARG), (dict(b=None), ARG), (dict(sb=None), ARG), (dict(c=None), ARG),
         (dict(t=5), ARG), (dict(m=-1), ARG), (dict(n=-1), ARG), (dict(k=0), ARG), (dict(k=-2), ARG),
-        (dict(lda=32), ARG), (dict(ldb=40), ARG), (dict(ldc=4), ARG), (dict(m=1 << 50), ARG),
+        (dict(lda=32), ARG), (dict(ldb=40), ARG), (dict(ldc=4), ARG), (dict(m=1 << 50), ARG), (dict(m=1 << 36), ARG),
         (dict(k=131072, lda=131072, ldb=131072), UNSUP), (dict(lda=(1 << 23) + 16), UNSUP),
         (dict(ldb=(1 << 23) + 16), UNSUP), (dict(a=A + 4), ALIGN), (dict(b=A + 8), ALIGN), (dict(sa=A + 1), ALIGN),
         (dict(sb=A + 2), ALIGN), (dict(c=A + 1), ALIGN), (dict(c=A + 2, t=0), ALIGN),
@@ -104,7 +104,8 @@ REFUSED = [
         (dict(dy=None), ARG), (dict(codes=None), ARG), (dict(exps=None), ARG), (dict(dw=None), ARG), (dict(t=3), ARG),
         (dict(wt=3), ARG), (dict(rows=-1), ARG), (dict(n=-1), ARG), (dict(dim=0), ARG), (dict(ldy=4), ARG),
         (dict(ldw=39), ARG), (dict(rows=BIG), ARG), (dict(n=BIG), ARG), (dict(dim=BIG, ldw=BIG), ARG),
-        (dict(wt=1, acc=1), UNSUP), (dict(ldy=(1 << 23) + 8), UNSUP), (dict(dy=A + 1), ALIGN),
+        (dict(wt=1, acc=1), UNSUP), (dict(ldy=(1 << 23) + 8), UNSUP),
+        (dict(dim=(1 << 23) + 32, ldw=(1 << 23) + 32), UNSUP), (dict(dy=A + 1), ALIGN),
         (dict(dw=A + 2), ALIGN), (dict(codes=A + 8), ALIGN), (dict(exps=A + 8), ALIGN),
         (dict(rows=1 << 16), ARG), (dict(rows=1 << 16, ws=A, wb=16), ARG),  # too little workspace
         (dict(rows=1 << 16, ws=A + 8, wb=1 << 40), ALIGN),
