@@ -24,7 +24,8 @@ struct Args {
     int64_t m, n;
     int32_t k;
     int64_t ldc;
-    bool wide;  // rows of C start at multiples of four elements
+    bool wide;   // rows of C start at multiples of four elements
+    bool lines;  // and at multiples of 16 bytes
 };
 
 // C = (sum * sa) * sb: the scales are applied one after the other, so that
@@ -243,6 +244,37 @@ k_mm_int8_pipe(Args g, T* __restrict__ c) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) sb[i][e] = g.sb[min(col + e, g.n - 1)];
     }
+    if (g.lines && n0 + BN <= g.n && m0 + BM <= g.m) {
+        // 16 tokens at a time through the wave's part of LDS, so that a store
+        // takes whole pieces of a few rows of C, not eight bytes of 16 (4096 x
+        // 4096 x 128: 11.5 us against 15.0; 16384 x 8192 x 8192 827 against
+        // 851).  Piece p of row r in slot p ^ r.
+        constexpr int RB = FN * 16 * (int)sizeof(T), PR = RB / 16;
+        static_assert((PR & (PR - 1)) == 0 && PR <= WAVE && NW * 16 * RB <= 2 * STAGE, "a wave's part of LDS");
+        __syncthreads();  // every wave has read its last fragments
+        uint8_t* own = lds + w * (16 * RB);
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+#pragma unroll
+            for (int i = 0; i < FN; ++i) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = scaled(acc[i][j][e], sa[j], sb[i][e]);
+                const int at = (i * 16 + 4 * (l >> 4)) * (int)sizeof(T), r = l & 15;
+                store4(reinterpret_cast<T*>(own + r * RB + (((at >> 4) ^ (r & (PR - 1))) << 4) + (at & 15)), 4, v, true);
+            }
+            wave_lds_sync();
+            T* cj = c + (m0 + (wm * FM + j) * 16) * g.ldc + n0 + wn * FN * 16;
+#pragma unroll
+            for (int q = 0; q < RB / 64; ++q) {
+                const int r = (q * WAVE + l) / PR, p = (q * WAVE + l) % PR;
+                *reinterpret_cast<u32x4*>(cj + r * g.ldc + p * (16 / (int)sizeof(T))) =
+                    *reinterpret_cast<const u32x4*>(own + r * RB + ((p ^ (r & (PR - 1))) << 4));
+            }
+            wave_lds_sync();
+        }
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
         const int64_t row = m0 + (wm * FM + j) * 16 + (l & 15);
@@ -370,29 +402,32 @@ hipError_t launch_few(const Args& g, T* c, hipStream_t stream) {
 // Which tile: the one whose rounds of blocks over the 256 compute units take
 // the least time.  `round_us` is the measured time of one full round at k =
 // 4096 without the launch itself (2 us); all grow with k alike.  Against the
-// next best shape, whole calls, weights from HBM, at n = k = 4096:
-//   m    1: 16 x 16 5.5 us (32 x 16 8.7)     m  16 (n 16384): 32 x 16 16.1 (16 x 16 18.5)
-//   m   32: 16 x 32 7.6 (32 x 32 9.0)        m  61: 32 x 32 8.5 (16 x 64 9.5)
-//   m  128: 32 x 64 9.7 (32 x 32 13.3)       m 256: 64 x 64 14.4 (32 x 64 15.5)
-//   m  512: 128 x 64 19.5 (128 x 128 24.7)   m 1024: 128 x 128, 256 bytes of k 25.0 (128 bytes 30.1)
-//   m 2048: 128 x 128, 128 bytes of k 45.3 (256 x 256 53.5)  m 4096: 256 x 256 58.7 (128 x 128 79.7)
+// next best shape, whole calls, weights from HBM, at n = k = 4096 (16384
+// where it says so):
+//   m    1: 16 x 16 5.6 us (32 x 16 6.2)     m  16 (16384): 32 x 16 13.5 (32 x 32 15.5)
+//   m   32: 32 x 16 6.7 (32 x 32 8.4)        m  32 (16384): 32 x 32 16.4 (32 x 64 17.1)
+//   m   61: 32 x 32 8.4 (32 x 64 9.8)        m  61 (16384): 64 x 64 18.4 (32 x 64 18.9)
+//   m  128: 32 x 64 9.6 (32 x 32 13.1)       m 256: 64 x 64 14.4 (32 x 64 15.6)
+//   m  512: 128 x 64 19.3 (128 x 128 24.0)   m 1024: 128 x 128, 256 bytes of k 25.9 (128 bytes 29.6)
+//   m 2048: 128 x 128, 128 bytes of k 39.3 (256 bytes 47.6)  m 4096: 256 x 256 55.9 (128 x 128 76.3)
 struct Shape {
     int bn, bm, slots;  // channels, tokens, blocks at work at one time
     float round_us;
 };
 constexpr Shape kShapes[] = {
-    {16, 16, 256, 4.0f},  {32, 16, 256, 6.8f},   {16, 32, 256, 5.4f},   {32, 32, 256, 6.5f},    {32, 64, 256, 7.2f},
-    {64, 64, 256, 12.0f}, {128, 64, 256, 17.6f}, {128, 128, 256, 22.8f}, {128, 128, 512, 43.0f}, {256, 256, 256, 51.0f},
+    {16, 16, 256, 4.0f},  {32, 16, 256, 4.7f},   {32, 32, 256, 6.5f},    {32, 64, 256, 7.2f},
+    {64, 64, 256, 12.0f}, {128, 64, 256, 17.6f}, {128, 128, 256, 22.8f}, {128, 128, 512, 38.0f}, {256, 256, 256, 51.0f},
 };
 
 int shape_of(int64_t m, int64_t n) {
-    int best = 0;
-    double least = 0;
-    for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); ++i) {
+    constexpr int kAll = sizeof(kShapes) / sizeof(kShapes[0]);
+    int best = kAll - 1;
+    double least = 1e300;
+    for (int i = 0; i < kAll; ++i) {
         const Shape& s = kShapes[i];
         const int64_t blocks = ((n + s.bn - 1) / s.bn) * ((m + s.bm - 1) / s.bm);
         const double us = (double)((blocks + s.slots - 1) / s.slots) * s.round_us;
-        if (i == 0 || us < least) {
+        if (us < least && blocks < int64_t(1) << 23) {  // a grid has fewer than 2^32 threads
             best = i;
             least = us;
         }
@@ -405,13 +440,12 @@ hipError_t launch(const Args& g, T* c, hipStream_t stream) {
     switch (shape_of(g.m, g.n)) {
         case 0: return launch_few<T, 1, 1, 8, 2>(g, c, stream);
         case 1: return launch_few<T, 2, 1, 6, 2>(g, c, stream);
-        case 2: return launch_few<T, 1, 2, 8, 1>(g, c, stream);
-        case 3: return launch_few<T, 2, 2, 8, 1>(g, c, stream);
-        case 4: return launch_few<T, 2, 4, 6, 1>(g, c, stream);
-        case 5: return launch_few<T, 4, 4, 4, 1>(g, c, stream);
-        case 6: return launch_pipe<T, 128, 64, 2, 2, 256>(g, c, stream);
-        case 7: return launch_pipe<T, 128, 128, 2, 2, 256>(g, c, stream);
-        case 8: return launch_pipe<T, 128, 128, 2, 2, 128>(g, c, stream);
+        case 2: return launch_few<T, 2, 2, 8, 1>(g, c, stream);
+        case 3: return launch_few<T, 2, 4, 6, 1>(g, c, stream);
+        case 4: return launch_few<T, 4, 4, 4, 1>(g, c, stream);
+        case 5: return launch_pipe<T, 128, 64, 2, 2, 256>(g, c, stream);
+        case 6: return launch_pipe<T, 128, 128, 2, 2, 256>(g, c, stream);
+        case 7: return launch_pipe<T, 128, 128, 2, 2, 128>(g, c, stream);
         default: return launch_pipe<T, 256, 256, 2, 4, 128>(g, c, stream);
     }
 }
@@ -422,7 +456,8 @@ hipError_t launch_matmul_int8(const void* a, const float* a_scale, int64_t lda, 
                               int64_t ldb, int64_t m, int64_t n, int64_t k, void* c, bool bf16, int64_t ldc,
                               hipStream_t stream) {
     const Args g{static_cast<const uint8_t*>(a), a_scale, lda, static_cast<const uint8_t*>(b), b_scale, ldb, m, n,
-                 (int32_t)k, ldc, ldc % 4 == 0 && reinterpret_cast<uintptr_t>(c) % (bf16 ? 8 : 16) == 0};
+                 (int32_t)k, ldc, ldc % 4 == 0 && reinterpret_cast<uintptr_t>(c) % (bf16 ? 8 : 16) == 0,
+                 ldc % (bf16 ? 8 : 4) == 0 && reinterpret_cast<uintptr_t>(c) % 16 == 0};
     return bf16 ? launch(g, static_cast<BF16*>(c), stream) : launch(g, static_cast<float*>(c), stream);
 }
 

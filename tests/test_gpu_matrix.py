@@ -204,6 +204,24 @@ def test_matmul_large_tiles_long_k(qc, m, n, k):
     assert torch.equal(c.get(), want)
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("more,skip", [(0, 0), (8, 0), (4, 0), (3, 0), (8, 2)])
+@pytest.mark.parametrize("m,n,k", [(500, 4000, 300), (1000, 4000, 260), (2000, 4000, 130), (3700, 3400, 70)])
+def test_matmul_tile_stores(qc, m, n, k, more, skip, dtype):
+    """Whole tiles of C at every alignment of its rows, each row and column
+    with a scale of its own (powers of two, so fp32 is exact)."""
+    a, b = codes_of(m, k, 31), codes_of(n, k, 32)
+    sa = torch.exp2((torch.arange(m) % 7).float())
+    sb = torch.exp2(-(torch.arange(n) % 11).float())
+    c = Buf(m, n, n + more, dtype, skip)
+    kp = ref.up(k, 16)
+    qc.qc_matmul_int8(strided(a, kp), sa.cuda(), kp, strided(b, kp), sb.cuda(), kp, m, n, k, c.t, qt(qc, dtype), n + more)
+    torch.cuda.synchronize()
+    c.check()
+    sums = torch.from_numpy(a.numpy().astype(np.float32) @ b.numpy().astype(np.float32).T)
+    assert torch.equal(c.get(), ((sums * sa[:, None]) * sb[None, :]).to(dtype))
+
+
 @pytest.mark.parametrize("m,n,k,lda,ldb,ldc,skip", [(5, 40, 100, 128, 160, 43, 1), (40, 70, 333, 352, 336, 71, 3),
                                                      (200, 130, 77, 96, 80, 132, 2), (300, 300, 300, 320, 304, 304, 0)])
 def test_matmul_strides(qc, m, n, k, lda, ldb, ldc, skip):
