@@ -7,9 +7,15 @@
 // fp32 sums.  A bf16 dY goes in as it is too; an fp32 dY as three bf16
 // pieces of 8 mantissa bits each, which add up to it exactly.
 //
-// Both operands are summed over their slow axis.  Tiles of 64 tokens lie
-// in LDS as [token][channel] and are read with ds_read_b64_tr_b16, which
-// hands each lane four tokens of one channel.
+// Both operands are summed over their slow axis.  Tiles of 32 tokens (64 in
+// the simple kernel) lie in LDS as [token][channel] and are read with
+// ds_read_b64_tr_b16, which hands each lane four tokens of one channel.
+//
+// Large products are bound by the matrix cores, which this power budget runs
+// at 1.85-1.97 PFLOP/s on random bf16 values, and by LDS, which the same waves
+// use to convert X beside them: 16384 x 4096 x 8192 (tokens, n, dim) 870 us,
+// 1.26 PFLOP/s; 4096 x 4096 x 4096 117 us, 1.17.  Small ones by the latency of
+// their few stages and of a second launch that joins the splits.
 #include "qc_lds.hpp"
 #include "qc_launch.hpp"
 
@@ -284,8 +290,9 @@ __device__ __forceinline__ void pieces4(f32x4 x, u32x2 (&q)[3]) {
 }
 
 // --------------------------------------------------------------- pipelined
-// bf16 gradients, n at least 8.  One block computes BN output x BD input channels with WN x WD waves, in stages of 32
-// tokens.  Everything is loaded straight into LDS, two stages before its use:
+// bf16 gradients, n at least 8.  One block computes BN output x BD input
+// channels with WN x WD waves, in stages of 32 tokens.  Everything is loaded
+// straight into LDS, two stages before its use:
 // dY as it is, X as codes and exponent words.  Each lane's 16 codes and their
 // exponents land in a place of its own, so the lane converts them to bf16 as
 // soon as its own wave's loads have landed and writes them to X's tile, which
@@ -514,21 +521,30 @@ k_ckpt8_wgrad_pipe(Args g) {
 // The same for fp32 gradients, n at least 4: each wave's part of dY lands in
 // a place of its own too, and is taken apart into its three bf16 pieces, a
 // tile each, when X is converted.  The three products of a step share X's
-// fragments.  A batch holds dY and X of one stage.
-template <int BN, int BD, int WN, int WD>
-__global__ void __launch_bounds__(WN * WD * WAVE)
+// fragments.
+//
+// A stage is three parts, a product with one piece of dY each, of FN steps.
+// The barrier stands before the third part, whose fragments are in registers
+// by then: every wave has read the stage's tiles, so the stage after next may
+// be converted over them, and the next one is whole.  With the barrier and the
+// first fragments at a stage's start, 4096 x 4096 x 4096 took 575 us; so it
+// takes 500 with tiles of 128 x 128 and 347 with 128 x 256, which read and
+// convert less of dY, the wider operand, for a product: three of them, at
+// 1.19 PFLOP/s.
+template <int BD>
+__global__ void __launch_bounds__(512)
 k_ckpt8_wgrad_pipe_f32(Args g) {
-    constexpr int NW = WN * WD;
-    constexpr int FN = BN / WN / 16, FD = BD / WD / 16;
+    constexpr int BN = 128, NW = 8, WN = 2, FN = 4, FD = BD / 64;
     constexpr int YB = BN * 2, XB = BD * 2, YT = ST * YB, XT = ST * XB;
-    constexpr int YN = ST * BN * 4 / 1024 / NW;    // loads of dY a wave and stage
-    constexpr int XN = ST * BD / 256 / NW;         // and of X's codes (4 a lane)
-    constexpr int TPW = ST / NW;                   // tokens of X a wave converts
-    constexpr int LOADS = YN + XN + 1;
-    constexpr int RAW = YN * 1024 + XN * 256 + 256;  // a wave's loads of a stage: dY, codes, exponents
-    static_assert(BN == 128 && BD == 128 && XN == 2 && TPW * NW == ST && YN == 2 && FN == 4, "tile shape");
-    constexpr int BUF = 3 * YT + XT, RAT = 2 * BUF;  // LDS: two buffers of tiles, four raw stages
-    __shared__ __align__(1024) uint8_t lds[RAT + 4 * NW * RAW];
+    constexpr int YN = 2;                      // loads of dY a wave and stage
+    constexpr int LOADS = YN + 2;              // and X's codes and exponents
+    constexpr int TOK = 1024 / BD;             // tokens of X a wave loads
+    constexpr int XW = ST / TOK;               // waves that load different ones
+    constexpr int XH = BD / 128;               // pieces of 8 codes that a lane converts, of the 16 it loads
+    constexpr int RAW = YN * 1024 + 1024 + 256;  // a wave's loads of a stage
+    static_assert(YN * 1024 * NW == ST * BN * 4 && NW * WAVE * 8 * XH == ST * BD, "tile shape");
+    constexpr int BUF = 3 * YT + XT, RAT = 2 * BUF;  // LDS: two buffers of tiles, three raw stages
+    __shared__ __align__(1024) uint8_t lds[RAT + 3 * NW * RAW];
 
     const uint32_t tn = (uint32_t)((g.n + BN - 1) / BN), td = (uint32_t)((g.dim + BD - 1) / BD);
     const Tile2 tile = tile_of<8>(blockIdx.x, tn, td);
@@ -549,25 +565,23 @@ k_ckpt8_wgrad_pipe_f32(Args g) {
     const int yc = l & 31;                          // this lane's piece of a token
     const int ycol = (int)min(n0 + yc * 4, last_piece);
     const int yover = max(ycol + 4 - (int)g.n, 0);  // values of it past n
-    const int xd = l % 32 * 4, xcol = (int)min(d0 + xd, g.pitch - 4);  // this lane's codes of X, in each load
-    const int ecol = (int)min(d0 / 32, g.epitch - 4);
     auto token_y = [&](int i) { return (w * YN + i) * 2 + (l >> 5); };
-    auto token_x = [&](int i) { return w * TPW + i * 2 + (l >> 5); };
-    const int token_e = w * TPW + (l >> 4);  // the token whose exponents this lane loads
-    int yoff[YN], xoff[XN];
+    const int xt = w % XW * TOK + l / (BD / 16), xq = l % (BD / 16);  // this lane's token of a stage, and 16 codes of it
+    const int xcol = (int)min(d0 + xq * 16, g.pitch - 16);
+    const int ecol = (int)min((d0 + xq * 16) / 128 * 4, g.epitch - 4);
+    int yoff[YN];
 #pragma unroll
     for (int i = 0; i < YN; ++i) yoff[i] = (token_y(i) * (int)g.ldy + ycol) * 4;
-#pragma unroll
-    for (int i = 0; i < XN; ++i) xoff[i] = token_x(i) * (int)g.pitch + xcol;
-    const int eoff = token_e * (int)g.epitch + ecol;
+    const int xoff = xt * (int)g.pitch + xcol, eoff = xt * (int)g.epitch + ecol;
     // how many tokens a stage has (all of them but in the last one)
     auto tokens_of = [&](int s) { return (int)min(tokens - (int64_t)s * ST, (int64_t)ST); };
-    // FAST, here and below: the stage is whole and not the matrix's last rows
-    auto load = [&](auto fast, int part, int s) {  // one of the LOADS of a stage
+    // FAST, here and below: the stage is whole and not the matrix's last rows.
+    // `slot`: the stage's number modulo 3.
+    auto load = [&](auto fast, int part, int s, int slot) {  // one of the LOADS of a stage
         constexpr bool FAST = decltype(fast)::value;
         const int64_t t0 = (int64_t)s * ST;
         const int have = FAST ? ST : tokens_of(s);
-        const uint32_t at = lds0 + RAT + ((s & 3) * NW + w) * RAW;
+        const uint32_t at = lds0 + RAT + (slot * NW + w) * RAW;
         if (part < YN) {
             int off = yoff[part];
             if (!FAST) {
@@ -575,35 +589,32 @@ k_ckpt8_wgrad_pipe_f32(Args g) {
                 off = (t * (int)g.ldy + ycol - (t_first + t0 + t == g.rows - 1 ? yover : 0)) * 4;
             }
             load_lds16(buffer_of(ybase + t0 * g.ldy * 4, -1), at + part * 1024, off, 0);
-        } else if (part < YN + XN) {
-            const int i = part - YN, off = FAST ? xoff[i] : min(token_x(i), have - 1) * (int)g.pitch + xcol;
-            load_lds4(buffer_of(xbase + t0 * g.pitch, -1), at + YN * 1024 + i * 256, off, 0);
+        } else if (part == YN) {
+            const int off = FAST ? xoff : min(xt, have - 1) * (int)g.pitch + xcol;
+            load_lds16(buffer_of(xbase + t0 * g.pitch, -1), at + YN * 1024, off, 0);
         } else {
-            const int off = FAST ? eoff : min(token_e, have - 1) * (int)g.epitch + ecol;
-            load_lds4(buffer_of(ebase + t0 * g.epitch, -1), at + YN * 1024 + XN * 256, off, 0);
+            const int off = FAST ? eoff : min(xt, have - 1) * (int)g.epitch + ecol;
+            load_lds4(buffer_of(ebase + t0 * g.epitch, -1), at + YN * 1024 + 1024, off, 0);
         }
     };
-    auto load_all = [&](auto fast, int s) {
+    auto load_all = [&](int s) {
 #pragma unroll
-        for (int part = 0; part < LOADS; ++part) load(fast, part, s);
+        for (int part = 0; part < LOADS; ++part) load(std::false_type{}, part, s, s % 3);
     };
 
     // ---- conversion of a stage by the wave that loaded it: of each load of
-    // dY four values a lane, of each of X four codes
+    // dY four values a lane, of X 8 * XH codes
     f32x4 raw_y[YN];
-    uint32_t raw_x[XN], raw_e[XN];
-    auto read_raw = [&](int s) {
-        const uint8_t* at = lds + RAT + ((s & 3) * NW + w) * RAW;
+    u32x4 raw_x;
+    uint32_t raw_e;
+    auto read_raw = [&](int slot) {
+        const uint8_t* at = lds + RAT + (slot * NW + w) * RAW;
 #pragma unroll
         for (int i = 0; i < YN; ++i) raw_y[i] = *reinterpret_cast<const f32x4*>(at + i * 1024 + l * 16);
-#pragma unroll
-        for (int i = 0; i < XN; ++i) {
-            raw_x[i] = *reinterpret_cast<const uint32_t*>(at + YN * 1024 + i * 256 + l * 4);
-            // the exponents of this token's four groups are the lane's that loaded them
-            raw_e[i] = *reinterpret_cast<const uint32_t*>(at + YN * 1024 + XN * 256 + (token_x(i) - w * TPW) * 64);
-        }
+        raw_x = *reinterpret_cast<const u32x4*>(at + YN * 1024 + l * 16);
+        raw_e = *reinterpret_cast<const uint32_t*>(at + YN * 1024 + 1024 + l * 4);
     };
-    auto convert_y = [&](auto fast, int i, int s) {
+    auto convert_y = [&](auto fast, int i, int s, int buf) {
         f32x4 r = raw_y[i];
         const int t = token_y(i);
         if (!decltype(fast)::value) {  // tokens past the end, and the last row's short piece
@@ -620,97 +631,157 @@ k_ckpt8_wgrad_pipe_f32(Args g) {
         }
         u32x2 q[3];
         pieces4(r, q);
-        uint8_t* o = lds + (s & 1) * BUF + place(t, yc >> 1, YB) + 8 * (yc & 1);
+        uint8_t* o = lds + buf * BUF + place(t, yc >> 1, YB) + 8 * (yc & 1);
 #pragma unroll
         for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x2*>(o + p * YT) = q[p];
     };
-    auto convert_x = [&](auto fast, int i, int s) {
-        uint32_t codes = raw_x[i];
-        const int t = token_x(i);
-        float step = ckpt_step((raw_e[i] >> (8 * (xd >> 5))) & 0xFFu);
-        if (!decltype(fast)::value && t >= tokens_of(s)) {
-            codes = 0;
+    // Where a lane has two pieces, the upper four of eight neighbouring lanes
+    // write their second one first: eight pieces in different banks either
+    // time.  Where it has one, the upper four waves have the second ones.
+    const bool second = XH == 2 ? (l & 4) != 0 : w >= XW;
+    const int xplace = place(xt, xq * 2 + second, XB);
+    auto convert_x = [&](auto fast, int h, int s, int buf) {
+        float step = ckpt_step((raw_e >> (8 * ((xq >> 1) & 3))) & 0xFFu);
+        u32x2 q = second != (h == 1) ? u32x2{raw_x.z, raw_x.w} : u32x2{raw_x.x, raw_x.y};
+        if (!decltype(fast)::value && xt >= tokens_of(s)) {
             step = 0.0f;
+            q = u32x2{0, 0};
         }
-        *reinterpret_cast<u32x2*>(lds + (s & 1) * BUF + 3 * YT + place(t, xd >> 3, XB) + 2 * (xd & 4)) =
-            held4(codes, step);
+        const u32x2 a = held4(q.x, step), b = held4(q.y, step);
+        *reinterpret_cast<u32x4*>(lds + buf * BUF + 3 * YT + (xplace ^ (16 * h))) = u32x4{a.x, a.y, b.x, b.y};
     };
 
-    const int fbase = (l >> 2) * YB + 8 * (l & 1), fx0 = 3 * YT;
-    auto frag = [&](int at, int f) {
+    auto frag_at = [&](int f, int row_bytes) { return place(l >> 2, f * 2 + ((l & 3) >> 1), row_bytes) + 8 * (l & 1); };
+    const int yf = frag_at(wn * FN, YB), xf = 3 * YT + frag_at(wd * FD, XB);
+    auto frag = [&](int at, int row_bytes) {
         typedef short s16x8 __attribute__((ext_vector_type(8)));
-        const int o = at + fbase + (((f * 2 + ((l & 3) >> 1)) ^ (2 * ((l >> 2) & 7))) << 4);
-        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(lds + o));
-        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(lds + o + 16 * YB));
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(lds + at));
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(lds + at + 16 * row_bytes));
         return __builtin_bit_cast(bf16x8, s16x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w});
     };
+    auto read_y = [&](int buf, int p, int j) { return frag(buf * BUF + p * YT + (yf ^ (j << 5)), YB); };
+    auto read_x = [&](int buf, int i) { return frag(buf * BUF + (xf ^ (i << 5)), XB); };
 
     f32x4 acc[FD][FN] = {};
-    // Stage s is converted and this wave's loads of stage s + 1 have landed;
-    // every wave has read stage s - 1.  FAST: stages up to s + 3 are.
-    auto stage = [&](auto fast, int s) {
+    bf16x8 fx[2][FD], fy[2][FN];
+    // Stage s, s = P modulo 2 and = rot modulo 3.  On entry its first
+    // fragments and the raw values of stage s + 1 are in registers, and the
+    // first part of dY's is converted.  FAST: the stages up to s + 4 are.
+    auto stage = [&](auto phase, auto fast, int s, int rot) {
+        constexpr int P = decltype(phase)::value;
         constexpr bool FAST = decltype(fast)::value;
-        if (FAST || s + 2 < stages) lds_landed_but<LOADS>();
-        else lds_landed();
-        const int at = (s & 1) * BUF;
-        bf16x8 fx[FD], fy[2][FN];
-        if (FAST || s + 1 < stages) read_raw(s + 1);
-#pragma unroll
-        for (int i = 0; i < FD; ++i) fx[i] = frag(at + fx0, wd * FD + i);
-#pragma unroll
-        for (int j = 0; j < FN; ++j) fy[0][j] = frag(at, wn * FN + j);
-        if (FAST || s + 3 < stages) load_all(fast, s + 3);
+        const int rot2 = rot == 0 ? 2 : rot - 1, rot1 = rot == 2 ? 0 : rot + 1;  // of s + 2; of s + 1 and s + 4
 #pragma unroll
         for (int p = 0; p < 3; ++p) {
-            if (p < 2) {
 #pragma unroll
-                for (int j = 0; j < FN; ++j) fy[(p + 1) & 1][j] = frag(at + (p + 1) * YT, wn * FN + j);
-            }
-            if (FAST || s + 1 < stages) {  // beside the products
-                if (p < YN) convert_y(fast, p, s + 1);
-                else {
+            for (int j = 0; j < FN; ++j) {
+                if (p < 2) {
+                    fy[(P + p + 1) & 1][j] = read_y(P, p + 1, j);
+                    if (FAST || s + 1 < stages) {
+                        if (p == 0 && j == 0) convert_y(fast, 1, s + 1, P ^ 1);
+                        if (p == 0 && j == 2) convert_x(fast, 0, s + 1, P ^ 1);
+                        if (p == 1 && j == 0 && XH == 2) convert_x(fast, 1, s + 1, P ^ 1);
+                    }
+                } else {
+                    if (j == 0) {
+                        if (FAST || s + 3 < stages) lds_landed_but<LOADS>();
+                        else lds_landed();
+                        if (FAST || s + 2 < stages) read_raw(rot2);
+                    }
+                    fy[(P + 1) & 1][j] = read_y(P ^ 1, 0, j);
 #pragma unroll
-                    for (int i = 0; i < XN; ++i) convert_x(fast, i, s + 1);
+                    for (int i = j * FD / FN; i < (j + 1) * FD / FN; ++i) fx[P ^ 1][i] = read_x(P ^ 1, i);
+                    if (j == 2 && (FAST || s + 2 < stages)) convert_y(fast, 0, s + 2, P);
+                    if (FAST || s + 4 < stages) load(fast, j, s + 4, rot1);
                 }
-            }
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
 #pragma unroll
                 for (int i = 0; i < FD; ++i)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[i], fy[p & 1][j], acc[i][j], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[P][i], fy[(P + p) & 1][j], acc[i][j], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);  // keeps the reads where they stand, ahead of their use
+            }
         }
     };
+    static_assert(LOADS == FN, "a load a step");
     if (stages > 0) {
-        load_all(std::false_type{}, 0);
-        if (stages > 1) load_all(std::false_type{}, 1);
-        if (stages > 2) load_all(std::false_type{}, 2);
+        load_all(0);
+        if (stages > 1) load_all(1);
+        if (stages > 2) load_all(2);
         if (stages > 2) lds_landed_but<2 * LOADS>();
         else lds_landed();
         read_raw(0);
 #pragma unroll
-        for (int i = 0; i < YN; ++i) convert_y(std::false_type{}, i, 0);
+        for (int i = 0; i < YN; ++i) convert_y(std::false_type{}, i, 0, 0);
 #pragma unroll
-        for (int i = 0; i < XN; ++i) convert_x(std::false_type{}, i, 0);
-        int s = 0;
-        for (; s + 4 < stages; ++s) stage(std::true_type{}, s);
+        for (int h = 0; h < XH; ++h) convert_x(std::false_type{}, h, 0, 0);
+        if (stages > 3) {
+            load_all(3);
+            lds_landed_but<2 * LOADS>();
+        } else {
+            lds_landed();
+        }
+        if (stages > 1) {
+            read_raw(1);
+            convert_y(std::false_type{}, 0, 1, 1);
+        }
+#pragma unroll
+        for (int i = 0; i < FD; ++i) fx[0][i] = read_x(0, i);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) fy[0][j] = read_y(0, 0, j);
+        using std::integral_constant;
+        int s = 0, rot = 0;
+        auto turn = [&] { rot = rot == 2 ? 0 : rot + 1; };
+        for (; s + 6 < stages; s += 2) {
+            stage(integral_constant<int, 0>{}, std::true_type{}, s, rot);
+            turn();
+            stage(integral_constant<int, 1>{}, std::true_type{}, s + 1, rot);
+            turn();
+        }
 #pragma unroll 1
-        for (; s < stages; ++s) stage(std::false_type{}, s);
+        for (; s < stages; s += 2) {
+            stage(integral_constant<int, 0>{}, std::false_type{}, s, rot);
+            turn();
+            if (s + 1 < stages) stage(integral_constant<int, 1>{}, std::false_type{}, s + 1, rot);
+            turn();
+        }
     }
     store_dw<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16);
 }
 
-// dW (+)= the splits' partial sums, added in the splits' order.
+// dW (+)= the splits' partial sums.  A block takes 256 / G pieces of four
+// values with G waves each: wave i of them adds splits i, i + G, ..., several
+// loads on their way at a time, and the G sums are added in the waves' order.
+template <int G>
 __global__ void __launch_bounds__(256)
 k_ckpt8_wgrad_join(const float* __restrict__ part, int32_t splits, int64_t n, int64_t dim, int64_t ldp,
                    void* __restrict__ out, int64_t ldw, int32_t out_bf16, int32_t accumulate) {
-    const int64_t pieces_row = ldp / 4;
-    const int64_t total = n * pieces_row;
-    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < total; id += (int64_t)gridDim.x * 256) {
+    constexpr int PB = 256 / G;  // pieces of a block
+    __shared__ f32x4 sums[G > 1 ? 256 : 1];
+    const int64_t pieces_row = ldp / 4, total = n * pieces_row, stride = n * ldp;
+    const int at = threadIdx.x % PB, first = threadIdx.x / PB;
+    for (int64_t id0 = (int64_t)blockIdx.x * PB; id0 < total; id0 += (int64_t)gridDim.x * PB) {
+        const int64_t id = min(id0 + at, total - 1);
+        const float* p = part + id * 4;
+        f32x4 v{};
+        for (int s = first; s < splits; s += 4 * G) {
+            f32x4 q[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q[i] = ld_f4(p + (int64_t)min(s + i * G, splits - 1) * stride);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (s + i * G < splits) v = s == first && i == 0 ? q[0] : v + q[i];
+        }
+        if constexpr (G > 1) {
+            sums[threadIdx.x] = v;
+            __syncthreads();
+            if (first == 0) {
+#pragma unroll
+                for (int i = 1; i < G; ++i) v += sums[i * PB + at];
+            }
+            __syncthreads();
+            if (first != 0) continue;
+        }
+        if (id0 + at >= total) continue;
         const int64_t r = id / pieces_row, d = (id - r * pieces_row) * 4;
-        const float* p = part + r * ldp + d;
-        f32x4 v = ld_f4(p);
-        for (int s = 1; s < splits; ++s) v += ld_f4(p + (int64_t)s * n * ldp);
         for (int e = 0; e < 4; ++e) {
             if (d + e >= dim) continue;
             if (out_bf16) put(static_cast<BF16*>(out) + r * ldw + d + e, v[e]);
@@ -727,20 +798,25 @@ k_ckpt8_wgrad_join(const float* __restrict__ part, int32_t splits, int64_t n, in
 // the least time.  A round is what all 256 compute units do at one time
 // (`slots` blocks); it takes `stage_us` for each 32 tokens and `store_us` at
 // its end; joining splits takes a launch and the traffic of their sums.
-// Measured against each other: 4096 x 4096 x 4096 (tokens, n, dim) 256 x 256
-// 118 us, 128 x 128 181 us; 2048^3 128 x 128 35 us, 256 x 256 58 us; 4096 x
-// 1024 x 1024 in 1 split 58 us, 2 39 us, 4 28 us, 16 37 us; 16384 x 1024 x
-// 1024 256 x 256 in 16 splits 55 us, 128 x 128 in 8 62 us.
+// Measured against each other, whole calls:
+// bf16 (tokens x n x dim): 4096 x 4096 x 4096 256 x 256 115 us, 128 x 128 168;
+// 2048 x 2048 x 2048 128 x 128 34 us, 256 x 256 58; 4096 x 1024 x 1024 128 x
+// 128 in 1 split 56 us, 2 37, 4 27, 16 39; 16384 x 1024 x 1024 256 x 256 in 16
+// splits 54 us, 128 x 128 in 8 56.
+// fp32: 4096 x 4096 x 4096 128 x 256 347 us, 128 x 128 494; 2048 x 2048 x 2048
+// 128 x 256 in 2 splits 64 us, 128 x 128 in 1 68; 4096 x 1024 x 1024 128 x 256
+// in 8 splits 40 us, 128 x 128 in 4 47; 1027 x 510 x 770 in 9 splits 128 x 128
+// 19.9 us, 128 x 256 21.8.
 struct Shape {
-    int tile, slots;
+    int bn, bd, slots;
     float stage_us, store_us;
     float alone_us;  // stage_us when at most 256 blocks run, one a compute unit
 };
-constexpr Shape kBf16Shapes[] = {{128, 512, 0.75f, 4.0f, 0.45f}, {256, 256, 0.83f, 8.0f, 0.83f}};
-constexpr Shape kF32Shapes[] = {{128, 256, 1.05f, 4.0f, 1.05f}};
+constexpr Shape kBf16Shapes[] = {{128, 128, 512, 0.75f, 4.0f, 0.45f}, {256, 256, 256, 0.83f, 8.0f, 0.83f}};
+constexpr Shape kF32Shapes[] = {{128, 128, 256, 0.97f, 5.0f, 0.97f}, {128, 256, 256, 1.33f, 8.0f, 1.33f}};
 
 struct Plan {
-    int tile;
+    int bd;  // input channels of a tile
     int32_t splits;
     int64_t rows_per_split;
 };
@@ -749,31 +825,29 @@ Plan plan_of(int64_t rows, int64_t n, int64_t dim, bool bf16) {
     Plan best{128, 1, 64};
     double least = 0;
     const int64_t units = rows > 0 ? (rows + 63) / 64 : 1;  // splits are whole pairs of stages
-    for (const Shape& s : kBf16Shapes) {
-        const Shape& shape = bf16 ? s : kF32Shapes[0];
-        const int64_t tiles = ((n + shape.tile - 1) / shape.tile) * ((dim + shape.tile - 1) / shape.tile);
+    for (const Shape& shape : bf16 ? kBf16Shapes : kF32Shapes) {
+        const int64_t tiles = ((n + shape.bn - 1) / shape.bn) * ((dim + shape.bd - 1) / shape.bd);
         for (const int64_t want : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
             if (want > units) break;
             const int64_t per = (units + want - 1) / want, splits = (units + per - 1) / per;
             const int64_t blocks = tiles * splits, rounds = (blocks + shape.slots - 1) / shape.slots;
             double us = (double)rounds * (2.0 * (double)per * (blocks <= 256 ? shape.alone_us : shape.stage_us) + shape.store_us);
-            if (splits > 1) us += 2.5 + (double)(splits + 1) * (double)n * (double)dim * (4.0 / 6e6);
+            if (splits > 1) us += 2.8 + 0.1 * (double)splits + (double)(splits + 1) * (double)n * (double)dim * (4.0 / 8e6);
             if (least == 0 || us < least) {
                 least = us;
-                best = Plan{shape.tile, (int32_t)splits, per * 64};
+                best = Plan{shape.bd, (int32_t)splits, per * 64};
             }
         }
-        if (!bf16) break;
     }
     return best;
 }
 
 int64_t part_pitch(int64_t dim) { return (dim + 3) & ~int64_t(3); }
 
-template <int BN, int BD, int WN, int WD>
+template <int BD>
 hipError_t launch_pipe_f32(const Args& g, int32_t splits, hipStream_t stream) {
-    const dim3 grid((unsigned)(((g.n + BN - 1) / BN) * ((g.dim + BD - 1) / BD)), (unsigned)splits);
-    hipLaunchKernelGGL((k_ckpt8_wgrad_pipe_f32<BN, BD, WN, WD>), grid, dim3(WN * WD * WAVE), 0, stream, g);
+    const dim3 grid((unsigned)(((g.n + 127) / 128) * ((g.dim + BD - 1) / BD)), (unsigned)splits);
+    hipLaunchKernelGGL((k_ckpt8_wgrad_pipe_f32<BD>), grid, dim3(512), 0, stream, g);
     return hipGetLastError();
 }
 
@@ -794,11 +868,17 @@ hipError_t launch_tile(const Args& g, int32_t splits, hipStream_t stream) {
 // g.out, g.ldw: the partial sums of launch_pipe or launch_tile
 hipError_t launch_join(const Args& g, int32_t splits, void* dw, bool dw_bf16, int64_t ldw, bool accumulate,
                        hipStream_t stream) {
-    const int64_t pieces = g.n * (g.ldw / 4), blocks = (pieces + 255) / 256;
-    hipLaunchKernelGGL(k_ckpt8_wgrad_join, dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), dim3(256), 0,
-                       stream, static_cast<const float*>(g.out), splits, g.n, g.dim, g.ldw, dw, ldw, (int32_t)dw_bf16,
-                       (int32_t)accumulate);
-    return hipGetLastError();
+    const int64_t pieces = g.n * (g.ldw / 4);
+    auto run = [&](auto kernel, int per_block) {
+        const int64_t blocks = (pieces + per_block - 1) / per_block;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), dim3(256), 0, stream,
+                           static_cast<const float*>(g.out), splits, g.n, g.dim, g.ldw, dw, ldw, (int32_t)dw_bf16,
+                           (int32_t)accumulate);
+        return hipGetLastError();
+    };
+    // Four waves a piece where one would leave compute units idle: 64 splits of
+    // 128 x 128 5.0 us against 9.9; 9 splits of 510 x 770 9.2 against 8.0.
+    return pieces <= 65536 ? run(k_ckpt8_wgrad_join<4>, 64) : run(k_ckpt8_wgrad_join<1>, 256);
 }
 
 }  // namespace
@@ -830,11 +910,15 @@ hipError_t launch_ckpt8_wgrad(const void* dy, bool dy_bf16, int64_t ldy, const v
     g.accumulate = p.splits > 1 ? 0 : accumulate;
     g.wide = g.ldw % 4 == 0 && reinterpret_cast<uintptr_t>(g.out) % (g.out_bf16 ? 8 : 16) == 0;
     hipError_t e;
-    if (!dy_bf16) e = n < 4 ? launch_tile<3, 128, 2, 2, 64>(g, p.splits, stream)
-                            : launch_pipe_f32<128, 128, 2, 4>(g, p.splits, stream);
-    else if (n < 8) e = launch_tile<1, 128, 2, 2, 64>(g, p.splits, stream);
-    else if (p.tile == 256) e = launch_pipe<256, 256, 2, 4>(g, p.splits, stream);
-    else e = launch_pipe<128, 128, 2, 2>(g, p.splits, stream);
+    if (!dy_bf16) {
+        if (n < 4) e = launch_tile<3, 128, 2, 2, 64>(g, p.splits, stream);
+        else if (p.bd == 256) e = launch_pipe_f32<256>(g, p.splits, stream);
+        else e = launch_pipe_f32<128>(g, p.splits, stream);
+    } else {
+        if (n < 8) e = launch_tile<1, 128, 2, 2, 64>(g, p.splits, stream);
+        else if (p.bd == 256) e = launch_pipe<256, 256, 2, 4>(g, p.splits, stream);
+        else e = launch_pipe<128, 128, 2, 2>(g, p.splits, stream);
+    }
     if (e != hipSuccess || p.splits == 1) return e;
     return launch_join(g, p.splits, dw, dw_bf16, ldw, accumulate, stream);
 }

@@ -364,6 +364,15 @@ def test_wgrad_large_tiles(qc, rows, n, dim):
     check_wgrad(got, dy, v, F32)
 
 
+@pytest.mark.parametrize("rows,n,dim", [(1, 2700, 3300), (33, 2701, 3302), (70, 3600, 3700), (129, 3503, 3425),
+                                        (190, 2563, 3329), (225, 3000, 4000), (609, 2602, 3601), (2048, 513, 2000)])
+def test_wgrad_large_tiles_fp32(qc, rows, n, dim):
+    """Stages from one to twenty, the last ones short, over the wide tile."""
+    dy, x = ref.matrix(rows, n, 1, F32), ref.matrix(rows, dim, 2, F32)
+    got, v = run_wgrad(qc, dy, x)
+    check_wgrad(got, dy, v, F32)
+
+
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
 @pytest.mark.parametrize("rows,n,dim,ldy,skip,ldw,wskip", [(100, 24, 50, 33, 1, 53, 1), (70, 64, 64, 72, 8, 68, 4),
                                                             (200, 40, 96, 48, 0, 97, 3), (2500, 48, 40, 56, 8, 41, 1)])
@@ -389,7 +398,7 @@ def test_wgrad_no_tokens(qc):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
-@pytest.mark.parametrize("rows,n,dim", [(70, 16, 96), (130, 13, 96), (65, 272, 160)])
+@pytest.mark.parametrize("rows,n,dim", [(70, 16, 96), (130, 13, 96), (65, 272, 160), (77, 2602, 3400)])
 def test_wgrad_infinities(qc, rows, n, dim, dtype):
     """An infinite gradient makes its channel infinite (or NaN where values
     of both signs meet it), a NaN group its columns; all else stays finite.
