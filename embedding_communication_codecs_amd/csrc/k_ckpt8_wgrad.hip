@@ -527,7 +527,7 @@ k_ckpt8_wgrad_pipe(Args g) {
 // The barrier stands before the third part, whose fragments are in registers
 // by then: every wave has read the stage's tiles, so the stage after next may
 // be converted over them, and the next one is whole.  With the barrier and the
-// first fragments at a stage's start, 4096 x 4096 x 4096 took 575 us; so it
+// first fragments at a stage's start, 4096 x 4096 x 4096 took 530 us; so it
 // takes 500 with tiles of 128 x 128 and 347 with 128 x 256, which read and
 // convert less of dY, the wider operand, for a product: three of them, at
 // 1.19 PFLOP/s.
