@@ -9,7 +9,8 @@
 // All of this is bound by HBM.  16 lanes hold 128 consecutive values of a
 // row, 8 each (one 16-byte load of bf16): a group is four lanes, its largest
 // magnitude two DPP steps away, and the four exponent bytes of the 128 values
-// leave as one word.
+// leave as one word.  8192 x 8192 bf16: save and restore 34.5 us each, 5.9
+// TB/s; the gated activation 88 us forward and 85 backward, 6.2 and 6.4 TB/s.
 #include "qc_matrix.hpp"
 #include "qc_launch.hpp"
 

@@ -11,11 +11,13 @@
 // the simple kernel) lie in LDS as [token][channel] and are read with
 // ds_read_b64_tr_b16, which hands each lane four tokens of one channel.
 //
-// Large products are bound by the matrix cores, which this power budget runs
-// at 1.85-1.97 PFLOP/s on random bf16 values, and by LDS, which the same waves
-// use to convert X beside them: 16384 x 4096 x 8192 (tokens, n, dim) 870 us,
-// 1.26 PFLOP/s; 4096 x 4096 x 4096 117 us, 1.17.  Small ones by the latency of
-// their few stages and of a second launch that joins the splits.
+// Large products are bound by what the power budget allows: the matrix cores
+// alone run at 1.85-1.97 PFLOP/s on random bf16 values, and LDS traffic and
+// conversion take their share of it.  16384 x 4096 x 8192 (tokens, n, dim) 880
+// us, 1.25 PFLOP/s; 4096 x 4096 x 4096 120 us, 1.15.  Where the conversion and
+// the reads stand among the products, and the waves' priorities, do not change
+// these by more than 2%.  Small ones are bound by the latency of their few
+// stages and of a second launch that joins the splits.
 #include "qc_lds.hpp"
 #include "qc_launch.hpp"
 
@@ -292,12 +294,12 @@ __device__ __forceinline__ void pieces4(f32x4 x, u32x2 (&q)[3]) {
 // --------------------------------------------------------------- pipelined
 // bf16 gradients, n at least 8.  One block computes BN output x BD input
 // channels with WN x WD waves, in stages of 32 tokens.  Everything is loaded
-// straight into LDS, two stages before its use:
-// dY as it is, X as codes and exponent words.  Each lane's 16 codes and their
-// exponents land in a place of its own, so the lane converts them to bf16 as
-// soon as its own wave's loads have landed and writes them to X's tile, which
-// the next barrier shows to the block.  Load batch b holds dY of stage b and
-// X of stage b + 1: converted X is needed one barrier later than landed dY.
+// straight into LDS, two stages before its use: dY as it is, X as codes and
+// exponent words.  Each lane's 16 codes and their exponents land in a place of
+// its own, so the lane converts them to bf16 as soon as its own wave's loads
+// have landed and writes them to X's tile, which the next barrier shows to the
+// block.  Load batch b holds dY of stage b and X of stage b + 1: converted X is
+// needed one barrier later than landed dY.
 //
 // As in the INT8 product, fragments are read ahead of their use and into
 // the next stage, and the only barrier of a stage stands in its middle.
@@ -527,10 +529,10 @@ k_ckpt8_wgrad_pipe(Args g) {
 // The barrier stands before the third part, whose fragments are in registers
 // by then: every wave has read the stage's tiles, so the stage after next may
 // be converted over them, and the next one is whole.  With the barrier and the
-// first fragments at a stage's start, 4096 x 4096 x 4096 took 530 us; so it
-// takes 500 with tiles of 128 x 128 and 347 with 128 x 256, which read and
-// convert less of dY, the wider operand, for a product: three of them, at
-// 1.19 PFLOP/s.
+// first fragments at a stage's start, 4096 x 4096 x 4096 of normal values took
+// 575 us; so it takes 380 with tiles of 128 x 256, three products at 1.08
+// PFLOP/s.  128 x 128 reads and converts dY, the wider operand, twice as often
+// for a product (494 us where 128 x 256 takes 347, values of few bits).
 template <int BD>
 __global__ void __launch_bounds__(512)
 k_ckpt8_wgrad_pipe_f32(Args g) {

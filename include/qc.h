@@ -525,8 +525,9 @@ const char* qc_status_str(int32_t status);
  * of a wider matrix are passed as they are.  Types are QC_F32 or QC_BF16.
  * Codes and exponents are 16-byte aligned, scales 4-byte aligned.  A
  * matrix with rows == 0 is a valid empty call.  Rows are at most
- * 2^23 elements apart in the two products.  Unlike the codecs above, these
- * accept infinities and NaNs and keep them visible, as stated.
+ * 2^23 elements apart in the two products.  No output overlaps an input or
+ * another output.  Unlike the codecs above, these accept infinities and NaNs
+ * and keep them visible, as stated.
  * ---------------------------------------------------------------------
  */
 
@@ -603,7 +604,8 @@ int qc_decode_ckpt8(const int8_t* codes, const uint8_t* exps, int64_t rows, int6
  *   dw[j][d] (+)= sum over tokens t of dy[t][j] * X[t][d],
  * X the values the checkpoint stands for.  Every product is exact and the
  * sum is taken in fp32, in an order that depends on the sizes alone (the
- * same call gives the same bits).
+ * same call gives the same bits).  Gradients, products and sums below the
+ * smallest normal number (2^-126) may count as zero.
  *
  *   dy          [rows][n] of type dytype, row stride ldy.
  *   codes, exps a checkpoint of [rows][dim].
