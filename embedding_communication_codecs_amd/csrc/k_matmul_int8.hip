@@ -30,8 +30,7 @@ struct Args {
     int64_t m, n;
     int32_t k;
     int64_t ldc;
-    bool wide;   // rows of C start at multiples of four elements
-    bool lines;  // and at multiples of 16 bytes
+    int32_t align;  // rows of C start at multiples of so many bytes: 16, 8, 4 or 2
 };
 
 // C = (sum * sa) * sb: the scales are applied one after the other, so that
@@ -250,50 +249,60 @@ k_mm_int8_pipe(Args g, T* __restrict__ c) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) sb[i][e] = g.sb[min(col + e, g.n - 1)];
     }
-    if (g.lines && n0 + BN <= g.n && m0 + BM <= g.m) {
-        // 16 tokens at a time through the wave's part of LDS, so that a store
-        // takes whole pieces of a few rows of C, not eight bytes of 16 (4096 x
-        // 4096 x 128: 11.5 us against 15.0; 16384 x 8192 x 8192 827 against
-        // 851).  Piece p of row r in slot p ^ r.
-        constexpr int RB = FN * 16 * (int)sizeof(T), PR = RB / 16;
-        static_assert((PR & (PR - 1)) == 0 && PR <= WAVE && NW * 16 * RB <= 2 * STAGE, "a wave's part of LDS");
-        __syncthreads();  // every wave has read its last fragments
-        uint8_t* own = lds + w * (16 * RB);
-#pragma unroll
-        for (int j = 0; j < FM; ++j) {
-#pragma unroll
-            for (int i = 0; i < FN; ++i) {
-                float v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = scaled(acc[i][j][e], sa[j], sb[i][e]);
-                const int at = (i * 16 + 4 * (l >> 4)) * (int)sizeof(T), r = l & 15;
-                store4(reinterpret_cast<T*>(own + r * RB + (((at >> 4) ^ (r & (PR - 1))) << 4) + (at & 15)), 4, v, true);
+    // 16 tokens at a time through the wave's part of LDS, so that a store takes
+    // long pieces of a few rows of C and not eight bytes of 16 rows (4096 x
+    // 4096 x 128: 11.5 us against 15.0; 16384 x 8192 x 8192 827 against 851;
+    // 1280 x 3206 x 3776, rows at multiples of four bytes, 33.3 against 38.7).
+    // 16-byte piece p of row r
+    // in slot p ^ r.
+    constexpr int COLS = FN * 16, RB = COLS * (int)sizeof(T), PR = RB / 16;
+    static_assert((PR & (PR - 1)) == 0 && PR <= WAVE && NW * 16 * RB <= 2 * STAGE, "a wave's part of LDS");
+    __syncthreads();  // every wave has read its last fragments
+    uint8_t* own = lds + w * (16 * RB);
+    // 16 rows of C from LDS, U bytes (a vector of type V) a lane and store
+    auto write = [&](auto unit, auto inside, int64_t row0, int64_t col0) {
+        typedef decltype(unit) V;
+        constexpr int U = sizeof(V), PW = RB / U, E = U / (int)sizeof(T);
+        constexpr bool INSIDE = decltype(inside)::value;
+#pragma unroll 4
+        for (int q = 0; q < 16 * PW / WAVE; ++q) {
+            const int r = (q * WAVE + l) / PW, at = (q * WAVE + l) % PW * U;
+            const uint8_t* from = own + r * RB + (((at >> 4) ^ (r & (PR - 1))) << 4) + (at & 15);
+            const int64_t row = row0 + r, col = col0 + at / (int)sizeof(T), left = INSIDE || row < g.m ? g.n - col : 0;
+            T* to = c + row * g.ldc + col;
+            if (INSIDE || left >= E) {
+                *reinterpret_cast<V*>(to) = *reinterpret_cast<const V*>(from);
+            } else {
+                for (int e = 0; e < E; ++e)
+                    if (e < left) to[e] = reinterpret_cast<const T*>(from)[e];
             }
-            wave_lds_sync();
-            T* cj = c + (m0 + (wm * FM + j) * 16) * g.ldc + n0 + wn * FN * 16;
-#pragma unroll
-            for (int q = 0; q < RB / 64; ++q) {
-                const int r = (q * WAVE + l) / PR, p = (q * WAVE + l) % PR;
-                *reinterpret_cast<u32x4*>(cj + r * g.ldc + p * (16 / (int)sizeof(T))) =
-                    *reinterpret_cast<const u32x4*>(own + r * RB + ((p ^ (r & (PR - 1))) << 4));
-            }
-            wave_lds_sync();
         }
-        return;
-    }
+    };
+    typedef std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t> One;
+    const bool inside = n0 + BN <= g.n && m0 + BM <= g.m;
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
-        const int64_t row = m0 + (wm * FM + j) * 16 + (l & 15);
-        T* cr = c + row * g.ldc;
 #pragma unroll
         for (int i = 0; i < FN; ++i) {
-            const int64_t col = n0 + (wn * FN + i) * 16 + 4 * (l >> 4);
-            const int64_t left = row < g.m ? g.n - col : 0;
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = scaled(acc[i][j][e], sa[j], sb[i][e]);
-            store4(cr + col, left < 4 ? (int)left : 4, v, g.wide);
+            const int at = (i * 16 + 4 * (l >> 4)) * (int)sizeof(T), r = l & 15;
+            store4(reinterpret_cast<T*>(own + r * RB + (((at >> 4) ^ (r & (PR - 1))) << 4) + (at & 15)), 4, v, true);
         }
+        wave_lds_sync();
+        const int64_t row0 = m0 + (wm * FM + j) * 16, col0 = n0 + wn * COLS;
+        if (g.align == 16) {
+            if (inside) write(u32x4{}, std::true_type{}, row0, col0);
+            else write(u32x4{}, std::false_type{}, row0, col0);
+        } else if (g.align == 8) {
+            write(u32x2{}, std::false_type{}, row0, col0);
+        } else if (g.align == 4) {
+            write(uint32_t{}, std::false_type{}, row0, col0);
+        } else {
+            write(One{}, std::false_type{}, row0, col0);
+        }
+        wave_lds_sync();
     }
 }
 
@@ -393,7 +402,7 @@ k_mm_int8_few(Args g, T* __restrict__ c) {
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = scaled(sum[e], sa, e < left ? g.sb[col + e] : 0.0f);
-            store4(c + row * g.ldc + col, left < 4 ? (int)left : 4, v, g.wide);
+            store4(c + row * g.ldc + col, left < 4 ? (int)left : 4, v, g.align >= 4 * (int)sizeof(T));
         }
     }
 }
@@ -461,9 +470,9 @@ hipError_t launch(const Args& g, T* c, hipStream_t stream) {
 hipError_t launch_matmul_int8(const void* a, const float* a_scale, int64_t lda, const void* b, const float* b_scale,
                               int64_t ldb, int64_t m, int64_t n, int64_t k, void* c, bool bf16, int64_t ldc,
                               hipStream_t stream) {
+    const uintptr_t rows_at = reinterpret_cast<uintptr_t>(c) | (uintptr_t)(ldc * (bf16 ? 2 : 4));
     const Args g{static_cast<const uint8_t*>(a), a_scale, lda, static_cast<const uint8_t*>(b), b_scale, ldb, m, n,
-                 (int32_t)k, ldc, ldc % 4 == 0 && reinterpret_cast<uintptr_t>(c) % (bf16 ? 8 : 16) == 0,
-                 ldc % (bf16 ? 8 : 4) == 0 && reinterpret_cast<uintptr_t>(c) % 16 == 0};
+                 (int32_t)k, ldc, rows_at % 16 == 0 ? 16 : rows_at % 8 == 0 ? 8 : rows_at % 4 == 0 ? 4 : 2};
     return bf16 ? launch(g, static_cast<BF16*>(c), stream) : launch(g, static_cast<float*>(c), stream);
 }
 
