@@ -27,6 +27,8 @@ namespace qc {
 namespace {
 
 typedef __attribute__((address_space(3))) s16x4* lds4;
+typedef f32x4 f32x4_a4 __attribute__((aligned(4)));  // four values of dW, wherever they start
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
 
 struct Args {
     const void* dy;
@@ -39,7 +41,6 @@ struct Args {
     void* out;               // dW, or the first split's partial sums
     int64_t ldw, split_stride;
     int32_t out_bf16, accumulate;
-    bool wide;  // rows of dW start at multiples of four elements
 };
 
 // Byte offset of 16-byte piece `c` of token `t` in a tile of `row_bytes` a
@@ -73,46 +74,12 @@ __device__ __forceinline__ void pieces(float x, uint32_t (&p)[3]) {
 }
 
 // A wave's sums to dW.  Lane l holds output channel l % 16 of each of FN
-// tiles, input channels 4 * (l / 16) .. + 3 of each of FD.  Where rows of dW
-// start anywhere, 16 of them at a time pass through the wave's `own` part of
-// LDS (1,024 * FD bytes, free by now), so that a store takes neighbouring
-// values of one or two rows (piece p of row r in slot p ^ r): 1000 x 4096 x
-// 4095 47 us against 69, 243 x 2240 x 2243 19 against 25.
+// tiles, input channels 4 * (l / 16) .. + 3 of each of FD.  Four of them are
+// one store wherever their row starts (1000 x 4096 x 4095 46 us against 69 with
+// a store a value).
 template <int FN, int FD>
-__device__ __forceinline__ void store_dw(const Args& g, f32x4 (&acc)[FD][FN], int64_t n0, int64_t d0, uint8_t* own) {
-    int l = lane_id();
-    asm volatile("" : "+v"(l));  // what follows from it is computed here: held through the main loop, it would not fit
-    if (!g.wide) {
-        constexpr int COLS = FD * 16, PR = FD * 4, ROWS = WAVE / COLS;  // of a row; rows of a store
-        static_assert(COLS <= WAVE && (FD & (FD - 1)) == 0, "a store takes whole rows");
-        const int col = l % COLS;
-        const int64_t d = d0 + col;
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-#pragma unroll
-            for (int i = 0; i < FD; ++i) {
-                const int r = l & 15, p = i * 4 + (l >> 4);
-                *reinterpret_cast<f32x4*>(own + r * (COLS * 4) + ((p ^ (r & (PR - 1))) << 4)) = acc[i][j];
-            }
-            wave_lds_sync();
-#pragma unroll
-            for (int q = 0; q < 16 / ROWS; ++q) {
-                const int r = q * ROWS + l / COLS;
-                const int64_t n = n0 + j * 16 + r;
-                const float v = *reinterpret_cast<const float*>(own + r * (COLS * 4) + (((col >> 2) ^ (r & (PR - 1))) << 4) +
-                                                                (col & 3) * 4);
-                if (n >= g.n || d >= g.dim) continue;
-                if (g.out_bf16) {
-                    put(static_cast<BF16*>(g.out) + n * g.ldw + d, v);
-                } else {
-                    float* o = static_cast<float*>(g.out) + (int64_t)blockIdx.y * g.split_stride + n * g.ldw + d;
-                    *o = g.accumulate ? *o + v : v;
-                }
-            }
-            wave_lds_sync();
-        }
-        return;
-    }
+__device__ __forceinline__ void store_dw(const Args& g, f32x4 (&acc)[FD][FN], int64_t n0, int64_t d0) {
+    const int l = lane_id();
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
         const int64_t n = n0 + j * 16 + (l & 15);
@@ -125,7 +92,7 @@ __device__ __forceinline__ void store_dw(const Args& g, f32x4 (&acc)[FD][FN], in
                 const int64_t left = g.dim - d - 16 * i;
                 const f32x4 v = acc[i][j];
                 if (left >= 4)
-                    *reinterpret_cast<u32x2*>(o + 16 * i) = u32x2{bf16_pair(v.x, v.y), bf16_pair(v.z, v.w)};
+                    *reinterpret_cast<u32x2_a2*>(o + 16 * i) = u32x2{bf16_pair(v.x, v.y), bf16_pair(v.z, v.w)};
                 else
                     for (int e = 0; e < 4; ++e)
                         if (e < left) put(o + 16 * i + e, v[e]);
@@ -137,7 +104,7 @@ __device__ __forceinline__ void store_dw(const Args& g, f32x4 (&acc)[FD][FN], in
 #pragma unroll
             for (int i = 0; i < FD; ++i) {
                 const int64_t left = g.dim - d - 16 * i;
-                if (left >= 4) acc[i][j] += *reinterpret_cast<const f32x4*>(o + 16 * i);
+                if (left >= 4) acc[i][j] += *reinterpret_cast<const f32x4_a4*>(o + 16 * i);
                 else
                     for (int e = 0; e < 4; ++e)
                         if (e < left) acc[i][j][e] += o[16 * i + e];
@@ -146,7 +113,7 @@ __device__ __forceinline__ void store_dw(const Args& g, f32x4 (&acc)[FD][FN], in
 #pragma unroll
         for (int i = 0; i < FD; ++i) {
             const int64_t left = g.dim - d - 16 * i;
-            if (left >= 4) *reinterpret_cast<f32x4*>(o + 16 * i) = acc[i][j];
+            if (left >= 4) *reinterpret_cast<f32x4_a4*>(o + 16 * i) = acc[i][j];
             else
                 for (int e = 0; e < 4; ++e)
                     if (e < left) o[16 * i + e] = acc[i][j][e];
@@ -303,8 +270,7 @@ k_ckpt8_wgrad(Args g) {
         }
     }
 
-    __syncthreads();  // every wave is done with the tiles
-    store_dw<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16, lds + w * (1024 * FD));
+    store_dw<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16);
 }
 
 // The same of four neighbours, packed (word 0 holds values 0 and 1), without
@@ -554,8 +520,7 @@ k_ckpt8_wgrad_pipe(Args g) {
             stage(integral_constant<int, 1>{}, std::false_type{}, s + 1);
         }
     }
-    __syncthreads();  // every wave is done with the tiles
-    store_dw<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16, lds + w * (1024 * FD));
+    store_dw<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16);
 }
 
 // The same for fp32 gradients, n at least 4: each wave's part of dY lands in
@@ -784,8 +749,7 @@ k_ckpt8_wgrad_pipe_f32(Args g) {
             turn();
         }
     }
-    __syncthreads();  // every wave is done with the tiles
-    store_dw<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16, lds + w * (1024 * FD));
+    store_dw<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16);
 }
 
 // dW (+)= the splits' partial sums.  A block takes 256 / G pieces of four
@@ -823,13 +787,20 @@ k_ckpt8_wgrad_join(const float* __restrict__ part, int32_t splits, int64_t n, in
         }
         if (id0 + at >= total) continue;
         const int64_t r = id / pieces_row, d = (id - r * pieces_row) * 4;
-        for (int e = 0; e < 4; ++e) {
-            if (d + e >= dim) continue;
-            if (out_bf16) put(static_cast<BF16*>(out) + r * ldw + d + e, v[e]);
-            else {
-                float* o = static_cast<float*>(out) + r * ldw + d + e;
-                *o = accumulate ? *o + v[e] : v[e];
-            }
+        if (out_bf16) {
+            BF16* o = static_cast<BF16*>(out) + r * ldw + d;
+            if (d + 4 <= dim) *reinterpret_cast<u32x2_a2*>(o) = u32x2{bf16_pair(v.x, v.y), bf16_pair(v.z, v.w)};
+            else
+                for (int e = 0; e < 4; ++e)
+                    if (d + e < dim) put(o + e, v[e]);
+            continue;
+        }
+        float* o = static_cast<float*>(out) + r * ldw + d;
+        if (d + 4 <= dim) {
+            *reinterpret_cast<f32x4_a4*>(o) = accumulate ? *reinterpret_cast<const f32x4_a4*>(o) + v : v;
+        } else {
+            for (int e = 0; e < 4; ++e)
+                if (d + e < dim) o[e] = accumulate ? o[e] + v[e] : v[e];
         }
     }
 }
@@ -949,7 +920,6 @@ hipError_t launch_ckpt8_wgrad(const void* dy, bool dy_bf16, int64_t ldy, const v
     g.split_stride = n * part_pitch(dim);
     g.out_bf16 = p.splits > 1 ? 0 : dw_bf16;
     g.accumulate = p.splits > 1 ? 0 : accumulate;
-    g.wide = g.ldw % 4 == 0 && reinterpret_cast<uintptr_t>(g.out) % (g.out_bf16 ? 8 : 16) == 0;
     hipError_t e;
     if (!dy_bf16) {
         if (n < 4) e = launch_tile<3, 128, 2, 2, 64>(g, p.splits, stream);

@@ -30,29 +30,28 @@ struct Args {
     int64_t m, n;
     int32_t k;
     int64_t ldc;
-    int32_t align;  // rows of C start at multiples of so many bytes: 16, 8, 4 or 2
 };
 
 // C = (sum * sa) * sb: the scales are applied one after the other, so that
 // two tiny ones cannot underflow together.
 __device__ __forceinline__ float scaled(int sum, float sa, float sb) { return ((float)sum * sa) * sb; }
 
-__device__ __forceinline__ void store4(BF16* p, int left, const float (&v)[4], bool wide) {
-    if (wide && left >= 4) {
-        *reinterpret_cast<u32x2*>(p) = u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+__device__ __forceinline__ u32x2 packed4(const BF16*, const float (&v)[4]) {
+    return u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+}
+__device__ __forceinline__ f32x4 packed4(const float*, const float (&v)[4]) { return f32x4{v[0], v[1], v[2], v[3]}; }
+
+// Four values, `left` of which exist, in one store wherever they start.
+template <class T>
+__device__ __forceinline__ void store4(T* p, int left, const float (&v)[4]) {
+    typedef decltype(packed4(p, v)) V;
+    typedef V V_at_any __attribute__((aligned(sizeof(T))));
+    if (left >= 4) {
+        *reinterpret_cast<V_at_any*>(p) = packed4(p, v);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (i < left) put(p + i, v[i]);
-    }
-}
-__device__ __forceinline__ void store4(float* p, int left, const float (&v)[4], bool wide) {
-    if (wide && left >= 4) {
-        *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < left) p[i] = v[i];
     }
 }
 
@@ -250,35 +249,14 @@ k_mm_int8_pipe(Args g, T* __restrict__ c) {
         for (int e = 0; e < 4; ++e) sb[i][e] = g.sb[min(col + e, g.n - 1)];
     }
     // 16 tokens at a time through the wave's part of LDS, so that a store takes
-    // long pieces of a few rows of C and not eight bytes of 16 rows (4096 x
-    // 4096 x 128: 11.5 us against 15.0; 16384 x 8192 x 8192 827 against 851;
-    // 1280 x 3206 x 3776, rows at multiples of four bytes, 33.3 against 38.7).
-    // 16-byte piece p of row r
-    // in slot p ^ r.
-    constexpr int COLS = FN * 16, RB = COLS * (int)sizeof(T), PR = RB / 16;
+    // whole 16-byte pieces of a few rows of C, wherever they start, and not
+    // eight bytes of 16 rows (4096 x 4096 x 128: 11.5 us against 15.0; 16384 x
+    // 8192 x 8192 827 against 851; 1280 x 3206 x 3776 30.5 against 38.7).  Piece
+    // p of row r in slot p ^ r.
+    constexpr int COLS = FN * 16, RB = COLS * (int)sizeof(T), PR = RB / 16, E = 16 / (int)sizeof(T);
     static_assert((PR & (PR - 1)) == 0 && PR <= WAVE && NW * 16 * RB <= 2 * STAGE, "a wave's part of LDS");
     __syncthreads();  // every wave has read its last fragments
     uint8_t* own = lds + w * (16 * RB);
-    // 16 rows of C from LDS, U bytes (a vector of type V) a lane and store
-    auto write = [&](auto unit, auto inside, int64_t row0, int64_t col0) {
-        typedef decltype(unit) V;
-        constexpr int U = sizeof(V), PW = RB / U, E = U / (int)sizeof(T);
-        constexpr bool INSIDE = decltype(inside)::value;
-#pragma unroll 4
-        for (int q = 0; q < 16 * PW / WAVE; ++q) {
-            const int r = (q * WAVE + l) / PW, at = (q * WAVE + l) % PW * U;
-            const uint8_t* from = own + r * RB + (((at >> 4) ^ (r & (PR - 1))) << 4) + (at & 15);
-            const int64_t row = row0 + r, col = col0 + at / (int)sizeof(T), left = INSIDE || row < g.m ? g.n - col : 0;
-            T* to = c + row * g.ldc + col;
-            if (INSIDE || left >= E) {
-                *reinterpret_cast<V*>(to) = *reinterpret_cast<const V*>(from);
-            } else {
-                for (int e = 0; e < E; ++e)
-                    if (e < left) to[e] = reinterpret_cast<const T*>(from)[e];
-            }
-        }
-    };
-    typedef std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t> One;
     const bool inside = n0 + BN <= g.n && m0 + BM <= g.m;
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
@@ -288,19 +266,24 @@ k_mm_int8_pipe(Args g, T* __restrict__ c) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = scaled(acc[i][j][e], sa[j], sb[i][e]);
             const int at = (i * 16 + 4 * (l >> 4)) * (int)sizeof(T), r = l & 15;
-            store4(reinterpret_cast<T*>(own + r * RB + (((at >> 4) ^ (r & (PR - 1))) << 4) + (at & 15)), 4, v, true);
+            const auto four = packed4(c, v);
+            *reinterpret_cast<std::remove_const_t<decltype(four)>*>(own + r * RB + (((at >> 4) ^ (r & (PR - 1))) << 4) +
+                                                                    (at & 15)) = four;
         }
         wave_lds_sync();
         const int64_t row0 = m0 + (wm * FM + j) * 16, col0 = n0 + wn * COLS;
-        if (g.align == 16) {
-            if (inside) write(u32x4{}, std::true_type{}, row0, col0);
-            else write(u32x4{}, std::false_type{}, row0, col0);
-        } else if (g.align == 8) {
-            write(u32x2{}, std::false_type{}, row0, col0);
-        } else if (g.align == 4) {
-            write(uint32_t{}, std::false_type{}, row0, col0);
-        } else {
-            write(One{}, std::false_type{}, row0, col0);
+#pragma unroll
+        for (int q = 0; q < RB / 64; ++q) {
+            const int r = (q * WAVE + l) / PR, p = (q * WAVE + l) % PR;
+            const uint8_t* from = own + r * RB + ((p ^ (r & (PR - 1))) << 4);
+            const int64_t row = row0 + r, col = col0 + p * E, left = inside || row < g.m ? g.n - col : 0;
+            T* to = c + row * g.ldc + col;
+            if (inside || left >= E) {
+                *reinterpret_cast<u32x4_a2*>(to) = *reinterpret_cast<const u32x4*>(from);
+            } else {
+                for (int e = 0; e < E; ++e)
+                    if (e < left) to[e] = reinterpret_cast<const T*>(from)[e];
+            }
         }
         wave_lds_sync();
     }
@@ -402,7 +385,7 @@ k_mm_int8_few(Args g, T* __restrict__ c) {
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = scaled(sum[e], sa, e < left ? g.sb[col + e] : 0.0f);
-            store4(c + row * g.ldc + col, left < 4 ? (int)left : 4, v, g.align >= 4 * (int)sizeof(T));
+            store4(c + row * g.ldc + col, left < 4 ? (int)left : 4, v);
         }
     }
 }
@@ -470,9 +453,8 @@ hipError_t launch(const Args& g, T* c, hipStream_t stream) {
 hipError_t launch_matmul_int8(const void* a, const float* a_scale, int64_t lda, const void* b, const float* b_scale,
                               int64_t ldb, int64_t m, int64_t n, int64_t k, void* c, bool bf16, int64_t ldc,
                               hipStream_t stream) {
-    const uintptr_t rows_at = reinterpret_cast<uintptr_t>(c) | (uintptr_t)(ldc * (bf16 ? 2 : 4));
     const Args g{static_cast<const uint8_t*>(a), a_scale, lda, static_cast<const uint8_t*>(b), b_scale, ldb, m, n,
-                 (int32_t)k, ldc, rows_at % 16 == 0 ? 16 : rows_at % 8 == 0 ? 8 : rows_at % 4 == 0 ? 4 : 2};
+                 (int32_t)k, ldc};
     return bf16 ? launch(g, static_cast<BF16*>(c), stream) : launch(g, static_cast<float*>(c), stream);
 }
 
