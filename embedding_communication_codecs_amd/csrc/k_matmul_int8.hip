@@ -125,13 +125,16 @@ __device__ __forceinline__ void zero_tail(uint8_t* lds, int valid) {
 
 // ------------------------------------------------------- pipelined tiles
 // One block computes BN channels x BM tokens with WN x WM waves, in stages of
-// K bytes of k, two of them in LDS.  A wave reads its fragments ahead of
-// their use, into the next stage too; the wait for that stage, and the only
+// K bytes of k, NB of them in LDS.  A wave reads its fragments ahead of their
+// use, into the next stage too; the wait for that stage, and the only
 // barrier, stand where the last fragments of this one have been read, and the
 // fragments already in registers keep the matrix cores busy across it.  The
-// loads of the stage after next follow at once, over the one just left, and
-// have a whole stage's time to arrive.
-template <class T, int BN, int BM, int WN, int WM, int K>
+// loads of the stage NB further on follow at once, over the one just left,
+// and have NB - 1 stages' time to arrive: a stage of a small tile is shorter
+// than a load takes, so it needs more of them (1024 x 4096 x 4096 with tiles
+// of 128 x 128: 21.6 us with four stages of 128 bytes, 25 with two of 256;
+// 256 x 4096 x 4096 with 64 x 64: 12.5 with four, 15.8 with two of 256).
+template <class T, int BN, int BM, int WN, int WM, int K, int NB>
 __global__ void __launch_bounds__(WN * WM * WAVE)
 k_mm_int8_pipe(Args g, T* __restrict__ c) {
     constexpr int NW = WN * WM, THREADS = NW * WAVE;
@@ -141,7 +144,7 @@ k_mm_int8_pipe(Args g, T* __restrict__ c) {
     constexpr int TB = BN * K, STAGE = (BN + BM) * K;      // weights first, then tokens
     // a stage's last read comes before the barrier, the next one's first after it
     static_assert(FN % 4 == 0 && FM >= 1 && STEPS - 1 - AHEAD <= TURN && STEPS - AHEAD >= TURN, "tile shape");
-    __shared__ __align__(1024) uint8_t lds[2 * STAGE];
+    __shared__ __align__(1024) uint8_t lds[NB * STAGE];
 
     const uint32_t tn = (uint32_t)((g.n + BN - 1) / BN), tm = (uint32_t)((g.m + BM - 1) / BM);
     const Tile2 tile = tile_of<4>(blockIdx.x, tn, tm);
@@ -166,11 +169,11 @@ k_mm_int8_pipe(Args g, T* __restrict__ c) {
     };
     auto fetch = [&](int s) {
 #pragma unroll
-        for (int part = 0; part < LOADS; ++part) fetch_part(std::false_type{}, part, s & 1, s);
+        for (int part = 0; part < LOADS; ++part) fetch_part(std::false_type{}, part, s % NB, s);
     };
     auto cut = [&](int s) {
         if (s >= whole) {  // the weights' bytes past k become zeros (integers: one side is enough)
-            zero_tail<BN, K, THREADS>(lds + (s & 1) * STAGE, g.k - s * K);
+            zero_tail<BN, K, THREADS>(lds + s % NB * STAGE, g.k - s * K);
             __syncthreads();
         }
     };
@@ -187,27 +190,29 @@ k_mm_int8_pipe(Args g, T* __restrict__ c) {
 
     i32x4 acc[FN][FM] = {};
     i32x4 fb[4], fa[2][FM];
-    // Stage s in buffer `buf`.  FAST: stages s + 1 and s + 2 exist and are whole.
-    auto stage = [&](int buf, auto fast, int s) {
+    // Stage s in buffer `buf`, the next one in `next`.  FAST: stages up to s +
+    // NB exist and are whole.
+    auto stage = [&](int buf, int next, auto fast, int s) {
         constexpr bool FAST = decltype(fast)::value;
 #pragma unroll
         for (int q = 0; q < STEPS; ++q) {
             const int kk = q / FN, i = q % FN;
             if (q + AHEAD < STEPS) fb[(q + AHEAD) % 4] = read_b(buf, q + AHEAD);
             if (q == TURN && (FAST || s + 1 < stages)) {
-                lds_landed();
+                if (FAST || s + NB - 1 < stages) lds_landed_but<(NB - 2) * LOADS>();
+                else lds_landed();
                 if (!FAST) cut(s + 1);
             }
-            if (q + AHEAD >= STEPS) fb[(q + AHEAD) % 4] = read_b(buf ^ 1, q + AHEAD - STEPS);
+            if (q + AHEAD >= STEPS) fb[(q + AHEAD) % 4] = read_b(next, q + AHEAD - STEPS);
             if (i >= FN / 2) {
                 constexpr int H = FN / 2;  // this step's share of the token fragments and of the loads
 #pragma unroll
                 for (int e = (i - H) * FM / H; e < (i - H + 1) * FM / H; ++e)
-                    fa[(kk + 1) & 1][e] = kk + 1 < KK ? read_a(buf, kk + 1, e) : read_a(buf ^ 1, 0, e);
-                if (kk + 1 == KK && (FAST || s + 2 < stages)) {
+                    fa[(kk + 1) & 1][e] = kk + 1 < KK ? read_a(buf, kk + 1, e) : read_a(next, 0, e);
+                if (kk + 1 == KK && (FAST || s + NB < stages)) {
 #pragma unroll
                     for (int d = (i - H) * LOADS / H; d < (i - H + 1) * LOADS / H; ++d)
-                        fetch_part(fast, d, buf, s + 2);
+                        fetch_part(fast, d, buf, s + NB);
                 }
             }
 #pragma unroll
@@ -217,25 +222,21 @@ k_mm_int8_pipe(Args g, T* __restrict__ c) {
         }
     };
 
-    fetch(0);
-    if (stages > 1) {
-        fetch(1);
-        lds_landed_but<LOADS>();
-    } else {
-        lds_landed();
-    }
+    for (int s = 0; s < NB && s < stages; ++s) fetch(s);
+    if (stages >= NB) lds_landed_but<(NB - 1) * LOADS>();
+    else lds_landed();
     cut(0);
 #pragma unroll
     for (int j = 0; j < FM; ++j) fa[0][j] = read_a(0, 0, j);
 #pragma unroll
     for (int q = 0; q < AHEAD; ++q) fb[q] = read_b(0, q);
     int s = 0;
-    for (; s + 3 < whole; s += 2) {
-        stage(0, std::true_type{}, s);
-        stage(1, std::true_type{}, s + 1);
+    for (; s + 2 * NB - 1 < whole; s += NB) {
+#pragma unroll
+        for (int u = 0; u < NB; ++u) stage(u, (u + 1) % NB, std::true_type{}, s + u);
     }
 #pragma unroll 1
-    for (; s < stages; ++s) stage(s & 1, std::false_type{}, s);
+    for (; s < stages; ++s) stage(s % NB, (s + 1) % NB, std::false_type{}, s);
 
     // every scale before the first store: a load after a store would wait for it
     float sa[FM];
@@ -254,7 +255,7 @@ k_mm_int8_pipe(Args g, T* __restrict__ c) {
     // 8192 x 8192 827 against 851; 1280 x 3206 x 3776 30.5 against 38.7).  Piece
     // p of row r in slot p ^ r.
     constexpr int COLS = FN * 16, RB = COLS * (int)sizeof(T), PR = RB / 16, E = 16 / (int)sizeof(T);
-    static_assert((PR & (PR - 1)) == 0 && PR <= WAVE && NW * 16 * RB <= 2 * STAGE, "a wave's part of LDS");
+    static_assert((PR & (PR - 1)) == 0 && PR <= WAVE && NW * 16 * RB <= NB * STAGE, "a wave's part of LDS");
     __syncthreads();  // every wave has read its last fragments
     uint8_t* own = lds + w * (16 * RB);
     const bool inside = n0 + BN <= g.n && m0 + BM <= g.m;
@@ -289,10 +290,10 @@ k_mm_int8_pipe(Args g, T* __restrict__ c) {
     }
 }
 
-template <class T, int BN, int BM, int WN, int WM, int K>
+template <class T, int BN, int BM, int WN, int WM, int K, int NB>
 hipError_t launch_pipe(const Args& g, T* c, hipStream_t stream) {
     const int64_t tiles = ((g.n + BN - 1) / BN) * ((g.m + BM - 1) / BM);
-    hipLaunchKernelGGL((k_mm_int8_pipe<T, BN, BM, WN, WM, K>), dim3((unsigned)tiles), dim3(WN * WM * WAVE), 0, stream, g,
+    hipLaunchKernelGGL((k_mm_int8_pipe<T, BN, BM, WN, WM, K, NB>), dim3((unsigned)tiles), dim3(WN * WM * WAVE), 0, stream, g,
                        c);
     return hipGetLastError();
 }
@@ -404,17 +405,18 @@ hipError_t launch_few(const Args& g, T* c, hipStream_t stream) {
 // where it says so):
 //   m    1: 16 x 16 5.6 us (32 x 16 6.2)     m  16 (16384): 32 x 16 13.5 (32 x 32 15.5)
 //   m   32: 32 x 16 6.7 (32 x 32 8.4)        m  32 (16384): 32 x 32 16.4 (32 x 64 17.1)
-//   m   61: 32 x 32 8.4 (32 x 64 9.8)        m  61 (16384): 64 x 64 18.4 (32 x 64 18.9)
-//   m  128: 32 x 64 9.6 (32 x 32 13.1)       m 256: 64 x 64 14.4 (32 x 64 15.6)
-//   m  512: 128 x 64 19.3 (128 x 128 24.0)   m 1024: 128 x 128, 256 bytes of k 25.9 (128 bytes 29.6)
-//   m 2048: 128 x 128, 128 bytes of k 39.3 (256 bytes 47.6)  m 4096: 256 x 256 55.9 (128 x 128 76.3)
+//   m   61: 32 x 32 8.4 (32 x 64 9.7)        m 128: 32 x 64 9.6 (64 x 64 12.4)
+//   m  256: 64 x 64 12.5 (32 x 64 16.0)      m 512: 64 x 128 16.0 (64 x 64 19.5)
+//   m 1024: 128 x 128 21.6 (128 x 256 29.1)  m 2048: 128 x 256 34.3 (128 x 128 44.2)
+//   m 4096: 256 x 256 55.9 (128 x 256 67.2)
 struct Shape {
-    int bn, bm, slots;  // channels, tokens, blocks at work at one time
+    int bn, bm;  // channels, tokens
     float round_us;
 };
+constexpr int kUnits = 256;  // compute units, each with one block at work
 constexpr Shape kShapes[] = {
-    {16, 16, 256, 4.0f},  {32, 16, 256, 4.7f},   {32, 32, 256, 6.5f},    {32, 64, 256, 7.2f},
-    {64, 64, 256, 12.0f}, {128, 64, 256, 17.6f}, {128, 128, 256, 22.8f}, {128, 128, 512, 38.0f}, {256, 256, 256, 51.0f},
+    {16, 16, 4.0f},   {32, 16, 4.7f},    {32, 32, 6.5f},    {32, 64, 7.4f},    {64, 64, 10.4f},
+    {64, 128, 14.1f}, {128, 128, 19.7f}, {128, 256, 32.2f}, {256, 256, 51.0f},
 };
 
 int shape_of(int64_t m, int64_t n) {
@@ -424,7 +426,7 @@ int shape_of(int64_t m, int64_t n) {
     for (int i = 0; i < kAll; ++i) {
         const Shape& s = kShapes[i];
         const int64_t blocks = ((n + s.bn - 1) / s.bn) * ((m + s.bm - 1) / s.bm);
-        const double us = (double)((blocks + s.slots - 1) / s.slots) * s.round_us;
+        const double us = (double)((blocks + kUnits - 1) / kUnits) * s.round_us;
         if (us < least && blocks < int64_t(1) << 23) {  // a grid has fewer than 2^32 threads
             best = i;
             least = us;
@@ -440,11 +442,11 @@ hipError_t launch(const Args& g, T* c, hipStream_t stream) {
         case 1: return launch_few<T, 2, 1, 6, 2>(g, c, stream);
         case 2: return launch_few<T, 2, 2, 8, 1>(g, c, stream);
         case 3: return launch_few<T, 2, 4, 6, 1>(g, c, stream);
-        case 4: return launch_few<T, 4, 4, 4, 1>(g, c, stream);
-        case 5: return launch_pipe<T, 128, 64, 2, 2, 256>(g, c, stream);
-        case 6: return launch_pipe<T, 128, 128, 2, 2, 256>(g, c, stream);
-        case 7: return launch_pipe<T, 128, 128, 2, 2, 128>(g, c, stream);
-        default: return launch_pipe<T, 256, 256, 2, 4, 128>(g, c, stream);
+        case 4: return launch_pipe<T, 64, 64, 1, 4, 128, 4>(g, c, stream);
+        case 5: return launch_pipe<T, 64, 128, 1, 4, 128, 4>(g, c, stream);
+        case 6: return launch_pipe<T, 128, 128, 2, 4, 128, 4>(g, c, stream);
+        case 7: return launch_pipe<T, 128, 256, 2, 4, 128, 3>(g, c, stream);
+        default: return launch_pipe<T, 256, 256, 2, 4, 128, 2>(g, c, stream);
     }
 }
 

@@ -189,7 +189,9 @@ def test_matmul_large_tiles(qc, m, n, k, dtype):
 
 @pytest.mark.parametrize("m,n,k", [(3700, 3400, 1500), (2000, 1900, 1024), (1500, 2100, 641), (3584, 3840, 448),
                                    (9, 5000, 1333), (30, 4001, 2700), (60, 3900, 1100), (120, 4002, 2900),
-                                   (250, 3907, 1300), (500, 4000, 1601), (1000, 4003, 1700), (2000, 4000, 1111)])
+                                   (250, 3907, 1300), (500, 4000, 1601), (1000, 4003, 1700), (2000, 4000, 1111),
+                                   (256, 4096, 512), (250, 4000, 513), (512, 4096, 1024), (500, 4090, 385),
+                                   (1024, 4096, 1152), (1020, 4000, 640), (2048, 4096, 768), (2010, 3900, 897)])
 def test_matmul_large_tiles_long_k(qc, m, n, k):
     """The same over enough k for the steady state of the pipeline; codes small
     enough that every sum is below 2^24 and fp32 on the host exact."""
@@ -206,7 +208,8 @@ def test_matmul_large_tiles_long_k(qc, m, n, k):
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
 @pytest.mark.parametrize("more,skip", [(0, 0), (8, 0), (4, 0), (3, 0), (8, 2)])
-@pytest.mark.parametrize("m,n,k", [(500, 4000, 300), (1000, 4000, 260), (2000, 4000, 130), (3700, 3400, 70)])
+@pytest.mark.parametrize("m,n,k", [(250, 4000, 200), (500, 4000, 300), (1000, 4000, 260), (2000, 4000, 130),
+                                   (3700, 3400, 70)])
 def test_matmul_tile_stores(qc, m, n, k, more, skip, dtype):
     """Whole tiles of C at every alignment of its rows, each row and column
     with a scale of its own (powers of two, so fp32 is exact)."""
