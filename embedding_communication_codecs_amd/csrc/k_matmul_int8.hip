@@ -9,7 +9,7 @@
 //
 // Large products are bound by the matrix cores at the clock that the power
 // budget leaves them (random codes 2.3-2.8 POP/s, all zeros 3.4: 16384 x 8192
-// x 8192 785 us, 4096 x 4096 x 4096 55-59 us, their matrix cores busy three
+// x 8192 785 us, 4096 x 4096 x 4096 53 us, their matrix cores busy three
 // quarters of the time); a few tokens by the weights' bytes and one load's
 // latency (one token x 4096 x 4096 4.8 us, 16 MB at 3.5 TB/s).
 #include "qc_lds.hpp"
