@@ -571,7 +571,8 @@ k_ckpt8_wgrad_pipe_f32(Args g) {
     const int ycol = (int)min(n0 + yc * 4, last_piece);
     const int yover = max(ycol + 4 - (int)g.n, 0);  // values of it past n
     auto token_y = [&](int i) { return (w * YN + i) * 2 + (l >> 5); };
-    const int xt = w % XW * TOK + l / (BD / 16), xq = l % (BD / 16);  // this lane's token of a stage, and 16 codes of it
+    // this lane's token of a stage, and 16 codes of it
+    const int xt = w % XW * TOK + l / (BD / 16), xq = l % (BD / 16);
     const int xcol = (int)min(d0 + xq * 16, g.pitch - 16);
     const int ecol = (int)min((d0 + xq * 16) / 128 * 4, g.epitch - 4);
     int yoff[YN];
@@ -843,8 +844,10 @@ Plan plan_of(int64_t rows, int64_t n, int64_t dim, bool bf16) {
             if (want > units) break;
             const int64_t per = (units + want - 1) / want, splits = (units + per - 1) / per;
             const int64_t blocks = tiles * splits, rounds = (blocks + shape.slots - 1) / shape.slots;
-            double us = (double)rounds * (2.0 * (double)per * (blocks <= 256 ? shape.alone_us : shape.stage_us) + shape.store_us);
-            if (splits > 1) us += 2.8 + 0.1 * (double)splits + (double)(splits + 1) * (double)n * (double)dim * (4.0 / 8e6);
+            const double stage_us = blocks <= 256 ? shape.alone_us : shape.stage_us;
+            double us = (double)rounds * (2.0 * (double)per * stage_us + shape.store_us);
+            if (splits > 1)
+                us += 2.8 + 0.1 * (double)splits + (double)(splits + 1) * (double)n * (double)dim * (4.0 / 8e6);
             if (least == 0 || us < least) {
                 least = us;
                 best = Plan{shape.bd, (int32_t)splits, per * 64};

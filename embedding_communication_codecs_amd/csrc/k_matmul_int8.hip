@@ -140,7 +140,8 @@ k_mm_int8_pipe(Args g, T* __restrict__ c) {
     constexpr int NW = WN * WM, THREADS = NW * WAVE;
     constexpr int FN = BN / WN / 16, FM = BM / WM / 16;
     constexpr int AHEAD = FN >= 8 ? 3 : 2;                 // weight fragments read ahead (of a ring of 4)
-    constexpr int KK = K / 64, STEPS = KK * FN, TURN = STEPS - FN / 2;   // a step: one weight fragment; the barrier's step
+    constexpr int KK = K / 64, STEPS = KK * FN;            // a step: one weight fragment
+    constexpr int TURN = STEPS - FN / 2;                   // the barrier's step
     constexpr int TB = BN * K, STAGE = (BN + BM) * K;      // weights first, then tokens
     // a stage's last read comes before the barrier, the next one's first after it
     static_assert(FN % 4 == 0 && FM >= 1 && STEPS - 1 - AHEAD <= TURN && STEPS - AHEAD >= TURN, "tile shape");
@@ -293,8 +294,8 @@ k_mm_int8_pipe(Args g, T* __restrict__ c) {
 template <class T, int BN, int BM, int WN, int WM, int K, int NB>
 hipError_t launch_pipe(const Args& g, T* c, hipStream_t stream) {
     const int64_t tiles = ((g.n + BN - 1) / BN) * ((g.m + BM - 1) / BM);
-    hipLaunchKernelGGL((k_mm_int8_pipe<T, BN, BM, WN, WM, K, NB>), dim3((unsigned)tiles), dim3(WN * WM * WAVE), 0, stream, g,
-                       c);
+    hipLaunchKernelGGL((k_mm_int8_pipe<T, BN, BM, WN, WM, K, NB>), dim3((unsigned)tiles), dim3(WN * WM * WAVE), 0,
+                       stream, g, c);
     return hipGetLastError();
 }
 

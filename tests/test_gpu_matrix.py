@@ -345,8 +345,8 @@ def check_wgrad(got, dy, v, wtype, start=None):
     assert rel <= (4e-3 if wtype is BF16 else 1e-5), rel
 
 
-WG = [(2049, 64, 130), (4500, 264, 200), (1, 8, 16), (1, 1, 1), (5, 33, 70), (63, 16, 32), (64, 128, 128), (65, 130, 127), (130, 250, 500), (200, 64, 257),
-      (257, 384, 129), (1000, 40, 72), (3000, 64, 100), (515, 8, 300)]
+WG = [(2049, 64, 130), (4500, 264, 200), (1, 8, 16), (1, 1, 1), (5, 33, 70), (63, 16, 32), (64, 128, 128),
+      (65, 130, 127), (130, 250, 500), (200, 64, 257), (257, 384, 129), (1000, 40, 72), (3000, 64, 100), (515, 8, 300)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
