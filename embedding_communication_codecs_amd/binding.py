@@ -433,22 +433,42 @@ def qc_majority_vote(words, m, n, out_words, stream=None):
 # ------------------------------------------------------- matrix operators
 
 
-def _mat(t, rows, cols, ld, esize, name):
+class _Dtypes(dict):
+    """torch dtypes that a tensor may have, by the type the call states or
+    "codes"; filled at its first use, as importing this module does not import
+    torch.  Any will do for a type that does not exist: the library refuses it."""
+
+    def __missing__(self, kind):
+        import torch
+
+        self.update({QC_F32: (torch.float32,), QC_BF16: (torch.bfloat16,), "codes": (torch.int8, torch.uint8)})
+        return self.setdefault(kind, ())
+
+
+_dtypes = _Dtypes()
+
+
+def _typed(t, kind, name):
+    want = _dtypes[kind]
+    if want and t.dtype not in want:
+        raise ValueError(f"{name} is a tensor of {t.dtype}, the call takes {' or '.join(map(str, want))}")
+
+
+def _mat(t, rows, cols, ld, kind, name):
     """Device address of a [rows][cols] matrix with row stride ld (elements),
-    checking that the tensor has elements of esize bytes and memory for all of
-    it; it may be a view into a wider matrix."""
+    checking that the tensor has elements of that kind (QC_F32, QC_BF16,
+    "codes") and memory for all of it; it may be a view into a wider matrix."""
     if t is None:
         return None
     if isinstance(t, int):
         return t
     s = t.shape
     if (len(s) == 2 and t.is_cuda and t.stride() == (ld, 1) and s[0] >= rows and s[1] >= cols
-            and t.element_size() == esize):
+            and t.dtype in _dtypes[kind]):
         return t.data_ptr()  # the common case; what follows finds out what is wrong, or that nothing is
+    _typed(t, kind, name)
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if t.element_size() != esize:
-        raise ValueError(f"{name} has elements of {t.element_size()} bytes, the call takes {esize}")
     if t.dim() > 2 and not t.is_contiguous():
         raise ValueError(f"{name} must be a matrix, or contiguous")
     if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
@@ -456,21 +476,24 @@ def _mat(t, rows, cols, ld, esize, name):
     if t.dim() == 2 and t.shape[0] > 1 and t.stride(0) != ld:
         raise ValueError(f"{name} has a row stride of {t.stride(0)}, the call says {ld}")
     if rows > 0 and cols > 0:
-        have = t.untyped_storage().nbytes() // esize - t.storage_offset()
+        have = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
         need = (rows - 1) * ld + cols
         if have < need:
             raise ValueError(f"{name} holds {have} elements, the call needs {need}")
     return t.data_ptr()
 
 
-def _esize(qtype):
-    return 2 if qtype == QC_BF16 else 4
+def _vec(t, count, kind, name):
+    """Device address of `count` contiguous elements of that kind."""
+    if t is not None and not isinstance(t, int):
+        _typed(t, kind, name)
+    return _ptr(t, count * (1 if kind == "codes" else 4), name)
 
 
 def _ckpt(codes, exps, rows, dim, name):
     cb = rows * (-(-dim // QC_CKPT_GROUP) * QC_CKPT_GROUP)
     eb = rows * (-(-dim // (4 * QC_CKPT_GROUP)) * 4)
-    return _ptr(codes, cb, name + "codes"), _ptr(exps, eb, name + "exps")
+    return _vec(codes, cb, "codes", name + "codes"), _vec(exps, eb, "codes", name + "exps")
 
 
 def ckpt8_bytes(rows: int, dim: int) -> tuple[int, int]:
@@ -485,27 +508,27 @@ qc_ckpt8_bytes = ckpt8_bytes
 
 def qc_encode_int8_rowwise(x, xtype, rows, dim, ldx, codes, ldq, scale, stream=None):
     _check(lib().qc_encode_int8_rowwise(
-        _mat(x, rows, dim, ldx, _esize(xtype), "x"), xtype, rows, dim, ldx,
-        _mat(codes, rows, -(-dim // 16) * 16, ldq, 1, "codes"), ldq, _ptr(scale, 4 * max(rows, 0), "scale"),
+        _mat(x, rows, dim, ldx, xtype, "x"), xtype, rows, dim, ldx,
+        _mat(codes, rows, -(-dim // 16) * 16, ldq, "codes", "codes"), ldq, _vec(scale, max(rows, 0), QC_F32, "scale"),
         _stream(stream)))
 
 
 def qc_matmul_int8(a, a_scale, lda, b, b_scale, ldb, m, n, k, c, ctype, ldc, stream=None):
     kp = -(-k // 16) * 16
     _check(lib().qc_matmul_int8(
-        _mat(a, m, kp, lda, 1, "a"), _ptr(a_scale, 4 * max(m, 0), "a_scale"), lda,
-        _mat(b, n, kp, ldb, 1, "b"), _ptr(b_scale, 4 * max(n, 0), "b_scale"), ldb, m, n, k,
-        _mat(c, m, n, ldc, _esize(ctype), "c"), ctype, ldc, _stream(stream)))
+        _mat(a, m, kp, lda, "codes", "a"), _vec(a_scale, max(m, 0), QC_F32, "a_scale"), lda,
+        _mat(b, n, kp, ldb, "codes", "b"), _vec(b_scale, max(n, 0), QC_F32, "b_scale"), ldb, m, n, k,
+        _mat(c, m, n, ldc, ctype, "c"), ctype, ldc, _stream(stream)))
 
 
 def qc_encode_ckpt8(x, xtype, rows, dim, ldx, codes, exps, stream=None):
-    _check(lib().qc_encode_ckpt8(_mat(x, rows, dim, ldx, _esize(xtype), "x"), xtype, rows, dim, ldx,
+    _check(lib().qc_encode_ckpt8(_mat(x, rows, dim, ldx, xtype, "x"), xtype, rows, dim, ldx,
                                  *_ckpt(codes, exps, rows, dim, ""), _stream(stream)))
 
 
 def qc_decode_ckpt8(codes, exps, rows, dim, out, otype, ldo, stream=None):
     _check(lib().qc_decode_ckpt8(*_ckpt(codes, exps, rows, dim, ""), rows, dim,
-                                 _mat(out, rows, dim, ldo, _esize(otype), "out"), otype, ldo, _stream(stream)))
+                                 _mat(out, rows, dim, ldo, otype, "out"), otype, ldo, _stream(stream)))
 
 
 def qc_ckpt8_wgrad_workspace(rows, n, dim, dytype) -> int:
@@ -523,26 +546,24 @@ def qc_ckpt8_wgrad(dy, dytype, ldy, codes, exps, rows, n, dim, dw, wtype, ldw, a
     if workspace is not None and isinstance(workspace, int):
         raise ValueError("workspace must be a GPU tensor")
     _check(lib().qc_ckpt8_wgrad(
-        _mat(dy, rows, n, ldy, _esize(dytype), "dy"), dytype, ldy, *_ckpt(codes, exps, rows, dim, ""), rows, n, dim,
-        _mat(dw, n, dim, ldw, _esize(wtype), "dw"), wtype, ldw, 1 if accumulate else 0,
+        _mat(dy, rows, n, ldy, dytype, "dy"), dytype, ldy, *_ckpt(codes, exps, rows, dim, ""), rows, n, dim,
+        _mat(dw, n, dim, ldw, wtype, "dw"), wtype, ldw, 1 if accumulate else 0,
         _ptr(workspace, None, "workspace"), 0 if workspace is None else _bytes(workspace), _stream(stream)))
 
 
 def qc_swiglu_ckpt8(gate, up, xtype, ldx, rows, dim, h, ldh, gate_codes, gate_exps, up_codes, up_exps, stream=None):
-    es = _esize(xtype)
     _check(lib().qc_swiglu_ckpt8(
-        _mat(gate, rows, dim, ldx, es, "gate"), _mat(up, rows, dim, ldx, es, "up"), xtype, ldx, rows, dim,
-        _mat(h, rows, dim, ldh, es, "h"), ldh, *_ckpt(gate_codes, gate_exps, rows, dim, "gate_"),
+        _mat(gate, rows, dim, ldx, xtype, "gate"), _mat(up, rows, dim, ldx, xtype, "up"), xtype, ldx, rows, dim,
+        _mat(h, rows, dim, ldh, xtype, "h"), ldh, *_ckpt(gate_codes, gate_exps, rows, dim, "gate_"),
         *_ckpt(up_codes, up_exps, rows, dim, "up_"), _stream(stream)))
 
 
 def qc_swiglu_ckpt8_backward(dh, dhtype, lddh, gate_codes, gate_exps, up_codes, up_exps, rows, dim, dgate, dup, ldg,
                              stream=None):
-    es = _esize(dhtype)
     _check(lib().qc_swiglu_ckpt8_backward(
-        _mat(dh, rows, dim, lddh, es, "dh"), dhtype, lddh, *_ckpt(gate_codes, gate_exps, rows, dim, "gate_"),
-        *_ckpt(up_codes, up_exps, rows, dim, "up_"), rows, dim, _mat(dgate, rows, dim, ldg, es, "dgate"),
-        _mat(dup, rows, dim, ldg, es, "dup"), ldg, _stream(stream)))
+        _mat(dh, rows, dim, lddh, dhtype, "dh"), dhtype, lddh, *_ckpt(gate_codes, gate_exps, rows, dim, "gate_"),
+        *_ckpt(up_codes, up_exps, rows, dim, "up_"), rows, dim, _mat(dgate, rows, dim, ldg, dhtype, "dgate"),
+        _mat(dup, rows, dim, ldg, dhtype, "dup"), ldg, _stream(stream)))
 
 
 def qc_payload_bytes(fmt, n, group, bits) -> int:
