@@ -454,16 +454,17 @@ def _typed(t, kind, name):
         raise ValueError(f"{name} is a tensor of {t.dtype}, the call takes {' or '.join(map(str, want))}")
 
 
-def _mat(t, rows, cols, ld, kind, name):
+def _mat(t, rows, cols, ld, kind, name, padding=0):
     """Device address of a [rows][cols] matrix with row stride ld (elements),
     checking that the tensor has elements of that kind (QC_F32, QC_BF16,
-    "codes") and memory for all of it; it may be a view into a wider matrix."""
+    "codes") and holds all of it; it may be a view into a wider matrix.  The
+    padding after each row's cols may lie behind a view, in the same rows."""
     if t is None:
         return None
     if isinstance(t, int):
         return t
     s = t.shape
-    if (len(s) == 2 and t.is_cuda and t.stride() == (ld, 1) and s[0] >= rows and s[1] >= cols
+    if (len(s) == 2 and t.is_cuda and t.stride() == (ld, 1) and s[0] >= rows and s[1] >= cols + padding
             and t.dtype in _dtypes[kind]):
         return t.data_ptr()  # the common case; what follows finds out what is wrong, or that nothing is
     _typed(t, kind, name)
@@ -476,8 +477,13 @@ def _mat(t, rows, cols, ld, kind, name):
     if t.dim() == 2 and t.shape[0] > 1 and t.stride(0) != ld:
         raise ValueError(f"{name} has a row stride of {t.stride(0)}, the call says {ld}")
     if rows > 0 and cols > 0:
-        have = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
-        need = (rows - 1) * ld + cols
+        need = (rows - 1) * ld + cols + padding
+        if t.dim() == 2 and t.shape[0] > 1:
+            if t.shape[0] < rows or t.shape[1] < cols:
+                raise ValueError(f"{name} holds {t.shape[0]} x {t.shape[1]} elements, the call needs {rows} x {cols}")
+            have = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
+        else:
+            have = t.numel()
         if have < need:
             raise ValueError(f"{name} holds {have} elements, the call needs {need}")
     return t.data_ptr()
@@ -509,15 +515,14 @@ qc_ckpt8_bytes = ckpt8_bytes
 def qc_encode_int8_rowwise(x, xtype, rows, dim, ldx, codes, ldq, scale, stream=None):
     _check(lib().qc_encode_int8_rowwise(
         _mat(x, rows, dim, ldx, xtype, "x"), xtype, rows, dim, ldx,
-        _mat(codes, rows, -(-dim // 16) * 16, ldq, "codes", "codes"), ldq, _vec(scale, max(rows, 0), QC_F32, "scale"),
+        _mat(codes, rows, dim, ldq, "codes", "codes", -dim % 16), ldq, _vec(scale, max(rows, 0), QC_F32, "scale"),
         _stream(stream)))
 
 
 def qc_matmul_int8(a, a_scale, lda, b, b_scale, ldb, m, n, k, c, ctype, ldc, stream=None):
-    kp = -(-k // 16) * 16
     _check(lib().qc_matmul_int8(
-        _mat(a, m, kp, lda, "codes", "a"), _vec(a_scale, max(m, 0), QC_F32, "a_scale"), lda,
-        _mat(b, n, kp, ldb, "codes", "b"), _vec(b_scale, max(n, 0), QC_F32, "b_scale"), ldb, m, n, k,
+        _mat(a, m, k, lda, "codes", "a", -k % 16), _vec(a_scale, max(m, 0), QC_F32, "a_scale"), lda,
+        _mat(b, n, k, ldb, "codes", "b", -k % 16), _vec(b_scale, max(n, 0), QC_F32, "b_scale"), ldb, m, n, k,
         _mat(c, m, n, ldc, ctype, "c"), ctype, ldc, _stream(stream)))
 
 

@@ -120,3 +120,50 @@ def test_codes_of_another_type(qc, call, name):
     for dtype in (I8, U8):
         with pytest.raises(Reached):
             call(qc, **{name: dtype})
+
+
+def out(qc, t, rows=3, dim=40, ldo=40):
+    qc.qc_decode_ckpt8(T((rows, 64), I8), T((rows, 4), U8), rows, dim, OnGpu(t), 0, ldo, stream=0)
+
+
+@pytest.mark.parametrize("view,ldo", [
+    (lambda: torch.zeros(9, 40)[:2], 40),             # a row short; there are rows below
+    (lambda: torch.zeros(9, 64)[:, :39], 64),         # a column short; there are columns beside
+    (lambda: torch.zeros(9, 64)[2:4, 8:48], 64),
+    (lambda: torch.zeros(500)[100:219], 40),          # an element short, flat
+    (lambda: torch.zeros(500)[100:219].view(1, 119), 40),
+    (lambda: torch.zeros(9, 2, 20)[:2], 40),
+    (lambda: torch.zeros(500)[:0], 40),
+    (lambda: torch.zeros(500)[7], 40),
+], ids=str)
+def test_views_smaller_than_the_call(qc, view, ldo):
+    """What lies beside a view is not the call's to write."""
+    with pytest.raises(ValueError, match="out holds"):
+        out(qc, view(), ldo=ldo)
+
+
+@pytest.mark.parametrize("view,ldo", [
+    (lambda: torch.zeros(9, 40)[4:7], 40), (lambda: torch.zeros(9, 64)[:3, 8:48], 64),
+    (lambda: torch.zeros(500)[100:220], 40), (lambda: torch.zeros(500)[100:268], 64),
+    (lambda: torch.zeros(1, 500)[:, :120], 40), (lambda: torch.zeros(3, 2, 20), 40),
+], ids=str)
+def test_views_large_enough_pass(qc, view, ldo):
+    with pytest.raises(Reached):
+        out(qc, view(), ldo=ldo)
+
+
+def test_codes_without_their_padding(qc):
+    """Codes may be a view that ends at k, where the padding up to 16 lies behind it in the same rows."""
+    a, b = torch.zeros((3, 48), dtype=I8), torch.zeros((5, 64), dtype=I8)
+
+    def args(a, b, m=3):
+        return OnGpu(a), T(4, F32), 48, OnGpu(b), T(5, F32), 64, m, 5, 40, T((4, 5), F32), 0, 5
+
+    with pytest.raises(Reached):
+        qc.qc_matmul_int8(*args(a[:, :40], b[:, :40]), stream=0)
+    with pytest.raises(ValueError, match="a holds"):  # the last row's padding is not there
+        qc.qc_matmul_int8(*args(torch.zeros(3 * 48 - 8, dtype=I8).as_strided((3, 40), (48, 1)), b), stream=0)
+    with pytest.raises(ValueError, match="a holds"):
+        qc.qc_matmul_int8(*args(torch.zeros((9, 48), dtype=I8)[:3, :40], b, 4), stream=0)
+    with pytest.raises(ValueError, match="a holds"):
+        qc.qc_matmul_int8(*args(a[:, :39], b), stream=0)
