@@ -428,7 +428,7 @@ int shape_of(int64_t m, int64_t n) {
         const Shape& s = kShapes[i];
         const int64_t blocks = ((n + s.bn - 1) / s.bn) * ((m + s.bm - 1) / s.bm);
         const double us = (double)((blocks + kUnits - 1) / kUnits) * s.round_us;
-        if (us < least && blocks < int64_t(1) << 23) {  // a grid has fewer than 2^32 threads
+        if (us < least && blocks < int64_t(1) << 23) {  // a grid has fewer than 2^32 threads; the last shape has
             best = i;
             least = us;
         }

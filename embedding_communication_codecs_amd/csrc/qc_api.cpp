@@ -501,6 +501,10 @@ namespace {
 constexpr int64_t kMaxMatrixElems = int64_t(1) << 56;
 constexpr int64_t kMaxProductStride = int64_t(1) << 23;  // 32-bit offsets inside a tile
 constexpr int64_t kMaxTiles = (int64_t(1) << 31) - 1;
+// A grid has fewer than 2^32 threads: 512 for a tile of 256 x 256 of the INT8
+// product, 256 for 2,048 values of a checkpoint's row.
+constexpr int64_t kMaxProductTiles = (int64_t(1) << 23) - 1;
+constexpr int64_t kMaxCkptDim = int64_t(1) << 34;
 
 bool bad_type(int32_t t) { return t != QC_F32 && t != QC_BF16; }
 
@@ -539,7 +543,7 @@ int qc_matmul_int8(const int8_t* a, const float* a_scale, int64_t lda, const int
     if (m == 0 || n == 0) return QC_OK;
     if (bad_matrix(m, n, ldc) || !a || !a_scale || !b || !b_scale || !c) return QC_ERR_ARG;
     if (k > 131071 || lda > kMaxProductStride || ldb > kMaxProductStride) return QC_ERR_UNSUPPORTED;
-    if (ceil_div(m, 16) > kMaxTiles / ceil_div(n, 16)) return QC_ERR_ARG;
+    if (ceil_div(m, 256) > kMaxProductTiles / ceil_div(n, 256)) return QC_ERR_ARG;
     if (misaligned(a) || misaligned(b) || misaligned4(a_scale) || misaligned4(b_scale) || misaligned_for(c, ctype))
         return QC_ERR_ALIGN;
     return launched(qc::launch_matmul_int8(a, a_scale, lda, b, b_scale, ldb, m, n, k, c, ctype == QC_BF16, ldc,
@@ -559,6 +563,7 @@ int qc_encode_ckpt8(const void* x, int32_t xtype, int64_t rows, int64_t dim, int
     if (bad_type(xtype) || bad_matrix(rows, dim, ldx)) return QC_ERR_ARG;
     if (rows == 0) return QC_OK;
     if (!x || !codes || !exps) return QC_ERR_ARG;
+    if (dim > kMaxCkptDim) return QC_ERR_UNSUPPORTED;
     if (misaligned_for(x, xtype) || misaligned(codes) || misaligned(exps)) return QC_ERR_ALIGN;
     return launched(qc::launch_encode_ckpt8(x, xtype == QC_BF16, ldx, rows, dim, codes, exps, hs(stream)));
 }
@@ -568,6 +573,7 @@ int qc_decode_ckpt8(const int8_t* codes, const uint8_t* exps, int64_t rows, int6
     if (bad_type(otype) || bad_matrix(rows, dim, ldo)) return QC_ERR_ARG;
     if (rows == 0) return QC_OK;
     if (!codes || !exps || !out) return QC_ERR_ARG;
+    if (dim > kMaxCkptDim) return QC_ERR_UNSUPPORTED;
     if (misaligned(codes) || misaligned(exps) || misaligned_for(out, otype)) return QC_ERR_ALIGN;
     return launched(qc::launch_decode_ckpt8(codes, exps, rows, dim, out, otype == QC_BF16, ldo, hs(stream)));
 }
@@ -610,6 +616,7 @@ int qc_swiglu_ckpt8(const void* gate, const void* up, int32_t xtype, int64_t ldx
     if (bad_type(xtype) || bad_matrix(rows, dim, ldx) || bad_matrix(rows, dim, ldh)) return QC_ERR_ARG;
     if (rows == 0) return QC_OK;
     if (!gate || !up || !h || !gate_codes || !gate_exps || !up_codes || !up_exps) return QC_ERR_ARG;
+    if (dim > kMaxCkptDim) return QC_ERR_UNSUPPORTED;
     if (misaligned_for(gate, xtype) || misaligned_for(up, xtype) || misaligned_for(h, xtype) ||
         misaligned(gate_codes) || misaligned(gate_exps) || misaligned(up_codes) || misaligned(up_exps))
         return QC_ERR_ALIGN;
@@ -623,6 +630,7 @@ int qc_swiglu_ckpt8_backward(const void* dh, int32_t dhtype, int64_t lddh, const
     if (bad_type(dhtype) || bad_matrix(rows, dim, lddh) || bad_matrix(rows, dim, ldg)) return QC_ERR_ARG;
     if (rows == 0) return QC_OK;
     if (!dh || !gate_codes || !gate_exps || !up_codes || !up_exps || !dgate || !dup) return QC_ERR_ARG;
+    if (dim > kMaxCkptDim) return QC_ERR_UNSUPPORTED;
     if (misaligned_for(dh, dhtype) || misaligned_for(dgate, dhtype) || misaligned_for(dup, dhtype) ||
         misaligned(gate_codes) || misaligned(gate_exps) || misaligned(up_codes) || misaligned(up_exps))
         return QC_ERR_ALIGN;

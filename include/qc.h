@@ -564,8 +564,8 @@ int qc_encode_int8_rowwise(const void* x, int32_t xtype, int64_t rows, int64_t d
  *   k           1 .. 131071 (codes may be -128: 131071 * 128^2 < 2^31).
  *   c           [m][n] of type ctype, row stride ldc, written.
  * Errors: ARG (NULL pointer, bad type, m or n < 0, k < 1, a stride below its
- *         row or not a multiple of 16), ALIGN, UNSUPPORTED (k or a stride
- *         above its limit).
+ *         row or not a multiple of 16, ceil(m / 256) * ceil(n / 256) at 2^23
+ *         or above), ALIGN, UNSUPPORTED (k or a stride above its limit).
  */
 int qc_matmul_int8(const int8_t* a, const float* a_scale, int64_t lda, const int8_t* b, const float* b_scale,
                    int64_t ldb, int64_t m, int64_t n, int64_t k, void* c, int32_t ctype, int64_t ldc,
@@ -590,7 +590,7 @@ int qc_matmul_int8(const int8_t* a, const float* a_scale, int64_t lda, const int
  * qc_decode_ckpt8 writes the values; bf16 output is exact for what
  * qc_encode_ckpt8 wrote.
  * Errors: ARG (NULL pointer, bad type, rows < 0, dim < 1, a stride below its
- *         row), ALIGN.
+ *         row), ALIGN, UNSUPPORTED (dim above 2^34, not for qc_ckpt8_bytes).
  */
 #define QC_CKPT_GROUP 32
 int qc_ckpt8_bytes(int64_t rows, int64_t dim, int64_t* code_bytes, int64_t* exp_bytes);
@@ -639,7 +639,7 @@ int qc_ckpt8_wgrad(const void* dy, int32_t dytype, int64_t ldy, const int8_t* co
  *   dh          [rows][dim] of type dhtype, row stride lddh.
  *   dgate, dup  [rows][dim], the same type, both with row stride ldg, written.
  * Errors: ARG (NULL pointer, bad type, rows < 0, dim < 1, a stride below its
- *         row), ALIGN.
+ *         row), ALIGN, UNSUPPORTED (dim above 2^34).
  */
 int qc_swiglu_ckpt8(const void* gate, const void* up, int32_t xtype, int64_t ldx, int64_t rows, int64_t dim, void* h,
                     int64_t ldh, int8_t* gate_codes, uint8_t* gate_exps, int8_t* up_codes, uint8_t* up_exps,
