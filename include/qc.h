@@ -586,7 +586,8 @@ int qc_matmul_int8(const int8_t* a, const float* a_scale, int64_t lda, const int
  *          past dim).
  *   exps   uint8, row pitch 4 * ceil(dim / 128) bytes, written entirely
  *          (zeros past the last group).
- * qc_ckpt8_bytes gives the bytes of both for a matrix (-1 for bad sizes).
+ * qc_ckpt8_bytes gives the bytes of both for a matrix; for sizes that are bad
+ * (ARG) it leaves *code_bytes and *exp_bytes as they are.
  * qc_decode_ckpt8 writes the values; bf16 output is exact for what
  * qc_encode_ckpt8 wrote.
  * Errors: ARG (NULL pointer, bad type, rows < 0, dim < 1, a stride below its
@@ -616,6 +617,8 @@ int qc_decode_ckpt8(const int8_t* codes, const uint8_t* exps, int64_t rows, int6
  *               (NULL if that is 0), used during the call: where rows are
  *               many and n * dim small, the tokens are split over several
  *               blocks, whose sums are held there until they are joined.
+ *               qc_ckpt8_wgrad_workspace() is -1, no status, for a bad type
+ *               or bad sizes.
  * Errors: ARG (NULL pointer, bad type, rows or n < 0, dim < 1, a stride below
  *         its row, too little workspace), ALIGN, UNSUPPORTED (accumulate with
  *         a bf16 dw, ldy or dim above 2^23).

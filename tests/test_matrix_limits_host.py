@@ -27,3 +27,13 @@ def test_sizes_of_long_rows(qc):  # noqa: F811
     c = ctypes.c_int64()
     assert qc.ckpt8_bytes(1, 1 << 34) == (1 << 34, 1 << 29)
     assert qc.lib().qc_ckpt8_bytes(1, 1 << 57, ctypes.byref(c), ctypes.byref(c)) == ARG
+
+
+def test_sizes_that_are_bad(qc):  # noqa: F811
+    """qc_ckpt8_bytes answers with a status and writes nothing; the workspace's size is -1."""
+    cb, eb = ctypes.c_int64(-7), ctypes.c_int64(-7)
+    for rows, dim in ((-1, 8), (1, 0), (1 << 57, 8), (1, 1 << 57)):
+        assert qc.lib().qc_ckpt8_bytes(rows, dim, ctypes.byref(cb), ctypes.byref(eb)) == ARG
+        assert (cb.value, eb.value) == (-7, -7)
+    for args in ((-1, 8, 8, 0), (8, -1, 8, 0), (8, 8, 0, 0), (8, 8, 8, 7), (1 << 57, 8, 8, 0)):
+        assert qc.lib().qc_ckpt8_wgrad_workspace(*args) == -1
