@@ -5,7 +5,8 @@
 // X's values are exact in bf16, so they go to v_mfma_f32_16x16x32_bf16 as
 // they are and every product is exact in fp32: nothing is rounded but the
 // fp32 sums.  A bf16 dY goes in as it is too; an fp32 dY as three bf16
-// pieces of 8 mantissa bits each, which add up to it exactly.
+// pieces of 8 mantissa bits each, which add up to it exactly; bits of it that
+// are too small for a bf16 value are added afterwards (add_rest).
 //
 // Both operands are summed over their slow axis.  Tiles of 32 tokens (64 in
 // the simple kernel) lie in LDS as [token][channel] and are read with
@@ -58,8 +59,9 @@ __device__ __forceinline__ u32x2 held4(uint32_t word, float step) {
 }
 
 // The three pieces of an fp32 value (8 mantissa bits each, cut off, so their
-// sum is exact); an infinity or a NaN is its first piece alone.
-__device__ __forceinline__ void pieces(float x, uint32_t (&p)[3]) {
+// sum is exact); an infinity or a NaN is its first piece alone.  `lost`
+// gathers the bits that the third leaves (its lower 16).
+__device__ __forceinline__ void pieces(float x, uint32_t (&p)[3], uint32_t& lost) {
     const uint32_t b = __float_as_uint(x);
     if ((b & kInfBits) == kInfBits) {
         p[0] = bf16_bits(x);
@@ -70,7 +72,90 @@ __device__ __forceinline__ void pieces(float x, uint32_t (&p)[3]) {
     const uint32_t rb = __float_as_uint(r);
     p[0] = b >> 16;
     p[1] = rb >> 16;
-    p[2] = __float_as_uint(r - __uint_as_float(rb & 0xFFFF0000u)) >> 16;
+    const uint32_t last = __float_as_uint(r - __uint_as_float(rb & 0xFFFF0000u));
+    p[2] = last >> 16;
+    lost |= last;
+}
+
+// What the three pieces leave of an fp32 gradient: bf16 has no bits below
+// 2^-133, so where a gradient below 2^-110 has some, no piece takes them.
+__device__ __forceinline__ float rest_of(float x) {
+    if ((__float_as_uint(x) & kInfBits) == kInfBits) return 0.0f;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) x -= __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
+    return x;
+}
+
+// Adds those remainders' products to a wave's sums (their layout: store_dw)
+// in fp32 multiply-adds; a remainder has 16 bits and X 8, so the products
+// are exact.  Only blocks that met a remainder call this: the wave looks for
+// its tokens that have one among its channels, a token for 16 lanes, and
+// multiplies for those, four at a time.  4096 x 4096 x 4096 of normal gradients
+// 347 us (344 without the look at their bits); one in a million of them at
+// 1e-36, in every block then, 655; one in a thousand 1,230.
+template <int FN, int FD>
+__device__ __forceinline__ void add_rest(const Args& g, f32x4 (&acc)[FD][FN], int64_t n0, int64_t d0, int64_t t_first,
+                                         int64_t t_end) {
+    constexpr uint32_t kBelow = (127u - 110u) << 24;  // 2^-110's bits, shifted as below
+    const int l = lane_id();
+    const float* column[FN];  // this lane's channels; those past n repeat the last one (sums that are not stored)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+        column[j] = static_cast<const float*>(g.dy) + min(n0 + j * 16 + (l & 15), g.n - 1);
+    auto gradient = [&](int64_t t, int j) {
+        const float x = column[j][min(t, t_end - 1) * g.ldy];  // without a branch: the loads are on their way together
+        return t < t_end ? x : 0.0f;
+    };
+    for (int64_t t0 = t_first; t0 < t_end; t0 += 32) {
+        bool small[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            uint32_t least = ~0u;  // of the magnitudes' bits less one: zeros are the largest
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                least = min(least, (__float_as_uint(gradient(t0 + 4 * u + (l >> 4), j)) << 1) - 1u);
+            small[u] = least < kBelow;
+        }
+        uint32_t tokens = 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const uint64_t lanes = __ballot(small[u]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tokens |= (lanes >> (16 * q) & 0xFFFFu) ? 1u << (4 * u + q) : 0u;
+        }
+        while (tokens) {
+            float r[4][FN], step[4][FD];
+            uint32_t word[4][FD];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                // none left: a token past the end, whose gradients read as zeros
+                const int64_t t = tokens ? t0 + __ffs((int)tokens) - 1 : t_end;
+                tokens &= tokens - 1u;
+#pragma unroll
+                for (int j = 0; j < FN; ++j) r[u][j] = gradient(t, j);
+#pragma unroll
+                for (int i = 0; i < FD; ++i) {
+                    // past the row: sums that are not stored
+                    const int64_t tx = min(t, t_end - 1), d = min(d0 + 16 * i + 4 * (l >> 4), g.pitch - 4);
+                    word[u][i] = *reinterpret_cast<const uint32_t*>(g.codes + tx * g.pitch + d);
+                    step[u][i] = ckpt_step(g.exps[tx * g.epitch + d / 32]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+#pragma unroll
+                for (int j = 0; j < FN; ++j) r[u][j] = rest_of(r[u][j]);
+#pragma unroll
+                for (int i = 0; i < FD; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float x = code_of(word[u][i], e) * step[u][i];
+#pragma unroll
+                        for (int j = 0; j < FN; ++j) acc[i][j][e] = __builtin_fmaf(r[u][j], x, acc[i][j][e]);
+                    }
+            }
+        }
+    }
 }
 
 // A wave's sums to dW.  Lane l holds output channel l % 16 of each of FN
@@ -137,6 +222,7 @@ k_ckpt8_wgrad(Args g) {
     constexpr int XG = TK * BD / 32 / THREADS;   // groups of X a thread converts
     static_assert(XG >= 1, "a group for every thread");
     __shared__ __align__(1024) uint8_t lds[2 * TILE];
+    __shared__ int rest;  // some gradient of the block has more bits than its pieces
 
     const int64_t tn = (g.n + BN - 1) / BN;
     const int64_t n0 = ((int64_t)blockIdx.x % tn) * BN, d0 = ((int64_t)blockIdx.x / tn) * BD;
@@ -184,6 +270,7 @@ k_ckpt8_wgrad(Args g) {
     // ---- dY
     constexpr int YC = TK * BN / 8 / THREADS;  // pieces of 8 values a thread stages
     float yv[YC][8];
+    uint32_t lost = 0;
     auto y_get = [&](int64_t t0) {
 #pragma unroll
         for (int i = 0; i < YC; ++i) {
@@ -206,8 +293,8 @@ k_ckpt8_wgrad(Args g) {
                     o[0][h] = (__float_as_uint(yv[i][2 * h]) >> 16) | (__float_as_uint(yv[i][2 * h + 1]) & 0xFFFF0000u);
                 } else {
                     uint32_t a[3], b[3];
-                    pieces(yv[i][2 * h], a);
-                    pieces(yv[i][2 * h + 1], b);
+                    pieces(yv[i][2 * h], a, lost);
+                    pieces(yv[i][2 * h + 1], b, lost);
 #pragma unroll
                     for (int q = 0; q < P; ++q) o[q][h] = a[q] | (b[q] << 16);
                 }
@@ -216,6 +303,7 @@ k_ckpt8_wgrad(Args g) {
             for (int q = 0; q < P; ++q)
                 *reinterpret_cast<u32x4*>(tile + q * YT + at) = u32x4{o[q][0], o[q][1], o[q][2], o[q][3]};
         }
+        if (P == 3 && (lost & 0xFFFFu)) rest = 1;
     };
 
     // ---- fragments: lane l reads 8 bytes of token r*16 + l/4, 16 channels
@@ -251,6 +339,10 @@ k_ckpt8_wgrad(Args g) {
 
     if (t_first < t_end) {
         y_get(t_first);
+        if (P == 3) {
+            if (threadIdx.x == 0) rest = 0;
+            __syncthreads();
+        }
         y_put(lds);
         x_get(t_first);
         x_put(lds + P * YT);
@@ -268,14 +360,16 @@ k_ckpt8_wgrad(Args g) {
                 y_put(lds + (buf ^ 1) * TILE);
             }
         }
+        // set before the last barrier, if at all
+        if (P == 3 && rest) add_rest<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16, t_first, t_end);
     }
 
     store_dw<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16);
 }
 
-// The same of four neighbours, packed (word 0 holds values 0 and 1), without
+// As pieces, of four neighbours, packed (word 0 holds values 0 and 1), without
 // a branch.
-__device__ __forceinline__ void pieces4(f32x4 x, u32x2 (&q)[3]) {
+__device__ __forceinline__ void pieces4(f32x4 x, u32x2 (&q)[3], uint32_t& lost) {
     auto upper = [](uint32_t lo, uint32_t hi) { return __builtin_amdgcn_perm(hi, lo, 0x07060302u); };
     uint32_t b[4];
 #pragma unroll
@@ -289,6 +383,7 @@ __device__ __forceinline__ void pieces4(f32x4 x, u32x2 (&q)[3]) {
                 x[e] = i > 1 || __builtin_isfinite(x[e]) ? r : 0.0f;  // an infinity is its first piece alone
             }
             b[e] = __float_as_uint(x[e]);
+            if (i == 2) lost |= b[e];
         }
         q[i] = u32x2{upper(b[0], b[1]), upper(b[2], b[3])};
     }
@@ -550,6 +645,7 @@ k_ckpt8_wgrad_pipe_f32(Args g) {
     static_assert(YN * 1024 * NW == ST * BN * 4 && NW * WAVE * 8 * XH == ST * BD, "tile shape");
     constexpr int BUF = 3 * YT + XT, RAT = 2 * BUF;  // LDS: two buffers of tiles, three raw stages
     __shared__ __align__(1024) uint8_t lds[RAT + 3 * NW * RAW];
+    __shared__ int rest;  // some gradient of the block has more bits than its pieces
 
     const uint32_t tn = (uint32_t)((g.n + BN - 1) / BN), td = (uint32_t)((g.dim + BD - 1) / BD);
     const Tile2 tile = tile_of<8>(blockIdx.x, tn, td);
@@ -620,6 +716,7 @@ k_ckpt8_wgrad_pipe_f32(Args g) {
         raw_x = *reinterpret_cast<const u32x4*>(at + YN * 1024 + l * 16);
         raw_e = *reinterpret_cast<const uint32_t*>(at + YN * 1024 + 1024 + l * 4);
     };
+    uint32_t lost = 0;
     auto convert_y = [&](auto fast, int i, int s, int buf) {
         f32x4 r = raw_y[i];
         const int t = token_y(i);
@@ -636,7 +733,7 @@ k_ckpt8_wgrad_pipe_f32(Args g) {
             }
         }
         u32x2 q[3];
-        pieces4(r, q);
+        pieces4(r, q, lost);
         uint8_t* o = lds + buf * BUF + place(t, yc >> 1, YB) + 8 * (yc & 1);
 #pragma unroll
         for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x2*>(o + p * YT) = q[p];
@@ -690,6 +787,8 @@ k_ckpt8_wgrad_pipe_f32(Args g) {
                     }
                 } else {
                     if (j == 0) {
+                        // every gradient has been converted by the last stage
+                        if (!FAST && s + 1 == stages && (lost & 0xFFFFu)) rest = 1;
                         if (FAST || s + 3 < stages) lds_landed_but<LOADS>();
                         else lds_landed();
                         if (FAST || s + 2 < stages) read_raw(rot2);
@@ -709,6 +808,7 @@ k_ckpt8_wgrad_pipe_f32(Args g) {
     };
     static_assert(LOADS == FN, "a load a step");
     if (stages > 0) {
+        if (threadIdx.x == 0) rest = 0;
         load_all(0);
         if (stages > 1) load_all(1);
         if (stages > 2) load_all(2);
@@ -749,6 +849,7 @@ k_ckpt8_wgrad_pipe_f32(Args g) {
             if (s + 1 < stages) stage(integral_constant<int, 1>{}, std::false_type{}, s + 1, rot);
             turn();
         }
+        if (rest) add_rest<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16, t_first, t_first + tokens);
     }
     store_dw<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16);
 }

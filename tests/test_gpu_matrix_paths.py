@@ -94,3 +94,15 @@ def test_fp32_gradients_whole(qc, rows, n, dim):
     got, v = run_wgrad(qc, dy, ref.matrix(rows, dim, 2, F32))
     want = value[:, None] * v[at]
     assert np.all(np.abs(got.double().numpy() - want) <= 4 * U32 * np.abs(want))
+
+
+@pytest.mark.parametrize("rows,n,dim", PIECES)
+def test_fp32_gradients_whole_when_small(qc, rows, n, dim):
+    """The same where a gradient has bits below 2^-133, the smallest that bf16
+    has, and the products are normal numbers: gradients from 2^-126 to 2^-100,
+    and activations around 2^60."""
+    dy, at, value = one_token_a_channel(rows, n, -126, -100, 6)
+    got, v = run_wgrad(qc, dy, ref.matrix(rows, dim, 2, F32) * 2.0 ** 60)
+    want = value[:, None] * v[at]
+    off = np.abs(got.double().numpy() - want)
+    assert np.all(off <= 4 * U32 * np.abs(want)), (off / np.maximum(np.abs(want), 2.0 ** -126)).max()
