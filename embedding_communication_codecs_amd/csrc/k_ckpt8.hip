@@ -127,18 +127,21 @@ k_dec_ckpt8(KeptIn k, Sizes z, T* __restrict__ out, int64_t ldo) {
 
 // s = 1 / (1 + exp(-x)) and c = 1 - s.  With a = exp(-|x|), in (0, 1], r =
 // 1 / (1 + a): r and a * r are the two of them, the larger first, neither
-// from a difference.  a = 2^t (1 + d ln 2) with t = fl(-|x| log2 e) and d what
-// its rounding left, so that a's relative error does not grow with |x|;
-// below 2^-126 it becomes 0.  r takes one Newton step from the hardware's
-// reciprocal.  About 20 issue slots against 45 with expf and divisions,
-// which the forward pass was bound by (8192 x 8192: 106 us).
+// from a difference.  -|x| log2 e = n + f with n the nearest integer and f
+// from multiply-adds with log2 e's two parts, so that a = 2^f 2^n has a relative
+// error that does not grow with |x|.  The scaling by 2^n is apart, as the
+// hardware's 2^y is 0 where its result is below 2^-126: gates from -87 to -103
+// have a sigmoid that another factor can make a normal number.  r takes one Newton step from the hardware's reciprocal.  About 22
+// issue slots against 45 with expf and divisions, which the forward pass was
+// bound by (8192 x 8192: 106 us).
 __device__ __forceinline__ void sigmoid(float x, float& s, float& c) {
-    constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0c0p-26f, kLn2 = 0x1.62e430p-1f;
-    const float m = fminf(fabsf(x), 200.0f);  // an infinity has no such d
-    const float t = m * -kLog2e;
-    const float d = __builtin_fmaf(m, -kLog2eLow, __builtin_fmaf(m, -kLog2e, -t));
-    const float e = __builtin_amdgcn_exp2f(t);
-    const float a = __builtin_fmaf(e, d * kLn2, e);
+    constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0c0p-26f;
+    const float m = fminf(fabsf(x), 130.0f);  // n stays above -188
+    const float sum = __builtin_fmaf(m, -kLog2e, kWhole), n = sum - kWhole;
+    const float f = __builtin_fmaf(m, -kLog2eLow, __builtin_fmaf(m, -kLog2e, -n));
+    // 2^(n + 64), whose exponent field comes from the sum's low bits, then 2^-64
+    const float up = __uint_as_float((__float_as_uint(sum) + (127u + 64u)) << 23);
+    const float a = __builtin_amdgcn_exp2f(f) * up * 0x1p-64f;
     const float q = 1.0f + a, r0 = __builtin_amdgcn_rcpf(q);
     const float r = __builtin_fmaf(__builtin_fmaf(-q, r0, 1.0f), r0, r0);
     const float ar = a * r;
@@ -186,9 +189,10 @@ k_swiglu_ckpt8_bwd(const T* __restrict__ dh, int64_t lddh, KeptIn kg, KeptIn ku,
         for (int e = 0; e < 8; ++e) {
             float s, c;
             sigmoid(g[e], s, c);
-            const float ds = d[e] * s;
-            const float a = ds * u[e] * (1.0f + g[e] * c);
-            u[e] = ds * g[e];
+            // silu's derivative first: it is never above 1.1, where dh * U may
+            // overflow, and a subnormal s is rounded no further before it is scaled
+            const float a = d[e] * (s * (1.0f + g[e] * c)) * u[e];
+            u[e] = d[e] * s * g[e];
             g[e] = a;
         }
         store8(dgate + p.row * ldg + p.col, left_of(p, z), g);
