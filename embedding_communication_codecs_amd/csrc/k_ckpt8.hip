@@ -131,9 +131,10 @@ k_dec_ckpt8(KeptIn k, Sizes z, T* __restrict__ out, int64_t ldo) {
 // from multiply-adds with log2 e's two parts, so that a = 2^f 2^n has a relative
 // error that does not grow with |x|.  The scaling by 2^n is apart, as the
 // hardware's 2^y is 0 where its result is below 2^-126: gates from -87 to -103
-// have a sigmoid that another factor can make a normal number.  r takes one Newton step from the hardware's reciprocal.  About 22
-// issue slots against 45 with expf and divisions, which the forward pass was
-// bound by (8192 x 8192: 106 us).
+// have a sigmoid that another factor can make a normal number.  r takes one
+// Newton step from the hardware's reciprocal.  About 22 issue slots against
+// 45 with expf and divisions, which the forward pass was bound by (8192 x
+// 8192: 106 us).
 __device__ __forceinline__ void sigmoid(float x, float& s, float& c) {
     constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0c0p-26f;
     const float m = fminf(fabsf(x), 130.0f);  // n stays above -188

@@ -402,6 +402,13 @@ __device__ __forceinline__ void pieces4(f32x4 x, u32x2 (&q)[3], uint32_t& lost) 
 // As in the INT8 product, fragments are read ahead of their use and into
 // the next stage, and the only barrier of a stage stands in its middle.
 constexpr int ST = 32;  // tokens of a stage
+// Bytes a descriptor reaches from its stage's first row.  A stage's offsets stay
+// below 2^31 (32 rows at most 2^25 bytes apart); a negative one counts as 2^31 and
+// more, past the descriptor, and loads zeros.  Descriptors that end where the
+// matrix does cost scalar registers and 3 to 10% where stages are few (515 x 8 x
+// 300: 9.0 us against 8.3), so that no load passes a matrix' end rests on the
+// clamps below alone.
+constexpr int kReach = 0x7FFFFFFF;
 
 template <int BN, int BD, int WN, int WD>
 __global__ void __launch_bounds__(WN * WD * WAVE)
@@ -465,7 +472,7 @@ k_ckpt8_wgrad_pipe(Args g) {
             const int col = ycol(i, lane);
             off = (t * (int)g.ldy + (patch && t == last && col == last_col ? (int)g.n - 8 : col)) * 2;
         }
-        load_lds16(buffer_of(ybase + t0 * g.ldy * 2, -1), lds0 + (s & 3) * YT + (w * YN + i) * 1024, off, 0);
+        load_lds16(buffer_of(ybase + t0 * g.ldy * 2, kReach), lds0 + (s & 3) * YT + (w * YN + i) * 1024, off, 0);
     };
     auto x_load = [&](auto fast, int part, int s) {
         int64_t t0 = (int64_t)s * ST;
@@ -475,8 +482,8 @@ k_ckpt8_wgrad_pipe(Args g) {
             t = min(xt, (int)min(tokens - 1 - t0, (int64_t)ST));
         }
         const uint32_t at = lds0 + RAT + ((s & 3) * NW + w) * RAW;
-        if (part == 0) load_lds16(buffer_of(xbase + t0 * g.pitch, -1), at, t * (int)g.pitch + xcol, 0);
-        else load_lds4(buffer_of(ebase + t0 * g.epitch, -1), at + 1024, t * (int)g.epitch + ecol, 0);
+        if (part == 0) load_lds16(buffer_of(xbase + t0 * g.pitch, kReach), at, t * (int)g.pitch + xcol, 0);
+        else load_lds4(buffer_of(ebase + t0 * g.epitch, kReach), at + 1024, t * (int)g.epitch + ecol, 0);
     };
     auto load = [&](auto fast, int part, int batch) {  // one of the LOADS of a batch
         if (part < YN) y_load(fast, part, batch);
@@ -690,13 +697,13 @@ k_ckpt8_wgrad_pipe_f32(Args g) {
                 const int t = min(token_y(part), have - 1);
                 off = (t * (int)g.ldy + ycol - (t_first + t0 + t == g.rows - 1 ? yover : 0)) * 4;
             }
-            load_lds16(buffer_of(ybase + t0 * g.ldy * 4, -1), at + part * 1024, off, 0);
+            load_lds16(buffer_of(ybase + t0 * g.ldy * 4, kReach), at + part * 1024, off, 0);
         } else if (part == YN) {
             const int off = FAST ? xoff : min(xt, have - 1) * (int)g.pitch + xcol;
-            load_lds16(buffer_of(xbase + t0 * g.pitch, -1), at + YN * 1024, off, 0);
+            load_lds16(buffer_of(xbase + t0 * g.pitch, kReach), at + YN * 1024, off, 0);
         } else {
             const int off = FAST ? eoff : min(xt, have - 1) * (int)g.epitch + ecol;
-            load_lds4(buffer_of(ebase + t0 * g.epitch, -1), at + YN * 1024 + 1024, off, 0);
+            load_lds4(buffer_of(ebase + t0 * g.epitch, kReach), at + YN * 1024 + 1024, off, 0);
         }
     };
     auto load_all = [&](int s) {
@@ -801,7 +808,8 @@ k_ckpt8_wgrad_pipe_f32(Args g) {
                 }
 #pragma unroll
                 for (int i = 0; i < FD; ++i)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[P][i], fy[(P + p) & 1][j], acc[i][j], 0, 0, 0);
+                    acc[i][j] =
+                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[P][i], fy[(P + p) & 1][j], acc[i][j], 0, 0, 0);
                 __builtin_amdgcn_sched_barrier(0);  // keeps the reads where they stand, ahead of their use
             }
         }
