@@ -857,7 +857,7 @@ k_ckpt8_wgrad_pipe_f32(Args g) {
             if (s + 1 < stages) stage(integral_constant<int, 1>{}, std::false_type{}, s + 1, rot);
             turn();
         }
-        if (rest) add_rest<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16, t_first, t_first + tokens);
+        if (__builtin_expect(rest, 0)) add_rest<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16, t_first, t_first + tokens);
     }
     store_dw<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16);
 }
