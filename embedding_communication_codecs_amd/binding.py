@@ -489,11 +489,14 @@ def _mat(t, rows, cols, ld, kind, name, padding=0):
     return t.data_ptr()
 
 
-def _vec(t, count, kind, name):
-    """Device address of `count` contiguous elements of that kind."""
-    if t is not None and not isinstance(t, int):
-        _typed(t, kind, name)
-    return _ptr(t, count * (1 if kind == "codes" else 4), name)
+def _vec(t, nbytes, kind, name):
+    """Device address of nbytes contiguous bytes of elements of that kind."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.is_cuda and t.dtype in _dtypes[kind] and t.is_contiguous() and t.nbytes >= nbytes:
+        return t.data_ptr()
+    _typed(t, kind, name)
+    return _ptr(t, nbytes, name)
 
 
 def _ckpt(codes, exps, rows, dim, name):
@@ -515,14 +518,14 @@ qc_ckpt8_bytes = ckpt8_bytes
 def qc_encode_int8_rowwise(x, xtype, rows, dim, ldx, codes, ldq, scale, stream=None):
     _check(lib().qc_encode_int8_rowwise(
         _mat(x, rows, dim, ldx, xtype, "x"), xtype, rows, dim, ldx,
-        _mat(codes, rows, dim, ldq, "codes", "codes", -dim % 16), ldq, _vec(scale, max(rows, 0), QC_F32, "scale"),
+        _mat(codes, rows, dim, ldq, "codes", "codes", -dim % 16), ldq, _vec(scale, 4 * rows, QC_F32, "scale"),
         _stream(stream)))
 
 
 def qc_matmul_int8(a, a_scale, lda, b, b_scale, ldb, m, n, k, c, ctype, ldc, stream=None):
     _check(lib().qc_matmul_int8(
-        _mat(a, m, k, lda, "codes", "a", -k % 16), _vec(a_scale, max(m, 0), QC_F32, "a_scale"), lda,
-        _mat(b, n, k, ldb, "codes", "b", -k % 16), _vec(b_scale, max(n, 0), QC_F32, "b_scale"), ldb, m, n, k,
+        _mat(a, m, k, lda, "codes", "a", -k % 16), _vec(a_scale, 4 * m, QC_F32, "a_scale"), lda,
+        _mat(b, n, k, ldb, "codes", "b", -k % 16), _vec(b_scale, 4 * n, QC_F32, "b_scale"), ldb, m, n, k,
         _mat(c, m, n, ldc, ctype, "c"), ctype, ldc, _stream(stream)))
 
 
