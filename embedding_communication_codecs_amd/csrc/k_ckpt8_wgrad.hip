@@ -12,13 +12,18 @@
 // the simple kernel) lie in LDS as [token][channel] and are read with
 // ds_read_b64_tr_b16, which hands each lane four tokens of one channel.
 //
-// Large products are bound by what the power budget allows: the matrix cores
-// alone run at 1.85-1.97 PFLOP/s on random bf16 values, and LDS traffic and
-// conversion take their share of it.  16384 x 4096 x 8192 (tokens, n, dim) 880
-// us, 1.25 PFLOP/s; 4096 x 4096 x 4096 120 us, 1.15.  Where the conversion and
-// the reads stand among the products, and the waves' priorities, do not change
-// these by more than 2%.  Small ones are bound by the latency of their few
-// stages and of a second launch that joins the splits.
+// 16384 x 4096 x 8192 (tokens, n, dim) takes 830-890 us, 1.24-1.33 PFLOP/s,
+// and 4096 x 4096 x 4096 116-122 us, 1.15, where the matrix cores alone run at
+// 1.85-1.97 PFLOP/s on random bf16 values.  They are busy 0.60 of the cycles:
+// a stage's barrier, fragment reads and conversion leave them waiting for the
+// rest.  Power takes the smaller part of the difference (all zeros take 747
+// and 105 us).  Where the conversion and the reads stand among the products,
+// and the waves' priorities, do not change these by more than 2%.
+//
+// Tiles of 128 x 128 are bound by their stages' latency: 0.45-0.55 us for 0.11 us
+// of products, with one wave a SIMD and loads that run three stages ahead
+// (2048 x 2048 x 2048: 64 stages, 34 us, matrix cores busy 0.22).  Splits that
+// are joined take a second launch of 4 to 5 us.
 #include "qc_lds.hpp"
 #include "qc_launch.hpp"
 
@@ -207,10 +212,12 @@ __device__ __forceinline__ void store_dw(const Args& g, f32x4 (&acc)[FD][FN], in
 }
 
 // ------------------------------------------------------------------- simple
-// Gradients of very few channels (n below 8 in bf16, below 4 in fp32).  One
-// block: BN output channels (columns of dY) x BD input channels (columns of
-// X), WN x WD waves, TK tokens a step, two steps in LDS; both operands pass
-// through registers.  P: pieces of dY (1: bf16, 3: fp32).
+// Gradients of very few channels (n below 8 in bf16, below 4 in fp32), as the
+// output layer of a regression, a reward or a few classes has them, whose rows
+// may be shorter than one load of the kernels below.  One block: BN output
+// channels (columns of dY) x BD input channels (columns of X), WN x WD waves,
+// TK tokens a step, two steps in LDS; both operands pass through registers.
+// P: pieces of dY (1: bf16, 3: fp32).
 template <int P, int BN, int BD, int WN, int WD, int TK>
 __global__ void __launch_bounds__(WN * WD * WAVE)
 k_ckpt8_wgrad(Args g) {
@@ -635,7 +642,7 @@ k_ckpt8_wgrad_pipe(Args g) {
 // by then: every wave has read the stage's tiles, so the stage after next may
 // be converted over them, and the next one is whole.  With the barrier and the
 // first fragments at a stage's start, 4096 x 4096 x 4096 of normal values took
-// 575 us; so it takes 380 with tiles of 128 x 256, three products at 1.08
+// 575 us; so it takes 340-380 with tiles of 128 x 256, three products at 1.08-1.2
 // PFLOP/s.  128 x 128 reads and converts dY, the wider operand, twice as often
 // for a product (494 us where 128 x 256 takes 347, values of few bits).
 template <int BD>
@@ -857,7 +864,8 @@ k_ckpt8_wgrad_pipe_f32(Args g) {
             if (s + 1 < stages) stage(integral_constant<int, 1>{}, std::false_type{}, s + 1, rot);
             turn();
         }
-        if (__builtin_expect(rest, 0)) add_rest<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16, t_first, t_first + tokens);
+        if (__builtin_expect(rest, 0))
+            add_rest<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16, t_first, t_first + tokens);
     }
     store_dw<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16);
 }

@@ -6,12 +6,13 @@
 // quotient x / scale, ties to even.  A row with an infinity or a NaN gets
 // scale NaN and codes 0; a zero scale gives codes 0.
 //
-// Bound by HBM (1.5 bytes read per byte written for bf16).  A row is held
-// in registers between the two uses of its values, by one wave where it is
-// short and by a block of 4 waves otherwise, so x is read once; rows longer
-// than 16,384 are read twice (the second read hits L2).  16384 x 8192 bf16: 67
-// us, 6.0 TB/s; 4096 x 4096 11.5 us; one row of 4096 2.3 us, the latency of
-// one load, one reduction over the block and one store.
+// Bound by HBM (2 bytes read per byte written for bf16, 4 for fp32).  A row is
+// held in registers between the two uses of its values, by one wave where it
+// is short and by a block of 4 waves otherwise, so x is read once.  16384 x
+// 8192 bf16: 67 us, 6.0 TB/s, fp32 115 us, 5.8; 4096 x 4096 bf16 11.5 us; one row of
+// 4096 2.3 us, the latency of one load, one reduction over the block and one
+// store.  Rows longer than 16,384 are read twice, from HBM both times: 4096 x
+// 28672 bf16 97 us, fp32 196, which is 6.1 and 5.4 TB/s with both reads counted.
 #include "qc_matrix.hpp"
 #include "qc_launch.hpp"
 
@@ -162,8 +163,8 @@ hipError_t launch_row(const T* x, int64_t rows, int64_t dim, int64_t ldx, uint8_
 template <class T>
 hipError_t launch(const T* x, int64_t rows, int64_t dim, int64_t ldx, uint8_t* codes, int64_t ldq, float* scale,
                   hipStream_t stream) {
-    // Few rows: a block a row even where a wave could hold it, so that the
-    // loads of a row are spread over four waves.
+    // By a row's length alone: a wave holds up to 1,024 values, 16 a lane; a
+    // block's four waves up to 16,384, 64 a lane.
     if (dim <= 512) return launch_row<T, 1, 1>(x, rows, dim, ldx, codes, ldq, scale, stream);
     if (dim <= 1024) return launch_row<T, 1, 2>(x, rows, dim, ldx, codes, ldq, scale, stream);
     if (dim <= 2048) return launch_row<T, 4, 1>(x, rows, dim, ldx, codes, ldq, scale, stream);

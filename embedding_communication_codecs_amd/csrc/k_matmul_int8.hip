@@ -401,9 +401,14 @@ hipError_t launch_few(const Args& g, T* c, hipStream_t stream) {
 
 // Which tile: the one whose rounds of blocks over the 256 compute units take
 // the least time.  `round_us` is the measured time of one full round at k =
-// 4096 without the launch itself (2 us); all grow with k alike.  Against the
-// next best shape, whole calls, weights from HBM, at n = k = 4096 (16384
-// where it says so):
+// 4096 without the launch itself (2 us).  A round has a part that does not
+// depend on k, and the few-token shapes share k among their waves in slabs of
+// 256 bytes, but the shapes keep their order: of all nine at k = 32, 64, 128, 256,
+// 512, 1024 and 4096, for 1 to 16384 tokens and n of 4096 and 8192, the one taken
+// was within 5% of the best, but at 61 x 8192 x 128 (4.2 us, 64 x 64 3.8).  16384
+// x 4096 x 128, for one: 256 x 256 34.4 us, 128 x 256 41.8, 128 x 128 56.4.
+// Against the next best shape, whole calls, weights from HBM, at n = k = 4096
+// (16384 where it says so):
 //   m    1: 16 x 16 5.6 us (32 x 16 6.2)     m  16 (16384): 32 x 16 13.5 (32 x 32 15.5)
 //   m   32: 32 x 16 6.7 (32 x 32 8.4)        m  32 (16384): 32 x 32 16.4 (32 x 64 17.1)
 //   m   61: 32 x 32 8.4 (32 x 64 9.7)        m 128: 32 x 64 9.6 (64 x 64 12.4)

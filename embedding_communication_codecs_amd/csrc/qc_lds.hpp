@@ -12,8 +12,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, in
 // 16 i.  Written as asm because the compiler takes every LDS access after
 // the builtin as dependent on it and waits for the load before the next
 // fragment read; it returns nothing in registers, and lds_landed() is the
-// wait that its readers need.  (m0 is a reserved register: the compiler sets it
-// right before each use of its own.)
+// wait that its readers need.  (m0, which holds the address in LDS, is a
+// reserved register: clang warns against naming it as clobbered, sets it right
+// before each use of its own, and has none in the kernels that include this.)
 __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds, int voff, int soff) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
@@ -40,7 +41,6 @@ __device__ __forceinline__ void lds_landed_but() {
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
-
 
 // Block b of `blocks` to tile (x, y) of a tx x ty grid.  Consecutive blocks go
 // to the eight XCDs in turn; each XCD gets a contiguous run of tiles, walked in

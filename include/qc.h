@@ -515,9 +515,10 @@ const char* qc_status_str(int32_t status);
 
 /*
  * ---------------------------------------------------------------------
- * Computing with 8-bit payloads: INT8 rows and their matrix product, and
+ * 8-bit matrix operators: INT8 rows and their matrix product, and
  * activations held in 8 bits ("checkpoints") between the forward and the
- * backward pass.
+ * backward pass.  Their formats are their own: the payloads of the encoders
+ * above do not enter them.
  *
  * Matrices are row-major with a row stride ("ld") in elements, at least the
  * number of columns; x, h, out, c, dy, dw and their gradients may start at
