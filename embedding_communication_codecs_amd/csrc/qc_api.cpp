@@ -606,6 +606,7 @@ int qc_ckpt8_wgrad(const void* dy, int32_t dytype, int64_t ldy, const int8_t* co
     if (misaligned_for(dy, dytype) || misaligned(codes) || misaligned(exps) || misaligned_for(dw, wtype) ||
         misaligned(workspace))
         return QC_ERR_ALIGN;
+    if (rows == 0 && accumulate) return QC_OK;  // adding +0 would change a -0
     return launched(qc::launch_ckpt8_wgrad(dy, dytype == QC_BF16, ldy, codes, exps, rows, n, dim, dw,
                                            wtype == QC_BF16, ldw, accumulate != 0, workspace, hs(stream)));
 }
