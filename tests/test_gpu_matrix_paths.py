@@ -112,7 +112,8 @@ def test_fp32_gradients_whole_when_small(qc, rows, n, dim):
 def test_no_tokens_added(qc, dtype):
     """Nothing is added: dW keeps its bits, zeros their signs and NaNs theirs."""
     n, dim = 9, 40
-    dw = torch.tensor([-0.0, 0.0, float("nan"), -float("inf"), 2.0 ** -149, 1.0]).repeat(n * dim // 6).view(n, dim).cuda()
+    values = torch.tensor([-0.0, 0.0, float("nan"), -float("inf"), 2.0 ** -149, 1.0])
+    dw = values.repeat(n * dim // 6).view(n, dim).cuda()
     before = dw.clone()
     none = lambda *shape, t: torch.empty(shape, dtype=t, device="cuda")  # noqa: E731
     qc.qc_ckpt8_wgrad(none(0, n, t=dtype), qc.QC_BF16 if dtype is BF16 else qc.QC_F32, n, none(0, 64, t=torch.int8),

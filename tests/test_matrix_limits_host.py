@@ -15,9 +15,9 @@ def test_product_of_too_many_tiles(qc, kw):  # noqa: F811
     assert status(qc, "qc_matmul_int8", *matmul(**kw)) == ARG
 
 
-@pytest.mark.parametrize("fn,args,ld", [("qc_encode_ckpt8", enc_ckpt, ("ldx",)), ("qc_decode_ckpt8", dec_ckpt, ("ldo",)),
-                                        ("qc_swiglu_ckpt8", swiglu, ("ldx", "ldh")),
-                                        ("qc_swiglu_ckpt8_backward", swiglu_bwd, ("lddh", "ldg"))])
+@pytest.mark.parametrize("fn,args,ld", [
+    ("qc_encode_ckpt8", enc_ckpt, ("ldx",)), ("qc_decode_ckpt8", dec_ckpt, ("ldo",)),
+    ("qc_swiglu_ckpt8", swiglu, ("ldx", "ldh")), ("qc_swiglu_ckpt8_backward", swiglu_bwd, ("lddh", "ldg"))])
 def test_checkpoint_of_too_long_rows(qc, fn, args, ld):  # noqa: F811
     dim = (1 << 34) + 1
     assert status(qc, fn, *args(rows=1, dim=dim, **{n: dim for n in ld})) == UNSUP

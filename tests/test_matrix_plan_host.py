@@ -66,7 +66,8 @@ def test_pieces_are_tested_on_every_fp32_kernel():
 
 def sizes_of(test):
     """The (m, n, k) that a test is parametrised with."""
-    return [s for mark in test.pytestmark if mark.name == "parametrize" and mark.args[0] == "m,n,k" for s in mark.args[1]]
+    marks = [m for m in test.pytestmark if m.name == "parametrize" and m.args[0] == "m,n,k"]
+    return [size for mark in marks for size in mark.args[1]]
 
 
 def test_every_product_tile_is_reached():
