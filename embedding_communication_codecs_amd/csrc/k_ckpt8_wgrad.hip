@@ -91,13 +91,50 @@ __device__ __forceinline__ float rest_of(float x) {
     return x;
 }
 
-// Adds those remainders' products to a wave's sums (their layout: store_dw)
-// in fp32 multiply-adds; a remainder has 16 bits and X 8, so the products
-// are exact.  Only blocks that met a remainder call this: the wave looks for
-// its tokens that have one among its channels, a token for 16 lanes, and
-// multiplies for those, four at a time.  4096 x 4096 x 4096 of normal gradients
-// 347 us (344 without the look at their bits); one in a million of them at
-// 1e-36, in every block then, 655; one in a thousand 1,230.
+// Whether such remainders can change a wave's sums (their layout: store_dw):
+// a product of one is below 2^-133 * 127 steps, and leaves a sum of 2^26 times
+// that and more as it is, being less than a quarter of its step.  The steps
+// are those of the wave's channels; a NaN group's sums are NaN whatever is
+// added.
+template <int FN, int FD>
+__device__ __forceinline__ bool rest_matters(const Args& g, const f32x4 (&acc)[FD][FN], int64_t n0, int64_t d0,
+                                             int64_t t_first, int64_t t_end) {
+    constexpr int U = 8, GROUPS = FD / 2;
+    const int l = lane_id();
+    uint32_t most = 0;
+    for (int64_t t0 = t_first + l; t0 - l < t_end; t0 += U * WAVE) {
+        uint32_t byte[U][GROUPS];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < GROUPS; ++k)
+                byte[u][k] = g.exps[min(t0 + u * WAVE, t_end - 1) * g.epitch + min(d0 / 32 + k, g.epitch - 1)];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < GROUPS; ++k) most = umax(most, byte[u][k] == kCkptNaN ? 0u : byte[u][k]);
+    }
+    const float large = ckpt_step(group_max_u32<WAVE>(most)) * (127.0f * 0x1p-107f);
+    bool small = false;
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int i = 0; i < FD; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                small |= fabsf(acc[i][j][e]) < large && n0 + j * 16 + (l & 15) < g.n &&
+                         d0 + 16 * i + 4 * (l >> 4) + e < g.dim;
+    return __any(small);
+}
+
+// Adds those remainders' products to a wave's sums in fp32 multiply-adds; a
+// remainder has 16 bits and X 8, so the products are exact.  Only where they
+// matter: the wave looks for its tokens that have a remainder among its
+// channels, a token for 16 lanes, and multiplies for those, four at a time.
+// 4096 x 4096 x 4096 of normal gradients 347 us (344 without the look at their
+// bits); some of them, few or many, at 1e-36 400, for finding that they do not
+// matter; with sums as small as they are, 650 for one in a million, 1,230 for
+// one in a thousand and 5,600 for every other.
 template <int FN, int FD>
 __device__ __forceinline__ void add_rest(const Args& g, f32x4 (&acc)[FD][FN], int64_t n0, int64_t d0, int64_t t_first,
                                          int64_t t_end) {
@@ -368,7 +405,10 @@ k_ckpt8_wgrad(Args g) {
             }
         }
         // set before the last barrier, if at all
-        if (P == 3 && rest) add_rest<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16, t_first, t_end);
+        if (P == 3 && rest) {
+            const int64_t nw = n0 + wn * FN * 16, dw = d0 + wd * FD * 16;
+            if (rest_matters<FN, FD>(g, acc, nw, dw, t_first, t_end)) add_rest<FN, FD>(g, acc, nw, dw, t_first, t_end);
+        }
     }
 
     store_dw<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16);
@@ -864,8 +904,11 @@ k_ckpt8_wgrad_pipe_f32(Args g) {
             if (s + 1 < stages) stage(integral_constant<int, 1>{}, std::false_type{}, s + 1, rot);
             turn();
         }
-        if (__builtin_expect(rest, 0))
-            add_rest<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16, t_first, t_first + tokens);
+        if (__builtin_expect(rest, 0)) {
+            const int64_t nw = n0 + wn * FN * 16, dw = d0 + wd * FD * 16;
+            const int64_t t_end = t_first + tokens;
+            if (rest_matters<FN, FD>(g, acc, nw, dw, t_first, t_end)) add_rest<FN, FD>(g, acc, nw, dw, t_first, t_end);
+        }
     }
     store_dw<FN, FD>(g, acc, n0 + wn * FN * 16, d0 + wd * FD * 16);
 }

@@ -608,7 +608,8 @@ int qc_decode_ckpt8(const int8_t* codes, const uint8_t* exps, int64_t rows, int6
  * sum is taken in fp32, in an order that depends on the sizes alone (the
  * same call gives the same bits).  Gradients, products and sums below the
  * smallest normal number (2^-126) may count as zero.  fp32 gradients below
- * 2^-110 (7.7e-34), other than zeros, take several times as long.
+ * 2^-110 (7.7e-34), other than zeros, take up to a sixth longer, and several
+ * times as long where sums are so small that their last bits matter.
  *
  *   dy          [rows][n] of type dytype, row stride ldy.
  *   codes, exps a checkpoint of [rows][dim].

@@ -108,6 +108,33 @@ def test_fp32_gradients_whole_when_small(qc, rows, n, dim):
     assert np.all(off <= 4 * U32 * np.abs(want)), (off / np.maximum(np.abs(want), 2.0 ** -126)).max()
 
 
+@pytest.mark.parametrize("rows,n,dim", PIECES)
+def test_fp32_gradients_whole_beside_large_ones(qc, rows, n, dim):
+    """Both kinds in a wave: sums that the bits below 2^-133 change and sums
+    that they do not reach."""
+    dy, at, value = one_token_a_channel(rows, n, -126, 8, 7)
+    got, v = run_wgrad(qc, dy, ref.matrix(rows, dim, 2, F32) * 2.0 ** 60)
+    want = value[:, None] * v[at]
+    assert np.all(np.abs(got.double().numpy() - want) <= 4 * U32 * np.abs(want))
+
+
+@pytest.mark.parametrize("rows,n,dim", PIECES)
+def test_small_gradients_among_large_ones(qc, rows, n, dim):
+    """Gradients whose last bits no sum shows; channel 1 has no others, and the
+    inputs' channel 2 is zero."""
+    dy, x = gradients(rows, n, F32), ref.matrix(rows, dim, 2, F32)
+    dy[torch.rand((rows, n), generator=torch.Generator().manual_seed(3)) < 0.01] = 1.2345e-37
+    dy[:, 1] = 1.2345e-37
+    x[:, 2] = 0
+    got, v = run_wgrad(qc, dy, x)
+    d = dy.double().numpy()
+    want, mag = d.T @ v, np.abs(d).T @ np.abs(v)
+    off = np.abs(got.double().numpy() - want)
+    assert np.all(off <= 2 * U32 * (3 * rows + 64) * mag), off.max()
+    for rows_ in (np.arange(n) != 1, np.arange(n) == 1):
+        assert np.linalg.norm(off[rows_]) <= norm_bound(rows, F32) * np.linalg.norm(want[rows_])
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=str)
 def test_no_tokens_added(qc, dtype):
     """Nothing is added: dW keeps its bits, zeros their signs and NaNs theirs."""
