@@ -12,7 +12,7 @@
 // the simple kernel) lie in LDS as [token][channel] and are read with
 // ds_read_b64_tr_b16, which hands each lane four tokens of one channel.
 //
-// 16384 x 4096 x 8192 (tokens, n, dim) takes 830-890 us, 1.24-1.33 PFLOP/s,
+// 16384 x 4096 x 8192 (tokens, n, dim) takes 830-900 us, 1.22-1.33 PFLOP/s,
 // and 4096 x 4096 x 4096 116-122 us, 1.15, where the matrix cores alone run at
 // 1.85-1.97 PFLOP/s on random bf16 values.  They are busy 0.60 of the cycles:
 // a stage's barrier, fragment reads and conversion leave them waiting for the
