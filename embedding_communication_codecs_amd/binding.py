@@ -25,6 +25,9 @@ QC_INDEX_SHIFT = 12
 QC_MAX_LIST_BUCKET = 32768
 QC_MAX_TOPK_BUCKET = 65536
 QC_CKPT_GROUP = 32
+QC_MX_GROUP = 32
+QC_STATE_BLOCK = 256
+QC_STATE_M, QC_STATE_R = 0, 1
 
 EXPORTS = (
     "qc_encode_uniform", "qc_encode_uniform_stochastic", "qc_encode_uniform_multi", "qc_encode_fp8_rowwise",
@@ -35,6 +38,9 @@ EXPORTS = (
     "qc_bucket_absmax_multi", "qc_encode_int8_shared_multi", "qc_encode_topk_multi",
     "qc_encode_int8_rowwise", "qc_matmul_int8", "qc_ckpt8_bytes", "qc_encode_ckpt8", "qc_decode_ckpt8",
     "qc_ckpt8_wgrad_workspace", "qc_ckpt8_wgrad", "qc_swiglu_ckpt8", "qc_swiglu_ckpt8_backward",
+    "qc_mxfp4_bytes", "qc_encode_mxfp4", "qc_decode_mxfp4", "qc_matmul_mxfp4_workspace", "qc_matmul_mxfp4",
+    "qc_linear_mxfp4_workspace", "qc_linear_mxfp4", "qc_grad_norm_workspace", "qc_grad_norm_multi", "qc_adamw_multi",
+    "qc_adamw8_multi", "qc_encode_state8", "qc_decode_state8",
     "qc_decode", "qc_decode_multi", "qc_dequant_accumulate", "qc_majority_vote", "qc_payload_bytes", "qc_status_str",
 )
 
@@ -57,6 +63,7 @@ def lib() -> ctypes.CDLL:
                 f"{LIB_PATH} is missing: build it with `python -m embedding_communication_codecs_amd.build`")
         L = ctypes.CDLL(LIB_PATH)
         P, I32, I64, U64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
+        F64 = ctypes.c_double
         sig = {
             "qc_encode_uniform": [P, P, I64, I32, I32, P, P, P, P],
             "qc_encode_uniform_stochastic": [P, P, I64, I32, I32, U64, U64, P, P, P, P],
@@ -93,6 +100,19 @@ def lib() -> ctypes.CDLL:
             "qc_ckpt8_wgrad": [P, I32, I64, P, P, I64, I64, I64, P, I32, I64, I32, P, I64, P],
             "qc_swiglu_ckpt8": [P, P, I32, I64, I64, I64, P, I64, P, P, P, P, P],
             "qc_swiglu_ckpt8_backward": [P, I32, I64, P, P, P, P, I64, I64, P, P, I64, P],
+            "qc_mxfp4_bytes": [I64, I64, P, P],
+            "qc_encode_mxfp4": [P, I32, I64, I64, I64, P, P, P, P, P],
+            "qc_decode_mxfp4": [P, P, I64, I64, P, I32, I64, P],
+            "qc_matmul_mxfp4_workspace": [I64, I64, I64],
+            "qc_matmul_mxfp4": [P, P, P, P, I64, I64, I64, P, I32, I64, I32, P, I64, P],
+            "qc_linear_mxfp4_workspace": [I64, I64, I64, I32],
+            "qc_linear_mxfp4": [P, I32, I64, P, P, I64, I64, I64, P, I32, I64, P, I64, P],
+            "qc_grad_norm_workspace": [I64],
+            "qc_grad_norm_multi": [P, I32, P, P, I32, I64, F64, P, I64, P, P],
+            "qc_adamw_multi": [P, I32, P, I32, P, P, I32, I64, P, P, P, F64, F64, F64, F64, F64, I64, P, P, P],
+            "qc_adamw8_multi": [P, I32, P, I32, P, P, I32, I64, P, P, P, P, P, F64, F64, F64, F64, F64, I64, P, P, P],
+            "qc_encode_state8": [I32, P, I64, P, P, P],
+            "qc_decode_state8": [I32, P, P, I64, P, I32, P],
             "qc_payload_bytes": [I32, I64, I32, I32],
             "qc_status_str": [I32],
         }
@@ -101,7 +121,9 @@ def lib() -> ctypes.CDLL:
             fn.argtypes = args
             fn.restype = ctypes.c_int
         L.qc_payload_bytes.restype = I64
-        L.qc_ckpt8_wgrad_workspace.restype = I64
+        for name in ("qc_ckpt8_wgrad_workspace", "qc_matmul_mxfp4_workspace", "qc_linear_mxfp4_workspace",
+                     "qc_grad_norm_workspace"):
+            getattr(L, name).restype = I64
         L.qc_status_str.restype = ctypes.c_char_p
         _lib = L
     return _lib
@@ -572,6 +594,167 @@ def qc_swiglu_ckpt8_backward(dh, dhtype, lddh, gate_codes, gate_exps, up_codes, 
         _mat(dh, rows, dim, lddh, dhtype, "dh"), dhtype, lddh, *_ckpt(gate_codes, gate_exps, rows, dim, "gate_"),
         *_ckpt(up_codes, up_exps, rows, dim, "up_"), rows, dim, _mat(dgate, rows, dim, ldg, dhtype, "dgate"),
         _mat(dup, rows, dim, ldg, dhtype, "dup"), ldg, _stream(stream)))
+
+
+# ------------------------------------------------- 4-bit matrix operators
+
+
+def _now():
+    import torch
+
+    return torch.cuda.current_device()
+
+
+def _here(*tensors):
+    """Refuses tensors of another device than the current one, whose stream and
+    kernels the call would use."""
+    now = None
+    for t in tensors:
+        if t is None or isinstance(t, int) or not t.is_cuda:
+            continue
+        now = _now() if now is None else now
+        if t.get_device() != now:
+            raise ValueError(f"a tensor is on GPU {t.get_device()}, the current one is {now}")
+
+
+def _space(workspace):
+    """Address and bytes of a workspace (a GPU tensor or None)."""
+    if workspace is None:
+        return None, 0
+    if isinstance(workspace, int):
+        raise ValueError("workspace must be a GPU tensor")
+    return _ptr(workspace, None, "workspace"), _bytes(workspace)
+
+
+def _mx(codes, scales, rows, dim, name):
+    cb = rows * (-(-dim // QC_MX_GROUP) * (QC_MX_GROUP // 2))
+    sb = rows * (-(-dim // (4 * QC_MX_GROUP)) * 4)
+    return _vec(codes, cb, "codes", name + "codes"), _vec(scales, sb, "codes", name + "scales")
+
+
+def mxfp4_bytes(rows: int, dim: int) -> tuple[int, int]:
+    """(code bytes, scale bytes) of a matrix of [rows][dim] in MXFP4."""
+    cb, sb = ctypes.c_int64(), ctypes.c_int64()
+    _check(lib().qc_mxfp4_bytes(rows, dim, ctypes.byref(cb), ctypes.byref(sb)))
+    return cb.value, sb.value
+
+
+qc_mxfp4_bytes = mxfp4_bytes
+
+
+def qc_encode_mxfp4(x, xtype, rows, dim, ldx, codes, scales, codes_t=None, scales_t=None, stream=None):
+    _here(x, codes, scales, codes_t, scales_t)
+    _check(lib().qc_encode_mxfp4(
+        _mat(x, rows, dim, ldx, xtype, "x"), xtype, rows, dim, ldx, *_mx(codes, scales, rows, dim, ""),
+        *_mx(codes_t, scales_t, dim, rows, "transposed "), _stream(stream)))
+
+
+def qc_decode_mxfp4(codes, scales, rows, dim, out, otype, ldo, stream=None):
+    _here(codes, scales, out)
+    _check(lib().qc_decode_mxfp4(*_mx(codes, scales, rows, dim, ""), rows, dim,
+                                 _mat(out, rows, dim, ldo, otype, "out"), otype, ldo, _stream(stream)))
+
+
+def qc_matmul_mxfp4_workspace(m, n, k) -> int:
+    """Bytes of workspace qc_matmul_mxfp4 needs for these sizes."""
+    need = int(lib().qc_matmul_mxfp4_workspace(m, n, k))
+    if need < 0:
+        _check(QC_ERR_ARG)
+    return need
+
+
+def qc_matmul_mxfp4(a, a_scales, b, b_scales, m, n, k, c, ctype, ldc, accumulate=False, workspace=None, stream=None):
+    """workspace: a GPU tensor of at least qc_matmul_mxfp4_workspace() bytes, or
+    None where that is 0."""
+    _here(a, a_scales, b, b_scales, c, workspace)
+    _check(lib().qc_matmul_mxfp4(
+        *_mx(a, a_scales, m, k, "a "), *_mx(b, b_scales, n, k, "b "), m, n, k, _mat(c, m, n, ldc, ctype, "c"), ctype,
+        ldc, 1 if accumulate else 0, *_space(workspace), _stream(stream)))
+
+
+def qc_linear_mxfp4_workspace(m, n, k, xtype) -> int:
+    """Bytes of workspace qc_linear_mxfp4 needs for these sizes."""
+    need = int(lib().qc_linear_mxfp4_workspace(m, n, k, xtype))
+    if need < 0:
+        _check(QC_ERR_ARG)
+    return need
+
+
+def qc_linear_mxfp4(x, xtype, ldx, b, b_scales, m, n, k, c, ctype, ldc, workspace=None, stream=None):
+    """workspace: a GPU tensor of at least qc_linear_mxfp4_workspace() bytes, or
+    None where that is 0."""
+    _here(x, b, b_scales, c, workspace)
+    _check(lib().qc_linear_mxfp4(
+        _mat(x, m, k, ldx, xtype, "x"), xtype, ldx, *_mx(b, b_scales, n, k, "b "), m, n, k,
+        _mat(c, m, n, ldc, ctype, "c"), ctype, ldc, *_space(workspace), _stream(stream)))
+
+
+# --------------------------------------------------------------- optimizer
+
+
+def qc_grad_norm_workspace(n) -> int:
+    """Bytes of workspace qc_grad_norm_multi needs for n elements."""
+    need = int(lib().qc_grad_norm_workspace(n))
+    if need < 0:
+        _check(QC_ERR_ARG)
+    return need
+
+
+def qc_grad_norm_multi(grads, gtype, offsets, seg_first, ntensors, n, max_norm, workspace, out, stream=None):
+    """grads/offsets/seg_first: device tables (see TensorTable) or raw
+    addresses; workspace: a GPU tensor of at least qc_grad_norm_workspace()
+    bytes."""
+    _here(grads, offsets, seg_first, workspace, out)
+    g = _list_args(grads, offsets, seg_first, ntensors, n)
+    _check(lib().qc_grad_norm_multi(g[0], gtype, *g[1:], max_norm, *_space(workspace), _vec(out, 8, QC_F32, "out"),
+                                    _stream(stream)))
+
+
+def _adamw(fn, params, ptype, grads, gtype, offsets, seg_first, ntensors, n, master, states, hyper, grad_scale,
+           schedule, stream):
+    _here(params, grads, offsets, seg_first, master, grad_scale, schedule, *(t for t, _, _, _ in states))
+    g = _list_args(grads, offsets, seg_first, ntensors, n)
+    _check(fn(
+        _ptr(params, 8 * max(ntensors, 0), "params"), ptype, g[0], gtype, *g[1:],
+        _vec(master, 4 * n, QC_F32, "master"), *(_vec(*s) for s in states), *hyper,
+        _vec(grad_scale, 4, QC_F32, "grad_scale"), _vec(schedule, 8, QC_F32, "schedule"), _stream(stream)))
+
+
+def qc_adamw_multi(params, ptype, grads, gtype, offsets, seg_first, ntensors, n, master, m, v, lr, beta1, beta2, eps,
+                   weight_decay, step, grad_scale=None, schedule=None, stream=None):
+    """params/grads/offsets/seg_first: device tables of two lists of the same
+    sizes (see TensorTable) or raw addresses."""
+    _adamw(lib().qc_adamw_multi, params, ptype, grads, gtype, offsets, seg_first, ntensors, n, master,
+           ((m, 4 * n, QC_F32, "m"), (v, 4 * n, QC_F32, "v")), (lr, beta1, beta2, eps, weight_decay, step), grad_scale,
+           schedule, stream)
+
+
+def qc_adamw8_multi(params, ptype, grads, gtype, offsets, seg_first, ntensors, n, master, m_codes, m_scale, r_codes,
+                    r_scale, lr, beta1, beta2, eps, weight_decay, step, grad_scale=None, schedule=None, stream=None):
+    """As qc_adamw_multi, with states of n codes and ceil(n / 256) scales each."""
+    sb = 4 * nbuckets(n, QC_STATE_BLOCK)
+    _adamw(lib().qc_adamw8_multi, params, ptype, grads, gtype, offsets, seg_first, ntensors, n, master,
+           ((m_codes, n, "codes", "m_codes"), (m_scale, sb, QC_F32, "m_scale"),
+            (r_codes, n, "codes", "r_codes"), (r_scale, sb, QC_F32, "r_scale")),
+           (lr, beta1, beta2, eps, weight_decay, step), grad_scale, schedule, stream)
+
+
+def _typed_flat(t, kind, n, name):
+    return _vec(t, n * (2 if kind == QC_BF16 else 4), kind, name)
+
+
+def qc_encode_state8(kind, x, n, codes, scale, stream=None):
+    _here(x, codes, scale)
+    _check(lib().qc_encode_state8(
+        kind, _vec(x, 4 * n, QC_F32, "x"), n, _vec(codes, n, "codes", "codes"),
+        _vec(scale, 4 * nbuckets(n, QC_STATE_BLOCK), QC_F32, "scale"), _stream(stream)))
+
+
+def qc_decode_state8(kind, codes, scale, n, out, otype, stream=None):
+    _here(codes, scale, out)
+    _check(lib().qc_decode_state8(
+        kind, _vec(codes, n, "codes", "codes"), _vec(scale, 4 * nbuckets(n, QC_STATE_BLOCK), QC_F32, "scale"), n,
+        _typed_flat(out, otype, n, "out"), otype, _stream(stream)))
 
 
 def qc_payload_bytes(fmt, n, group, bits) -> int:

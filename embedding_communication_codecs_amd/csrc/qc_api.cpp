@@ -8,6 +8,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cmath>
+
 #include "qc_launch.hpp"
 
 namespace {
@@ -637,6 +639,230 @@ int qc_swiglu_ckpt8_backward(const void* dh, int32_t dhtype, int64_t lddh, const
         return QC_ERR_ALIGN;
     return launched(qc::launch_swiglu_ckpt8_backward(dh, dhtype == QC_BF16, lddh, gate_codes, gate_exps, up_codes,
                                                      up_exps, rows, dim, dgate, dup, ldg, hs(stream)));
+}
+
+// ------------------------------------------------ 4-bit matrix operators
+
+namespace {
+
+// A launch has fewer than 2^32 threads: 256 for a tile of 128 x 128 values.
+constexpr int64_t kMaxMxTiles = (int64_t(1) << 24) - 1;
+
+bool bad_mx(int64_t rows, int64_t dim) {
+    return rows < 0 || dim < 1 || dim > kMaxMatrixElems / (rows > 0 ? rows : 1);
+}
+
+bool bad_mx_product(int64_t m, int64_t n, int64_t k) {
+    return bad_mx(m, k) || bad_mx(n, k) || (n > 0 && m > kMaxMatrixElems / n) ||
+           (m > 0 && n > 0 && ceil_div(m, 256) > kMaxProductTiles / ceil_div(n, 256));
+}
+
+}  // namespace
+
+int qc_mxfp4_bytes(int64_t rows, int64_t dim, int64_t* code_bytes, int64_t* scale_bytes) {
+    if (!code_bytes || !scale_bytes || bad_mx(rows, dim)) return QC_ERR_ARG;
+    *code_bytes = rows * (up_to(dim, QC_MX_GROUP) / 2);
+    *scale_bytes = rows * (up_to(dim, 4 * QC_MX_GROUP) / QC_MX_GROUP);
+    return QC_OK;
+}
+
+int qc_encode_mxfp4(const void* x, int32_t xtype, int64_t rows, int64_t dim, int64_t ldx, uint8_t* codes,
+                    uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t, qc_stream_t stream) {
+    if (bad_type(xtype) || bad_matrix(rows, dim, ldx)) return QC_ERR_ARG;
+    if (rows == 0) return QC_OK;
+    if (!x || !codes != !scales || !codes_t != !scales_t || (!codes && !codes_t)) return QC_ERR_ARG;
+    if (dim > kMaxCkptDim || (codes_t && rows > kMaxCkptDim)) return QC_ERR_UNSUPPORTED;
+    if (ceil_div(rows, 128) > kMaxMxTiles / ceil_div(dim, 128)) return QC_ERR_ARG;
+    if (misaligned_for(x, xtype) || misaligned(codes) || misaligned(scales) || misaligned(codes_t) ||
+        misaligned(scales_t))
+        return QC_ERR_ALIGN;
+    return launched(qc::launch_encode_mxfp4(x, xtype == QC_BF16, rows, dim, ldx, codes, scales, codes_t, scales_t,
+                                            hs(stream)));
+}
+
+int qc_decode_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t dim, void* out,
+                    int32_t otype, int64_t ldo, qc_stream_t stream) {
+    if (bad_type(otype) || bad_matrix(rows, dim, ldo)) return QC_ERR_ARG;
+    if (rows == 0) return QC_OK;
+    if (!codes || !scales || !out) return QC_ERR_ARG;
+    if (dim > kMaxCkptDim) return QC_ERR_UNSUPPORTED;
+    if (misaligned(codes) || misaligned(scales) || misaligned_for(out, otype)) return QC_ERR_ALIGN;
+    return launched(qc::launch_decode_mxfp4(codes, scales, rows, dim, out, otype == QC_BF16, ldo, hs(stream)));
+}
+
+int64_t qc_matmul_mxfp4_workspace(int64_t m, int64_t n, int64_t k) {
+    if (k < 1 || bad_mx_product(m, n, k)) return -1;
+    return m == 0 || n == 0 ? 0 : qc::matmul_mxfp4_workspace(m, n, k);
+}
+
+int qc_matmul_mxfp4(const uint8_t* a, const uint8_t* a_scales, const uint8_t* b, const uint8_t* b_scales, int64_t m,
+                    int64_t n, int64_t k, void* c, int32_t ctype, int64_t ldc, int32_t accumulate, void* workspace,
+                    int64_t workspace_bytes, qc_stream_t stream) {
+    if (bad_type(ctype) || k < 1 || bad_mx_product(m, n, k)) return QC_ERR_ARG;
+    if (accumulate && ctype != QC_F32) return QC_ERR_UNSUPPORTED;
+    if (m == 0 || n == 0) return QC_OK;
+    if (bad_matrix(m, n, ldc) || !a || !a_scales || !b || !b_scales || !c) return QC_ERR_ARG;
+    if (k > kMaxProductStride) return QC_ERR_UNSUPPORTED;
+    const int64_t need = qc::matmul_mxfp4_workspace(m, n, k);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return QC_ERR_ARG;
+    if (misaligned(a) || misaligned(a_scales) || misaligned(b) || misaligned(b_scales) || misaligned_for(c, ctype) ||
+        misaligned(workspace))
+        return QC_ERR_ALIGN;
+    return launched(qc::launch_matmul_mxfp4(a, a_scales, b, b_scales, m, n, k, c, ctype == QC_BF16, ldc,
+                                            accumulate != 0, workspace, hs(stream)));
+}
+
+int64_t qc_linear_mxfp4_workspace(int64_t m, int64_t n, int64_t k, int32_t xtype) {
+    if (bad_type(xtype) || k < 1 || bad_mx_product(m, n, k)) return -1;
+    return m == 0 || n == 0 ? 0 : qc::linear_mxfp4_workspace(m, n, k, xtype == QC_BF16);
+}
+
+int qc_linear_mxfp4(const void* x, int32_t xtype, int64_t ldx, const uint8_t* b, const uint8_t* b_scales, int64_t m,
+                    int64_t n, int64_t k, void* c, int32_t ctype, int64_t ldc, void* workspace,
+                    int64_t workspace_bytes, qc_stream_t stream) {
+    if (bad_type(xtype) || bad_type(ctype) || k < 1 || bad_mx_product(m, n, k)) return QC_ERR_ARG;
+    if (m == 0 || n == 0) return QC_OK;
+    if (bad_matrix(m, k, ldx) || bad_matrix(m, n, ldc) || !x || !b || !b_scales || !c) return QC_ERR_ARG;
+    if (k > kMaxProductStride) return QC_ERR_UNSUPPORTED;
+    if (ceil_div(m, 128) > kMaxMxTiles / ceil_div(k, 128)) return QC_ERR_ARG;
+    const int64_t need = qc::linear_mxfp4_workspace(m, n, k, xtype == QC_BF16);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return QC_ERR_ARG;
+    if (misaligned_for(x, xtype) || misaligned(b) || misaligned(b_scales) || misaligned_for(c, ctype) ||
+        misaligned(workspace))
+        return QC_ERR_ALIGN;
+    return launched(qc::launch_linear_mxfp4(x, xtype == QC_BF16, ldx, b, b_scales, m, n, k, c, ctype == QC_BF16, ldc,
+                                            workspace, hs(stream)));
+}
+
+// -------------------------------------------------------------- optimizer
+
+namespace {
+
+int check_optimizer_list(const void* const* grads, int32_t gtype, const int64_t* offsets, const int32_t* seg_first,
+                         int32_t ntensors, int64_t n, qc::ListSrc& l) {
+    if (bad_type(gtype) || n < 0 || n > kMaxListElems || ntensors < 1) return QC_ERR_ARG;
+    if (n == 0) return QC_OK;
+    if (!grads || !offsets || !seg_first) return QC_ERR_ARG;
+    if (misaligned8(grads) || misaligned8(offsets) || misaligned4(seg_first)) return QC_ERR_ALIGN;
+    l = qc::ListSrc{grads, offsets, seg_first, ntensors, n};
+    return QC_OK;
+}
+
+bool finite_from_0(double v) { return v >= 0.0 && std::isfinite(v); }
+
+struct AdamwArgs {
+    void* const* params;
+    int32_t ptype;
+    const void* const* grads;
+    int32_t gtype;
+    const int64_t* offsets;
+    const int32_t* seg_first;
+    int32_t ntensors;
+    int64_t n;
+    float* master;
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;
+    const float* grad_scale;
+    const float* schedule;
+};
+
+// Everything but the states.
+int check_adamw(const AdamwArgs& a, qc::AdamwList& l, qc::AdamwStep& s) {
+    if (bad_type(a.ptype) || (a.master && a.ptype != QC_BF16)) return QC_ERR_ARG;
+    if (!finite_from_0(a.lr) || !finite_from_0(a.eps) || !finite_from_0(a.weight_decay) || !(a.beta1 >= 0.0) ||
+        !(a.beta1 < 1.0) || !(a.beta2 >= 0.0) || !(a.beta2 < 1.0) || a.step < 1)
+        return QC_ERR_ARG;
+    const int st = check_optimizer_list(a.grads, a.gtype, a.offsets, a.seg_first, a.ntensors, a.n, l.grads);
+    if (st != QC_OK || a.n == 0) return st;
+    if (!a.params) return QC_ERR_ARG;
+    if (misaligned8(a.params) || misaligned(a.master) || misaligned4(a.grad_scale) || misaligned4(a.schedule))
+        return QC_ERR_ALIGN;
+    l.params = a.params;
+    l.p_bf16 = a.ptype == QC_BF16;
+    l.g_bf16 = a.gtype == QC_BF16;
+    l.master = a.master;
+    const double t = (double)a.step;
+    s.beta1 = (float)a.beta1;
+    s.beta2 = (float)a.beta2;
+    s.rest1 = (float)(1.0 - a.beta1);
+    s.rest2 = (float)(1.0 - a.beta2);
+    s.eps = (float)a.eps;
+    s.weight_decay = a.weight_decay;
+    s.log2_beta1 = std::log2(a.beta1);  // -inf for 0: 2^(t * -inf) = 0
+    s.log2_beta2 = std::log2(a.beta2);
+    s.decay = (float)(1.0 - a.lr * a.weight_decay);
+    s.rate = (float)(a.lr / (1.0 - std::pow(a.beta1, t)));
+    s.root = (float)(1.0 / std::sqrt(1.0 - std::pow(a.beta2, t)));
+    s.t = (uint32_t)a.step;
+    s.grad_scale = a.grad_scale;
+    s.schedule = a.schedule;
+    return QC_OK;
+}
+
+}  // namespace
+
+int64_t qc_grad_norm_workspace(int64_t n) { return n < 0 ? -1 : qc::grad_norm_workspace(n); }
+
+int qc_grad_norm_multi(const void* const* grads, int32_t gtype, const int64_t* offsets, const int32_t* seg_first,
+                       int32_t ntensors, int64_t n, double max_norm, void* workspace, int64_t workspace_bytes,
+                       float* out, qc_stream_t stream) {
+    qc::ListSrc l;
+    if (!(max_norm > 0.0)) return QC_ERR_ARG;
+    const int st = check_optimizer_list(grads, gtype, offsets, seg_first, ntensors, n, l);
+    if (st != QC_OK || n == 0) return st;
+    if (!out || !workspace || workspace_bytes < qc::grad_norm_workspace(n)) return QC_ERR_ARG;
+    if (misaligned8(workspace) || misaligned4(out)) return QC_ERR_ALIGN;
+    return launched(qc::launch_grad_norm(l, gtype == QC_BF16, max_norm, workspace, out, hs(stream)));
+}
+
+int qc_adamw_multi(void* const* params, int32_t ptype, const void* const* grads, int32_t gtype,
+                   const int64_t* offsets, const int32_t* seg_first, int32_t ntensors, int64_t n, float* master,
+                   float* m, float* v, double lr, double beta1, double beta2, double eps, double weight_decay,
+                   int64_t step, const float* grad_scale, const float* schedule, qc_stream_t stream) {
+    qc::AdamwList l;
+    qc::AdamwStep s;
+    const int st = check_adamw({params, ptype, grads, gtype, offsets, seg_first, ntensors, n, master, lr, beta1, beta2,
+                                eps, weight_decay, step, grad_scale, schedule},
+                               l, s);
+    if (st != QC_OK || n == 0) return st;
+    if (!m || !v) return QC_ERR_ARG;
+    if (misaligned(m) || misaligned(v)) return QC_ERR_ALIGN;
+    return launched(qc::launch_adamw(l, m, v, s, hs(stream)));
+}
+
+int qc_adamw8_multi(void* const* params, int32_t ptype, const void* const* grads, int32_t gtype,
+                    const int64_t* offsets, const int32_t* seg_first, int32_t ntensors, int64_t n, float* master,
+                    uint8_t* m_codes, float* m_scale, uint8_t* r_codes, float* r_scale, double lr, double beta1,
+                    double beta2, double eps, double weight_decay, int64_t step, const float* grad_scale,
+                    const float* schedule, qc_stream_t stream) {
+    qc::AdamwList l;
+    qc::AdamwStep s;
+    const int st = check_adamw({params, ptype, grads, gtype, offsets, seg_first, ntensors, n, master, lr, beta1, beta2,
+                                eps, weight_decay, step, grad_scale, schedule},
+                               l, s);
+    if (st != QC_OK || n == 0) return st;
+    if (!m_codes || !m_scale || !r_codes || !r_scale) return QC_ERR_ARG;
+    if (misaligned(m_codes) || misaligned(m_scale) || misaligned(r_codes) || misaligned(r_scale)) return QC_ERR_ALIGN;
+    return launched(qc::launch_adamw8(l, m_codes, m_scale, r_codes, r_scale, s, hs(stream)));
+}
+
+int qc_encode_state8(int32_t kind, const float* x, int64_t n, uint8_t* codes, float* scale, qc_stream_t stream) {
+    if (n < 0 || n > kMaxListElems) return QC_ERR_ARG;
+    if (kind != QC_STATE_M && kind != QC_STATE_R) return QC_ERR_UNSUPPORTED;
+    if (n == 0) return QC_OK;
+    if (!x || !codes || !scale) return QC_ERR_ARG;
+    if (misaligned(x) || misaligned(codes) || misaligned(scale)) return QC_ERR_ALIGN;
+    return launched(qc::launch_encode_state8(kind, x, n, codes, scale, hs(stream)));
+}
+
+int qc_decode_state8(int32_t kind, const uint8_t* codes, const float* scale, int64_t n, void* out, int32_t otype,
+                     qc_stream_t stream) {
+    if (n < 0 || n > kMaxListElems || bad_type(otype)) return QC_ERR_ARG;
+    if (kind != QC_STATE_M && kind != QC_STATE_R) return QC_ERR_UNSUPPORTED;
+    if (n == 0) return QC_OK;
+    if (!codes || !scale || !out) return QC_ERR_ARG;
+    if (misaligned(codes) || misaligned(scale) || misaligned(out)) return QC_ERR_ALIGN;
+    return launched(qc::launch_decode_state8(kind, codes, scale, n, out, otype == QC_BF16, hs(stream)));
 }
 
 }  // extern "C"

@@ -139,4 +139,52 @@ hipError_t launch_ckpt8_wgrad(const void* dy, bool dy_bf16, int64_t ldy, const v
                               int64_t rows, int64_t n, int64_t dim, void* dw, bool dw_bf16, int64_t ldw,
                               bool accumulate, void* workspace, hipStream_t stream);
 
+// MXFP4: either pair of outputs may be NULL.
+hipError_t launch_encode_mxfp4(const void* x, bool bf16, int64_t rows, int64_t dim, int64_t ldx, void* codes,
+                               void* scales, void* codes_t, void* scales_t, hipStream_t stream);
+
+hipError_t launch_decode_mxfp4(const void* codes, const void* scales, int64_t rows, int64_t dim, void* out, bool bf16,
+                               int64_t ldo, hipStream_t stream);
+
+int64_t matmul_mxfp4_workspace(int64_t m, int64_t n, int64_t k);
+hipError_t launch_matmul_mxfp4(const void* a, const void* a_scales, const void* b, const void* b_scales, int64_t m,
+                               int64_t n, int64_t k, void* c, bool bf16, int64_t ldc, bool accumulate,
+                               void* workspace, hipStream_t stream);
+int64_t linear_mxfp4_workspace(int64_t m, int64_t n, int64_t k, bool x_bf16);
+hipError_t launch_linear_mxfp4(const void* x, bool x_bf16, int64_t ldx, const void* b, const void* b_scales, int64_t m,
+                               int64_t n, int64_t k, void* c, bool bf16, int64_t ldc, void* workspace,
+                               hipStream_t stream);
+
+// The optimizer's constants of one step: schedule, where given, replaces the
+// last three (see qc_adamw_multi).
+struct AdamwStep {
+    float beta1, beta2, rest1, rest2;  // rest: 1 - beta
+    float eps;
+    double weight_decay, log2_beta1, log2_beta2;
+    float decay, rate, root;  // 1 - lr weight_decay, lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
+    uint32_t t;
+    const float* grad_scale;
+    const float* schedule;
+};
+
+// Gradients, parameters and flat states; `wide` states are fp32, others codes
+// with a scale per block.
+struct AdamwList {
+    ListSrc grads;
+    void* const* params;
+    bool g_bf16, p_bf16;
+    float* master;
+};
+
+hipError_t launch_adamw(const AdamwList& l, float* m, float* v, const AdamwStep& s, hipStream_t stream);
+hipError_t launch_adamw8(const AdamwList& l, uint8_t* m_codes, float* m_scale, uint8_t* r_codes, float* r_scale,
+                         const AdamwStep& s, hipStream_t stream);
+hipError_t launch_encode_state8(int32_t kind, const float* x, int64_t n, uint8_t* codes, float* scale,
+                                hipStream_t stream);
+hipError_t launch_decode_state8(int32_t kind, const uint8_t* codes, const float* scale, int64_t n, void* out,
+                                bool bf16, hipStream_t stream);
+int64_t grad_norm_workspace(int64_t n);
+hipError_t launch_grad_norm(const ListSrc& l, bool bf16, double max_norm, void* workspace, float* out,
+                            hipStream_t stream);
+
 }  // namespace qc

@@ -654,6 +654,204 @@ int qc_swiglu_ckpt8_backward(const void* dh, int32_t dhtype, int64_t lddh, const
                              const uint8_t* gate_exps, const int8_t* up_codes, const uint8_t* up_exps, int64_t rows,
                              int64_t dim, void* dgate, void* dup, int64_t ldg, qc_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------
+ * 4-bit matrix operators: matrices in microscaled 4-bit floating point
+ * (MXFP4: E2M1 values, a power-of-two scale per 32 of them) and their
+ * product.  The rules of the 8-bit matrix operators above hold here too;
+ * rows are at most 2^23 values long in the products.
+ * ---------------------------------------------------------------------
+ */
+
+/*
+ * MXFP4: per group of QC_MX_GROUP = 32 consecutive values of a row (the last
+ * group of a row may be short), E = the smallest integer in [-126, 126] with
+ * max|x| < 7 * 2^E; a code is the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (codes
+ * 0..7, ties to the even code) to |x| * 2^-E, plus 8 where x has a minus sign
+ * (zeros too).  No value is off by more than half of the step 2^(E+1) that
+ * lies above 4 * 2^E.  The scale byte is E + 127 (E8M0).  A group with an
+ * infinity or a NaN has byte 255 and codes 0 and stands for NaNs, and so does
+ * every result of a product that it enters.
+ *
+ *   codes    two a byte, the value with the even index in the low half; row
+ *            pitch 16 * ceil(dim / 32) bytes, written entirely (zeros past
+ *            dim).
+ *   scales   uint8, row pitch 4 * ceil(dim / 128) bytes, written entirely
+ *            (zeros past the last group).
+ * qc_mxfp4_bytes gives the bytes of both for a matrix; for sizes that are bad
+ * (ARG) it leaves *code_bytes and *scale_bytes as they are.
+ *
+ * qc_encode_mxfp4 encodes x [rows][dim] into codes and scales, and its
+ * transpose [dim][rows], groups along the rows of x, into codes_t and
+ * scales_t, from one reading of x.  Either pair may be NULL: a weight matrix w
+ * of [n][k] enters the forward product as it is and that of the input's
+ * gradient transposed; the gradient of the weights takes both its operands
+ * transposed.  Unlike for the other calls, rows == 0 is empty for both pairs.
+ * qc_decode_mxfp4 writes the values; they are exact in fp32 and in bf16.
+ * Errors: ARG (NULL x or out, one of a pair NULL, both pairs NULL, bad type,
+ *         rows < 0, dim < 1, a stride below its row, 2^24 tiles of 128 x 128
+ *         values or more), ALIGN, UNSUPPORTED (rows, where transposed, or dim
+ *         above 2^34, not for qc_mxfp4_bytes).
+ */
+#define QC_MX_GROUP 32
+int qc_mxfp4_bytes(int64_t rows, int64_t dim, int64_t* code_bytes, int64_t* scale_bytes);
+int qc_encode_mxfp4(const void* x, int32_t xtype, int64_t rows, int64_t dim, int64_t ldx, uint8_t* codes,
+                    uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t, qc_stream_t stream);
+int qc_decode_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t dim, void* out,
+                    int32_t otype, int64_t ldo, qc_stream_t stream);
+
+/*
+ * Product of two MXFP4 matrices, both with k along the rows:
+ *   c[i][j] (+)= sum over l of A[i][l] * B[j][l].
+ * Products are exact, sums are taken in fp32 in an order that depends on the
+ * sizes alone (the same call gives the same bits) and rounded once to c's
+ * type.  Products and sums below the smallest normal number (2^-126) may
+ * count as zero.
+ *
+ *   a, a_scales   MXFP4 of [m][k]: tokens.   b, b_scales   of [n][k]: weights.
+ *                 Codes past k in the last group are zeros, as the encoder
+ *                 writes them.
+ *   c             [m][n] of type ctype, row stride ldc, written; with
+ *                 accumulate != 0 (QC_F32 only) added to.
+ *   k             at least 1.
+ *   workspace     device memory of at least qc_matmul_mxfp4_workspace() bytes
+ *                 (NULL if that is 0), used during the call: where k is long
+ *                 and m * n small, k is split over several blocks, whose sums
+ *                 are held there until they are joined.  Calls that may run
+ *                 at the same time, from two streams or two captured graphs,
+ *                 need one each.  qc_matmul_mxfp4_workspace() is -1, no
+ *                 status, for bad sizes.
+ * Errors: ARG (NULL pointer, bad type, m or n < 0, k < 1, a stride below its
+ *         row, too little workspace, 2^23 tiles of 256 x 256 or more), ALIGN,
+ *         UNSUPPORTED (accumulate with a bf16 c, k above 2^23).
+ */
+int64_t qc_matmul_mxfp4_workspace(int64_t m, int64_t n, int64_t k);
+int qc_matmul_mxfp4(const uint8_t* a, const uint8_t* a_scales, const uint8_t* b, const uint8_t* b_scales, int64_t m,
+                    int64_t n, int64_t k, void* c, int32_t ctype, int64_t ldc, int32_t accumulate, void* workspace,
+                    int64_t workspace_bytes, qc_stream_t stream);
+
+/*
+ * Linear layer on weights in MXFP4: x [m][k] of type xtype, row stride ldx, is
+ * encoded as qc_encode_mxfp4 encodes it, and c = X B^T as qc_matmul_mxfp4
+ * forms it (the order of the sums may differ).  A few tokens take one launch;
+ * for more, the codes of x lie in the workspace between two.
+ *   workspace     as for qc_matmul_mxfp4, qc_linear_mxfp4_workspace() bytes.
+ * Errors: as qc_matmul_mxfp4, plus ARG for an x of 2^24 tiles of 128 x 128
+ *         values or more.
+ */
+int64_t qc_linear_mxfp4_workspace(int64_t m, int64_t n, int64_t k, int32_t xtype);
+int qc_linear_mxfp4(const void* x, int32_t xtype, int64_t ldx, const uint8_t* b, const uint8_t* b_scales, int64_t m,
+                    int64_t n, int64_t k, void* c, int32_t ctype, int64_t ldc, void* workspace,
+                    int64_t workspace_bytes, qc_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------
+ * The optimizer's side of a tensor list: what becomes of the gradients that
+ * qc_decode_multi or the receive-side sums leave.  Gradients and parameters
+ * are lists of tensors of the same sizes in the same order, read and written
+ * in place; optimizer states are flat arrays laid out for the concatenation,
+ * as the error feedback of the *_multi encoders is.  params and grads are
+ * device arrays of ntensors device pointers (fp32 or bf16 by ptype and gtype,
+ * aligned to the element); offsets, seg_first, ntensors and n as for
+ * qc_encode_uniform_multi.  No tensor overlaps another one or an array of the
+ * call.  Infinities and NaNs are accepted and stay visible.  n == 0 is a valid
+ * empty call that writes nothing.
+ * ---------------------------------------------------------------------
+ */
+
+/*
+ * The norm of a list of gradients and the coefficient that clips it:
+ *   out[0] = sqrt(sum of g^2),  out[1] = min(1, max_norm / out[0]) (1 for a
+ * norm of zero, a NaN for a norm that is not finite), both from a sum in 64
+ * bits whose order depends on n alone.
+ *
+ *   max_norm   above 0; infinity for the norm alone.
+ *   workspace  device memory of at least qc_grad_norm_workspace(n) bytes,
+ *              used during the call; 8-byte aligned.  (-1 for n < 0.)
+ *   out        fp32[2], written (4-byte aligned).
+ * Errors: ARG (NULL pointer, bad type, n < 0, ntensors < 1, max_norm not above
+ *         0, too little workspace), ALIGN.
+ */
+int64_t qc_grad_norm_workspace(int64_t n);
+int qc_grad_norm_multi(const void* const* grads, int32_t gtype, const int64_t* offsets, const int32_t* seg_first,
+                       int32_t ntensors, int64_t n, double max_norm, void* workspace, int64_t workspace_bytes,
+                       float* out, qc_stream_t stream);
+
+/*
+ * One AdamW step (decoupled weight decay) over a list of tensors.  With g the
+ * gradient times *grad_scale, t the step, in fp32:
+ *   m = beta1 m + (1 - beta1) g,    v = beta2 v + (1 - beta2) g^2,
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps).
+ *
+ *   params      read (unless master is given) and written, rounded once.
+ *   master      fp32[n] or NULL: with bf16 parameters, the weights proper,
+ *               read and written in the parameters' place; the parameters
+ *               become their rounded copy.
+ *   m, v        fp32[n], read and written; zeros before the first step.
+ *   step        t, from 1 on.
+ *   grad_scale  device fp32[1] or NULL (1): out + 1 of qc_grad_norm_multi, or
+ *               the reciprocal of a loss scale (4-byte aligned).
+ *   schedule    device fp32[2] or NULL: {lr, t}, read by the call in the
+ *               place of its arguments, so that a captured graph can be
+ *               replayed for other steps (t a whole number from 1 to 2^24).
+ * Errors: ARG (NULL pointer, bad type, n < 0, ntensors < 1, master with fp32
+ *         parameters, lr, eps or weight_decay negative or not finite, beta1
+ *         or beta2 outside [0, 1), step < 1), ALIGN.
+ */
+int qc_adamw_multi(void* const* params, int32_t ptype, const void* const* grads, int32_t gtype,
+                   const int64_t* offsets, const int32_t* seg_first, int32_t ntensors, int64_t n, float* master,
+                   float* m, float* v, double lr, double beta1, double beta2, double eps, double weight_decay,
+                   int64_t step, const float* grad_scale, const float* schedule, qc_stream_t stream);
+
+/*
+ * The same step with its states in 8 bits: m and r = sqrt(v), each a code per
+ * element and an fp32 scale per block of QC_STATE_BLOCK = 256 consecutive
+ * elements of the concatenation (the last may be short); 2 + 1/32 bytes an
+ * element.
+ *
+ * A code c > 0 stands for F(c) * scale, code 0 for 0:
+ *   QC_STATE_M  sign (bit 7) and 7 bits: F(c) = the fp32 number with the bits
+ *               (896 + c) << 20: 1/8 apart within a power of two, from
+ *               1.125 * 2^-15 to 1.875;
+ *   QC_STATE_R  8 bits, no sign: (1792 + c) << 19: 1/16 apart, from 1.0625 *
+ *               2^-15 to 1.9375.
+ * scale = max(amax * fl(1 / F(largest)), 2^-100) with amax the block's largest
+ * magnitude, 0 where that is 0.  A block with an infinity or a NaN gets scale
+ * NaN and codes 0 and stands for NaNs.
+ *
+ * After a step, y = |x| * fl(1 / scale) lies between two codes; it becomes the
+ * upper one where its place between them is above 1 - u, u = u32 / 2^32 with
+ *   u32 = 0x91E10DA5 * i + 0xC13FA9A9 * t  (+ 2^31 for r)  mod 2^32
+ * for element i of the concatenation at step t.  For every element these u
+ * cover [0, 1) evenly over the steps, so a state that moves by less than a
+ * code a step (v does: by 1 - beta2 of it) moves on average as it should,
+ * where rounding to nearest would leave it in its place.  Below F(1), m
+ * becomes 0 or F(1) by the same rule, and r above zero becomes F(1), so that no
+ * denominator vanishes.  The step itself uses m and v before they are rounded.
+ *
+ *   m_codes, r_codes   uint8[n]; m_scale, r_scale  fp32[ceil(n / 256)]; read
+ *                      and written; zeros before the first step.
+ *   Other arguments and errors as qc_adamw_multi.
+ *
+ * qc_encode_state8 and qc_decode_state8 turn n values (kind QC_STATE_M, or
+ * QC_STATE_R: r = sqrt(v), not below 0) into codes and scales, with u = 1/2
+ * (nearest), and codes into fp32 or bf16 (rounded once), to carry states
+ * between the two forms and to save them.  They are flat: x, out and codes are
+ * n elements.  Errors: ARG (NULL pointer, n < 0, bad type), ALIGN, UNSUPPORTED
+ * (kind).
+ */
+#define QC_STATE_BLOCK 256
+enum qc_state { QC_STATE_M = 0, QC_STATE_R = 1 };
+int qc_adamw8_multi(void* const* params, int32_t ptype, const void* const* grads, int32_t gtype,
+                    const int64_t* offsets, const int32_t* seg_first, int32_t ntensors, int64_t n, float* master,
+                    uint8_t* m_codes, float* m_scale, uint8_t* r_codes, float* r_scale, double lr, double beta1,
+                    double beta2, double eps, double weight_decay, int64_t step, const float* grad_scale,
+                    const float* schedule, qc_stream_t stream);
+int qc_encode_state8(int32_t kind, const float* x, int64_t n, uint8_t* codes, float* scale, qc_stream_t stream);
+int qc_decode_state8(int32_t kind, const uint8_t* codes, const float* scale, int64_t n, void* out, int32_t otype,
+                     qc_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
