@@ -599,21 +599,25 @@ def qc_swiglu_ckpt8_backward(dh, dhtype, lddh, gate_codes, gate_exps, up_codes, 
 # ------------------------------------------------- 4-bit matrix operators
 
 
-def _now():
-    import torch
+_device = None  # the current device's index
 
-    return torch.cuda.current_device()
+
+def _now():
+    global _device
+    if _device is None:
+        import torch
+
+        torch.cuda.init()
+        _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _device()
 
 
 def _here(*tensors):
     """Refuses tensors of another device than the current one, whose stream and
     kernels the call would use."""
-    now = None
+    now = _now()
     for t in tensors:
-        if t is None or isinstance(t, int) or not t.is_cuda:
-            continue
-        now = _now() if now is None else now
-        if t.get_device() != now:
+        if t is not None and t.__class__ is not int and t.get_device() != now and t.is_cuda:
             raise ValueError(f"a tensor is on GPU {t.get_device()}, the current one is {now}")
 
 

@@ -132,55 +132,58 @@ struct ScaleLoader {
         pitch = (int)spitch;
         rsrc = buffer_of(scales + row0 * spitch, last * pitch + len);
     }
-    // Rows [first, first + 32) of chunk c to `lds`; `len` bytes of a row exist.
+    // Rows [first, first + 32) of chunk c to `lds`, by the waves whose mask is not
+    // 0; `len` bytes of a row exist.
     // FAST: they are at least one piece, and either whole pieces or reach the
     // chunk's end.  What lies past them repeats others and is not used.
     template <bool FAST>
-    __device__ __forceinline__ void load(int first, int c, int len, uint32_t lds) const {
+    __device__ __forceinline__ void load(int mask, int first, int c, int len, uint32_t lds) const {
         const int l = lane_id();
         if constexpr (FAST) {
             const int r = l >> 1, at = min(c * kScaleBytes + scale_piece(r, l & 1) * 16, len - 16);
-            load_lds16(rsrc, lds, min(first + r, last) * pitch + at, 0);
+            load_lds16_if(mask, rsrc, lds, min(first + r, last) * pitch + at);
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int slot = e * 16 + (l >> 2), r = slot >> 1;
                 const int at = c * kScaleBytes + scale_piece(r, slot & 1) * 16 + (l & 3) * 4;
-                load_lds4(rsrc, lds + e * 256, min(first + r, last) * pitch + min(at, len - 4), 0);
+                load_lds4_if(mask, rsrc, lds + e * 256, min(first + r, last) * pitch + min(at, len - 4));
             }
         }
     }
 };
 
-// A wave reads its fragments ahead of their use, into the next stage too; the
-// wait for that stage, and the only barrier, stand where the last fragments of
-// this one have been read, and the fragments already in registers keep the
-// matrix cores busy across it.  The loads of the stage NB further on follow at
-// once, over the one just left.  A stage has no branch: the compiler would move
-// matrix instructions across it, and their operands would fill the registers.
-// So loads are issued past the end too (they repeat the last pieces), and where
-// a tile has fewer blocks of scales a stage than waves, several load the same.
-template <class T, bool ADD, int BN, int BM, int WN, int WM, int NB>
-__global__ void __launch_bounds__(WN * WM * WAVE)
+// WN x WM waves share the tile, and KW (1 or 2) of them each one's part: two
+// take the four instructions' worth of k of a stage between them, so that a
+// wave of a small tile has two fragments of either side to multiply, and
+// join their sums at the end.  A wave reads the fragments of its next step while it
+// multiplies those of this one.  Before the last step of a stage has its turn,
+// all of the stage's fragments have been read: there stand the wait for the
+// next stage and the only barrier, and the matrix cores work on across it.
+// The loads of the stage NB further on follow, over the one just left: SOON of
+// them at once, the others with the steps of the next stage, as many at a time
+// would hold up the wave (16384 x 8192 x 8192: 487 us against 512).  A stage
+// has no branch: the compiler would move matrix instructions across it, and
+// their operands would fill the registers.  So loads are issued past the end
+// too (they repeat the last pieces), and those of the scales by fewer waves
+// than there are with an empty mask in the others.
+template <class T, bool ADD, int BN, int BM, int WN, int WM, int KW, int NB>
+__global__ void __launch_bounds__(WN * WM * KW * WAVE)
 k_mm_mx_pipe(Args g, T* __restrict__ c) {
-    constexpr int NW = WN * WM;
+    constexpr int NW = WN * WM * KW, STEPS = 4 / KW;
     constexpr int FN = BN / WN / 32, FM = BM / WM / 32;
-    constexpr int AHEAD = FN >= 4 ? 2 : 1;          // weight fragments read ahead (of a ring)
-    constexpr int RING = FN >= 4 ? 4 : 2;
-    constexpr int KK = 4, STEPS = KK * FN;          // a step: one weight fragment
-    constexpr int H = (FN + 1) / 2, TURN = STEPS - H;  // the barrier's step
     constexpr int TB = BN * kStage, STAGE = (BN + BM) * kStage;  // weights first, then tokens
-    constexpr int NC = NB == 2 ? 2 : 3, SBLOCKS = (BN + BM) / 128;  // chunks in LDS; blocks of scales a stage
-    // a stage's last read comes before the barrier, the next one's first after it
-    static_assert(FM >= 1 && STEPS - 1 - AHEAD <= TURN && STEPS - AHEAD >= TURN && SBLOCKS * 128 == BN + BM, "tile");
-    static_assert(NB * STAGE + NC * (BN + BM) * kScaleBytes <= 160 * 1024 && NB >= 2 && NB <= 4, "LDS");
-    __shared__ __align__(1024) uint8_t lds[NB * STAGE + NC * (BN + BM) * kScaleBytes];
+    constexpr int NC = NB == 2 ? 2 : 3;                          // chunks in LDS
+    constexpr int BLOCKS = (BN + BM) / 32, SBLOCKS = (BLOCKS + 3) / 4;  // of scales: a chunk's, a stage's
+    static_assert(FN >= 1 && FM % KW == 0 && FN * WN * 32 == BN && FM * WM * 32 == BM && STEPS % 2 == 0, "tile");
+    static_assert(NB * STAGE + NC * BLOCKS * 1024 <= 160 * 1024 && NB >= 2 && NB <= 4, "LDS");
+    __shared__ __align__(1024) uint8_t lds[NB * STAGE + NC * BLOCKS * 1024];
 
     const uint32_t tn = (uint32_t)((g.b.rows + BN - 1) / BN), tm = (uint32_t)((g.a.rows + BM - 1) / BM);
     const Tile2 tile = tile_of<4>(blockIdx.x, tn, tm);
     const int64_t n0 = (int64_t)tile.x * BN, m0 = (int64_t)tile.y * BM;
     const int w = __builtin_amdgcn_readfirstlane(wave_id());
-    const int wn = w % WN, wm = w / WN;
+    const int wk = w % KW, wn = w / KW % WN, wm = w / KW / WN;
     const int l = lane_id(), half = l >> 5;
     // this split's part of a row
     const int first = (int)blockIdx.y * g.stages_per_split;
@@ -189,35 +192,36 @@ k_mm_mx_pipe(Args g, T* __restrict__ c) {
     const int stages = (len + kStage - 1) / kStage, whole = len / kStage;
     Loader<BN, NW> lb;
     Loader<BM, NW> la;
-    constexpr int LOADS = lb.N + la.N;
+    constexpr int LOADS = lb.N + la.N, SOON = LOADS / 4;
+    constexpr int SLOTS = (STEPS - 1) * FN, LATER = (LOADS - SOON + SLOTS - 1) / SLOTS;  // of the others at a time
     lb.init(g.b.codes + first * kStage, g.pitch, n0, g.b.rows, len, w);
     la.init(g.a.codes + first * kStage, g.pitch, m0, g.a.rows, len, w);
     ScaleLoader xb, xa;
     xb.init(g.b.scales + first * 8, g.spitch, n0, g.b.rows, BN, slen);
     xa.init(g.a.scales + first * 8, g.spitch, m0, g.a.rows, BM, slen);
 
-    const uint32_t lds0 = lds_addr(lds);
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
     auto fetch_part = [&](auto fast, int part, int buf, int s) {  // one of LOADS
         constexpr bool FAST = decltype(fast)::value;
         if (part < lb.N) lb.template load<FAST>(part, lds0 + buf * STAGE, w, s, len);
         else la.template load<FAST>(part - lb.N, lds0 + buf * STAGE + TB, w, s, len);
     };
     auto fetch_scales = [&](auto fast, int chunk, int quarter) {
-        const int block = quarter * SBLOCKS + w % SBLOCKS;
+        const int block = min(quarter * SBLOCKS + w % SBLOCKS, BLOCKS - 1);
+        const int mask = w < SBLOCKS ? -1 : 0;
         const bool weights = block * 32 < BN;
         const ScaleLoader x = {weights ? xb.rsrc : xa.rsrc, weights ? xb.last : xa.last, xb.pitch};
-        x.template load<decltype(fast)::value>(block * 32 - (weights ? 0 : BN), chunk, slen,
-                                               lds0 + NB * STAGE + (chunk % NC) * ((BN + BM) * kScaleBytes) +
-                                                   block * 1024);
+        x.template load<decltype(fast)::value>(mask, block * 32 - (weights ? 0 : BN), chunk, slen,
+                                               lds0 + NB * STAGE + (chunk % NC * BLOCKS + block) * 1024);
     };
 
     // fragments: row l % 32, piece half * 4 + kk (an xor of kk * 16 in the address)
     const int frag = (l & 31) * kStage + (piece_slot(l & 31, half * 4) << 4);
     const int rb = wn * FN * 32 * kStage + frag, ra = TB + wm * FM * 32 * kStage + frag;
-    auto read_b = [&](auto fast, int buf, int q, int s) {
-        i32x4 v = *reinterpret_cast<const i32x4*>(lds + buf * STAGE + (rb ^ (q / FN * 16)) + q % FN * (32 * kStage));
+    auto read_b = [&](auto fast, int buf, int kk, int i, int s) {
+        i32x4 v = *reinterpret_cast<const i32x4*>(lds + buf * STAGE + (rb ^ (kk * 16)) + i * (32 * kStage));
         // the weights' pieces past a row's end become zeros (one side is enough)
-        if (!decltype(fast)::value && s * kStage + (half * 4 + q / FN) * 16 >= len) v = i32x4{0, 0, 0, 0};
+        if (!decltype(fast)::value && s * kStage + (half * 4 + kk) * 16 >= len) v = i32x4{0, 0, 0, 0};
         return v;
     };
     auto read_a = [&](int buf, int kk, int j) {
@@ -225,7 +229,7 @@ k_mm_mx_pipe(Args g, T* __restrict__ c) {
     };
     int sb[FN], sa[FM];
     auto read_scales = [&](int s, int (&nb)[FN], int (&na)[FM]) {
-        const uint8_t* at = lds + NB * STAGE + (s / kChunk % NC) * ((BN + BM) * kScaleBytes) + (l & 31) * kScaleBytes +
+        const uint8_t* at = lds + NB * STAGE + (s / kChunk % NC) * (BLOCKS * 1024) + (l & 31) * kScaleBytes +
                             (scale_piece(l & 31, (s >> 1) & 1) << 4) + ((s & 1) << 3) + (half << 2);
         const bool there = s * 8 + half * 4 < slen;  // words past a row's end are another row's
 #pragma unroll
@@ -239,38 +243,54 @@ k_mm_mx_pipe(Args g, T* __restrict__ c) {
             na[j] = there ? v : 0;
         }
     };
+    // a wave's own instructions of a stage: with KW > 1 the byte of the scale
+    // words that they name depends on the wave, so it is brought down
+    auto mine = [&](int (&x)[FN], int (&y)[FM]) {
+        if constexpr (KW > 1) {
+#pragma unroll
+            for (int i = 0; i < FN; ++i) x[i] = (int)((uint32_t)x[i] >> (8 * STEPS * wk));
+#pragma unroll
+            for (int j = 0; j < FM; ++j) y[j] = (int)((uint32_t)y[j] >> (8 * STEPS * wk));
+        }
+    };
 
     f32x16 acc[FN][FM] = {};
-    i32x4 fb[RING], fa[2][FM];
+    i32x4 fb[2][FN], fa[2][FM];
     // Stage s in buffer `buf`, the next one in `next`.  Fast: stages up to s +
     // NB exist and are whole.
     auto stage = [&](int buf, int next, auto fast, int s) {
         int nb[FN], na[FM];
 #pragma unroll
-        for (int q = 0; q < STEPS; ++q) {
-            const int kk = q / FN, i = q % FN;
-            if (q + AHEAD < STEPS) fb[(q + AHEAD) % RING] = read_b(fast, buf, q + AHEAD, s);
-            if (q == TURN) {
+        for (int t = 0; t < STEPS; ++t) {
+            const bool turn = t + 1 == STEPS;
+            if (turn) {
                 lds_landed_but<(NB - 2) * LOADS>();
                 fetch_scales(fast, (s + NB - 1) / kChunk + 1, (s + NB - 1) % kChunk);
                 read_scales(s + 1, nb, na);
             }
-            if (q + AHEAD >= STEPS) fb[(q + AHEAD) % RING] = read_b(fast, next, q + AHEAD - STEPS, s + 1);
-            if (i >= FN - H) {
-                // this step's share of the token fragments and of the loads
-                const int part = i - (FN - H);
+            // the next step's fragments
+            const int kk = turn ? wk * STEPS : wk * STEPS + t + 1, at = turn ? next : buf, ns = turn ? s + 1 : s;
 #pragma unroll
-                for (int e = part * FM / H; e < (part + 1) * FM / H; ++e)
-                    fa[(kk + 1) & 1][e] = kk + 1 < KK ? read_a(buf, kk + 1, e) : read_a(next, 0, e);
-                if (kk + 1 == KK) {
+            for (int j = 0; j < FM; ++j) fa[(t + 1) & 1][j] = read_a(at, kk, j);
 #pragma unroll
-                    for (int d = part * LOADS / H; d < (part + 1) * LOADS / H; ++d) fetch_part(fast, d, buf, s + NB);
+            for (int i = 0; i < FN; ++i) {
+                fb[(t + 1) & 1][i] = read_b(fast, at, kk, i, ns);
+                if (turn) {
+#pragma unroll
+                    for (int d = i * SOON / FN; d < (i + 1) * SOON / FN; ++d) fetch_part(fast, d, buf, s + NB);
+                } else {
+                    // the rest of the stage before's loads
+#pragma unroll
+                    for (int d = SOON + (t * FN + i) * LATER; d < min(LOADS, SOON + (t * FN + i + 1) * LATER); ++d)
+                        fetch_part(fast, d, (buf + NB - 1) % NB, s + NB - 1);
                 }
-            }
 #pragma unroll
-            for (int j = 0; j < FM; ++j) acc[i][j] = mfma32(kk, fb[q % RING], fa[kk & 1][j], acc[i][j], sb[i], sa[j]);
-            __builtin_amdgcn_sched_barrier(0);  // keeps the reads where they stand, ahead of their use
+                for (int j = 0; j < FM; ++j)
+                    acc[i][j] = mfma32(t, fb[t & 1][i], fa[t & 1][j], acc[i][j], sb[i], sa[j]);
+                __builtin_amdgcn_sched_barrier(0);  // keeps the reads where they stand, ahead of their use
+            }
         }
+        mine(nb, na);
 #pragma unroll
         for (int i = 0; i < FN; ++i) sb[i] = nb[i];
 #pragma unroll
@@ -282,14 +302,15 @@ k_mm_mx_pipe(Args g, T* __restrict__ c) {
 #pragma unroll
     for (int s = 0; s < NB; ++s) {
 #pragma unroll
-        for (int part = 0; part < LOADS; ++part) fetch_part(std::false_type{}, part, s, s);
+        for (int part = 0; part < (s + 1 < NB ? LOADS : SOON); ++part) fetch_part(std::false_type{}, part, s, s);
     }
-    lds_landed_but<(NB - 1) * LOADS>();
+    lds_landed_but<(NB - 2) * LOADS + SOON>();
     read_scales(0, sb, sa);
+    mine(sb, sa);
 #pragma unroll
-    for (int j = 0; j < FM; ++j) fa[0][j] = read_a(0, 0, j);
+    for (int j = 0; j < FM; ++j) fa[0][j] = read_a(0, wk * STEPS, j);
 #pragma unroll
-    for (int q = 0; q < AHEAD; ++q) fb[q] = read_b(std::false_type{}, 0, q, 0);
+    for (int i = 0; i < FN; ++i) fb[0][i] = read_b(std::false_type{}, 0, wk * STEPS, i, 0);
     // fast stages: where rows of scales end inside a piece, those whose chunks are whole
     const int fast_end = min(whole, slen % 16 == 0 ? whole : slen / kScaleBytes * kChunk - kChunk + 1);
     int s = 0;
@@ -299,17 +320,52 @@ k_mm_mx_pipe(Args g, T* __restrict__ c) {
     }
 #pragma unroll 1
     for (; s < stages; ++s) stage(s % NB, (s + 1) % NB, std::false_type{}, s);
+    lds_landed();  // every wave has read its last fragments, and no load is on its way
+
+    // Two waves with parts of one sum exchange halves of it, tokens by tokens.
+    constexpr int OM = FM / KW;
+    if constexpr (KW == 2) {
+        static_assert(NW * FN * OM * 4096 <= NB * STAGE, "exchange");
+        f32x4* out = reinterpret_cast<f32x4*>(lds + w * (FN * OM * 4096)) + l;
+        const f32x4* in = reinterpret_cast<const f32x4*>(lds + (w ^ 1) * (FN * OM * 4096)) + l;
+#pragma unroll
+        for (int j = 0; j < OM; ++j)
+#pragma unroll
+            for (int i = 0; i < FN; ++i) {
+                f32x16 give;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    give[e] = wk ? acc[i][j][e] : acc[i][j + OM][e];
+                    acc[i][j][e] = wk ? acc[i][j + OM][e] : acc[i][j][e];
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    out[((j * FN + i) * 4 + q) * WAVE] =
+                        f32x4{give[4 * q], give[4 * q + 1], give[4 * q + 2], give[4 * q + 3]};
+            }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < OM; ++j)
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const f32x4 v = in[((j * FN + i) * 4 + q) * WAVE];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
+                }
+        __syncthreads();
+    }
 
     // 32 tokens at a time through the wave's part of LDS, so that a store takes
     // whole 16-byte pieces of a few rows of C.  Piece p of row r in slot p ^ r.
     constexpr int COLS = FN * 32, RB = COLS * (int)sizeof(T), PR = RB / 16, E = 16 / (int)sizeof(T);
     static_assert((PR & (PR - 1)) == 0 && PR <= WAVE && NW * 32 * RB <= NB * STAGE, "a wave's part of LDS");
-    lds_landed();  // every wave has read its last fragments, and no load is on its way
     uint8_t* own = lds + w * (32 * RB);
     c += (int64_t)blockIdx.y * g.split_stride;
     const bool inside = n0 + BN <= g.b.rows && m0 + BM <= g.a.rows;
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
+    for (int j = 0; j < OM; ++j) {
 #pragma unroll
         for (int i = 0; i < FN; ++i) {
 #pragma unroll
@@ -324,7 +380,7 @@ k_mm_mx_pipe(Args g, T* __restrict__ c) {
             }
         }
         wave_lds_sync();
-        const int64_t row0 = m0 + (wm * FM + j) * 32, col0 = n0 + wn * COLS;
+        const int64_t row0 = m0 + (wm * FM + wk * OM + j) * 32, col0 = n0 + wn * COLS;
 #pragma unroll
         for (int q = 0; q < RB / 32; ++q) {
             const int r = (q * WAVE + l) / PR, p = (q * WAVE + l) % PR;
@@ -349,11 +405,11 @@ k_mm_mx_pipe(Args g, T* __restrict__ c) {
     }
 }
 
-template <class T, bool ADD, int BN, int BM, int WN, int WM, int NB>
+template <class T, bool ADD, int BN, int BM, int WN, int WM, int KW, int NB>
 hipError_t launch_pipe(const Args& g, int splits, T* c, hipStream_t stream) {
     const int64_t tiles = ((g.b.rows + BN - 1) / BN) * ((g.a.rows + BM - 1) / BM);
-    hipLaunchKernelGGL((k_mm_mx_pipe<T, ADD, BN, BM, WN, WM, NB>), dim3((unsigned)tiles, splits), dim3(WN * WM * WAVE),
-                       0, stream, g, c);
+    hipLaunchKernelGGL((k_mm_mx_pipe<T, ADD, BN, BM, WN, WM, KW, NB>), dim3((unsigned)tiles, splits),
+                       dim3(WN * WM * KW * WAVE), 0, stream, g, c);
     return hipGetLastError();
 }
 
@@ -496,8 +552,203 @@ hipError_t launch_few(const Args& g, T* c, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// The same for up to R tokens that are encoded on the way.  Every block encodes
+// them anew, but x lies in L2 after the first one has read it, and a launch is
+// saved.  For each slab a wave's lanes hold 8 values of a token each (a group
+// is four lanes, as in the encoder); codes and scale bytes go through the wave's
+// part of LDS, laid out as the loads of the kernel above would.  (With each
+// lane encoding the groups that it multiplies, all 16 rows of a tile whether
+// there are tokens or not, one token x 4096 x 4096 took 5.9 us.)
+struct X {
+    const void* x;
+    int64_t ldx, k;
+};
+
+template <class T, class V, int NT, int R, int WS, int NB>
+__global__ void __launch_bounds__(WS * WAVE)
+k_mm_mx_fused(Args g, X x, T* __restrict__ c) {
+    typedef SlabLoader<NT * 16> LB;
+    constexpr int SLAB = LB::BYTES, TOKENS = R * (kSlab + 16);
+    constexpr int ALL = NB * SLAB + TOKENS, OWN = ALL > NT * 1024 ? ALL : NT * 1024;
+    static_assert(WS * OWN <= 160 * 1024 && OWN % 16 == 0 && R <= 16, "LDS");
+    __shared__ __align__(1024) uint8_t lds[WS * OWN];
+    const int l = lane_id(), quad = l >> 4, w = __builtin_amdgcn_readfirstlane(wave_id());
+    const int64_t n0 = (int64_t)blockIdx.x * (NT * 16);
+    const int pitch = (int)g.pitch, spitch = (int)g.spitch;
+    LB lb;
+    lb.init(g.b, n0, g.pitch, g.spitch);
+    uint8_t* own = lds + w * OWN;
+    uint8_t* tokens = own + NB * SLAB;
+
+    f32x4 acc[NT] = {};
+    const int slabs = (pitch + kSlab - 1) / kSlab;
+    const int mine = (slabs - w + WS - 1) / WS;  // slabs w, w + WS, ...
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+        if (b < mine) lb.load(w + b * WS, lds_addr(own) + b * SLAB, pitch, spitch);
+    Raw8<V> v[R];
+    auto load_values = [&](int slab) {
+        const int64_t at = (int64_t)slab * (2 * kSlab) + 8 * l;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t row = min((int64_t)r, g.a.rows - 1);
+            v[r].template load<false>(static_cast<const V*>(x.x) + row * x.ldx + at, x.k - at);
+        }
+    };
+    if (mine > 0) load_values(w);
+    for (int it = 0; it < mine; ++it) {
+        const int slab = w + it * WS, buf = it % NB;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint32_t byte = mx_byte(quad_max(v[r].amax_bits()));
+            const uint32_t word = v[r].codes(mx_scale(byte));
+            *reinterpret_cast<uint32_t*>(tokens + r * kSlab + (((l >> 2) ^ r) << 4) + (l & 3) * 4) =
+                byte == kMxNaN ? 0u : word;
+            if ((l & 3) == 0) tokens[R * kSlab + r * 16 + (l >> 2)] = (uint8_t)byte;
+        }
+        // this slab's weights were fetched before its values, which have been used
+        asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+        if (it + 1 < mine) load_values(slab + WS);
+        wave_lds_sync();
+        const uint8_t* at = own + buf * SLAB;
+        const bool there = slab * 16 + quad * 4 < spitch;
+        const int row = min(l & 15, R - 1);
+        const int sa = *reinterpret_cast<const int*>(tokens + R * kSlab + row * 16 + quad * 4);
+        int sb[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int word = *reinterpret_cast<const int*>(at + NT * 16 * kSlab + i * 256 + (l & 15) * 16 + quad * 4);
+            sb[i] = there ? word : 0;
+        }
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            const int piece = quad * 4 + kk;
+            const i32x4 fa = *reinterpret_cast<const i32x4*>(tokens + row * kSlab + ((piece ^ row) << 4));
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                i32x4 fb = *reinterpret_cast<const i32x4*>(at + (i * 16 + (l & 15)) * kSlab + ((piece ^ (l & 15)) << 4));
+                if (slab * kSlab + piece * 16 >= pitch) fb = i32x4{0, 0, 0, 0};
+                acc[i] = mfma16(kk, fb, fa, acc[i], sb[i], sa);
+            }
+        }
+        // this slab and its tokens have been read
+        asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+        if (it + NB < mine) lb.load(slab + NB * WS, lds_addr(own) + buf * SLAB, pitch, spitch);
+    }
+
+    f32x4* sums = reinterpret_cast<f32x4*>(own);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) sums[i * WAVE + l] = acc[i];
+    __syncthreads();
+    for (int f = w; f < NT; f += WS) {
+        f32x4 sum = {};
+#pragma unroll
+        for (int s = 0; s < WS; ++s) sum += *reinterpret_cast<const f32x4*>(lds + s * OWN + (f * WAVE + l) * 16);
+        const int64_t row = l & 15, col = n0 + f * 16 + 4 * quad;
+        if (row < g.a.rows) {
+            T* to = c + row * g.ldc + col;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (col + e < g.b.rows) put(to + e, sum[e]);
+        }
+    }
+}
+
+template <class T, class V, int NT, int R, int WS, int NB>
+hipError_t launch_fused(const Args& g, const X& x, T* c, hipStream_t stream) {
+    const dim3 grid((unsigned)((g.b.rows + NT * 16 - 1) / (NT * 16)));
+    hipLaunchKernelGGL((k_mm_mx_fused<T, V, NT, R, WS, NB>), grid, dim3(WS * WAVE), 0, stream, g, x, c);
+    return hipGetLastError();
+}
+
+// ------------------------------------------------------------------ splits
+// Sums of the splits, in order, to c (or to what c holds).  A thread takes four
+// neighbouring columns; the parts' rows are whole fours.
+template <class T, bool ADD>
+__global__ void __launch_bounds__(256)
+k_mm_mx_join(const float* __restrict__ parts, int splits, int64_t stride, int64_t m, int64_t n, T* __restrict__ c,
+             int64_t ldc) {
+    const int64_t fours = (n + 3) / 4, total = m * fours;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        f32x4 sum = ld_f4(parts + i * 4);
+#pragma unroll 4
+        for (int s = 1; s < splits; ++s) sum += ld_f4(parts + s * stride + i * 4);
+        const int64_t row = i / fours, col = i % fours * 4;
+        T* to = c + row * ldc + col;
+        if (n - col >= 4) {
+            float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+            typedef decltype(packed4(to, v)) V;
+            typedef V V_at_any __attribute__((aligned(sizeof(T))));
+            if constexpr (ADD) {
+                const f32x4 old = *reinterpret_cast<const V_at_any*>(to);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = old[e] + v[e];
+            }
+            *reinterpret_cast<V_at_any*>(to) = packed4(to, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (col + e < n) put_result<ADD>(to + e, sum[e]);
+        }
+    }
+}
+
 // ------------------------------------------------------------------ choice
-// Placeholder rule: few tokens by 16 x 16 to 32 x 64, else by pipelined tiles.
+// Which tile, and in how many parts k: the least of
+//   rounds of blocks over the 256 compute units * (once + per_k * k) + join,
+// `once` and `per_k` (for 1,024 values) the measured time of a further round,
+// with n = 4096 (us; the shape's 256 blocks twice and eight times).  Of all shapes
+// at k = 256, 1024, 4096 and 8192 with m = 16 to 32768 the one taken was within 8%
+// of the best.  Against the next best, whole calls, weights from HBM, n = k = 4096:
+//   m   16: 16 x 16 4.4 us (32 x 16 5.2)     m   64: 32 x 32 5.9 (32 x 64 7.4)
+//   m  128: 32 x 64 7.5 (32 x 32 8.9)        m  256: 64 x 64 11.0 (32 x 64 11.9)
+//   m  512: 64 x 128 14.1 (64 x 64 14.3)     m 1024: 128 x 128 19.3 (128 x 256 23.6)
+//   m 2048: 128 x 256 27.6 (256 x 256 32.0)  m 4096: 256 x 256 42.0 (128 x 256 53.6)
+struct Shape {
+    int bn, bm;  // channels, tokens
+    float once, per_k;
+};
+constexpr int kUnits = 256;  // compute units, each with one block at work
+constexpr Shape kShapes[] = {
+    {16, 16, 1.2f, 0.2f},   {32, 16, 1.3f, 0.33f},   {32, 32, 1.5f, 0.47f},  {32, 64, 2.2f, 0.65f},  {64, 64, 1.5f, 1.07f},
+    {64, 128, 3.6f, 1.93f}, {128, 128, 4.5f, 2.75f}, {128, 256, 4.0f, 5.1f}, {256, 256, 8.3f, 7.5f},
+};
+constexpr int kAll = sizeof(kShapes) / sizeof(kShapes[0]), kFirstPipe = 4;
+// Parts are joined by a launch of its own (2.5 us) that reads them at 4 TB/s.
+// Only the pipelined tiles are split, as the others share k among their waves;
+// a part has at least four stages.
+constexpr int kMaxSplits = 16, kLeastStages = 4;
+
+struct Choice {
+    int shape, splits, stages_per_split;
+};
+
+int64_t up4(int64_t v) { return (v + 3) / 4 * 4; }
+
+Choice choose(int64_t m, int64_t n, int64_t k) {
+    const int stages = (int)(((k + 31) / 32 * 16 + kStage - 1) / kStage);
+    Choice best{kAll - 1, 1, stages};
+    double least = 1e300;
+    for (int i = 0; i < kAll; ++i) {
+        const Shape& s = kShapes[i];
+        const int64_t blocks = ((n + s.bn - 1) / s.bn) * ((m + s.bm - 1) / s.bm);
+        if (blocks >= int64_t(1) << 23) continue;  // a grid has fewer than 2^32 threads; the last shape has
+        for (int splits = 1; splits <= (i >= kFirstPipe ? kMaxSplits : 1); splits *= 2) {
+            const int each = (stages + splits - 1) / splits;
+            if (splits > 1 && (each < kLeastStages || blocks * splits > 2 * kUnits)) break;
+            const int parts = (stages + each - 1) / each;
+            const double kk = splits == 1 ? (double)k : (double)each * 2 * kStage;
+            double us = (double)((blocks * parts + kUnits - 1) / kUnits) * (s.once + s.per_k * kk / 1024.0);
+            if (parts > 1) us += 2.5 + (double)m * n * 4 * 2 * parts / 4e6;
+            if (us < least) {
+                best = Choice{i, parts, each};
+                least = us;
+            }
+        }
+    }
+    return best;
+}
+
 template <class T, bool ADD>
 hipError_t launch_shape(int shape, const Args& g, int splits, T* c, hipStream_t stream) {
     switch (shape) {
@@ -505,55 +756,96 @@ hipError_t launch_shape(int shape, const Args& g, int splits, T* c, hipStream_t 
         case 1: return launch_few<T, ADD, 2, 1, 6, 2>(g, c, stream);
         case 2: return launch_few<T, ADD, 2, 2, 8, 1>(g, c, stream);
         case 3: return launch_few<T, ADD, 2, 4, 6, 1>(g, c, stream);
-        case 4: return launch_pipe<T, ADD, 64, 64, 1, 2, 4>(g, splits, c, stream);
-        case 5: return launch_pipe<T, ADD, 128, 128, 1, 4, 4>(g, splits, c, stream);
-        case 6: return launch_pipe<T, ADD, 128, 256, 1, 4, 2>(g, splits, c, stream);
-        case 7: return launch_pipe<T, ADD, 256, 256, 2, 4, 2>(g, splits, c, stream);
-        default: return launch_pipe<T, ADD, 256, 256, 2, 2, 2>(g, splits, c, stream);
+        case 4: return launch_pipe<T, ADD, 64, 64, 1, 1, 2, 4>(g, splits, c, stream);
+        case 5: return launch_pipe<T, ADD, 64, 128, 1, 2, 2, 4>(g, splits, c, stream);
+        case 6: return launch_pipe<T, ADD, 128, 128, 2, 2, 2, 4>(g, splits, c, stream);
+        case 7: return launch_pipe<T, ADD, 128, 256, 2, 4, 1, 2>(g, splits, c, stream);
+        default: return launch_pipe<T, ADD, 256, 256, 2, 4, 1, 2>(g, splits, c, stream);
     }
 }
 
-int shape_of(int64_t m, int64_t n) {
-    if (m <= 16) return 0;
-    if (m <= 32) return 2;
-    if (m <= 64) return 3;
-    return ((m + 255) / 256) * ((n + 255) / 256) >= 200 ? 7 : 5;
+template <class T, bool ADD>
+hipError_t launch(const Choice& w, Args g, T* c, int64_t ldc, float* parts, hipStream_t stream) {
+    if (w.splits == 1) {
+        g.ldc = ldc;
+        return launch_shape<T, ADD>(w.shape, g, 1, c, stream);
+    }
+    const int64_t m = g.a.rows, n = g.b.rows;
+    g.ldc = up4(n);
+    g.split_stride = m * g.ldc;
+    const hipError_t e = launch_shape<float, false>(w.shape, g, w.splits, parts, stream);
+    if (e != hipSuccess) return e;
+    const int64_t blocks = (m * (g.ldc / 4) + 255) / 256;
+    hipLaunchKernelGGL((k_mm_mx_join<T, ADD>), dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, stream,
+                       parts, w.splits, g.split_stride, m, n, c, ldc);
+    return hipGetLastError();
 }
+
+Args args_of(const void* a, const void* a_scales, const void* b, const void* b_scales, int64_t m, int64_t n, int64_t k,
+             int stages_per_split) {
+    return Args{{static_cast<const uint8_t*>(a), static_cast<const uint8_t*>(a_scales), m},
+                {static_cast<const uint8_t*>(b), static_cast<const uint8_t*>(b_scales), n},
+                (k + 31) / 32 * 16,
+                (k + 127) / 128 * 4,
+                0,
+                stages_per_split,
+                0};
+}
+
+// Up to kFew tokens are encoded by the blocks that multiply them (8 tokens x
+// 4096 x 4096 6.2 us, in two launches 6.9; 16 tokens 8.0 and 7.0).  Blocks of 32
+// channels where those of 16 are more than the compute units and each encodes
+// eight tokens (8 x 8192 x 8192 11.0 us against 15.5).
+constexpr int kFew = 8;
+
+template <class T, class V>
+hipError_t fused(Args g, const X& x, T* c, int64_t ldc, hipStream_t stream) {
+    g.ldc = ldc;
+    if (g.a.rows == 1) return launch_fused<T, V, 1, 1, 8, 2>(g, x, c, stream);
+    if (g.a.rows <= 4) return launch_fused<T, V, 1, 4, 8, 2>(g, x, c, stream);
+    return g.b.rows > 16 * kUnits ? launch_fused<T, V, 2, 8, 8, 1>(g, x, c, stream)
+                                  : launch_fused<T, V, 1, 8, 8, 2>(g, x, c, stream);
+}
+
+int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
 
 int64_t matmul_mxfp4_workspace(int64_t m, int64_t n, int64_t k) {
-    (void)m, (void)n, (void)k;
-    return 0;
+    const Choice w = choose(m, n, k);
+    return w.splits > 1 ? w.splits * m * up4(n) * 4 : 0;
 }
 
 hipError_t launch_matmul_mxfp4(const void* a, const void* a_scales, const void* b, const void* b_scales, int64_t m,
                                int64_t n, int64_t k, void* c, bool bf16, int64_t ldc, bool accumulate,
                                void* workspace, hipStream_t stream) {
-    (void)workspace;
-    const int64_t pitch = (k + 31) / 32 * 16;
-    const Args g{{static_cast<const uint8_t*>(a), static_cast<const uint8_t*>(a_scales), m},
-                 {static_cast<const uint8_t*>(b), static_cast<const uint8_t*>(b_scales), n},
-                 pitch, (k + 127) / 128 * 4, ldc, (int)((pitch + kStage - 1) / kStage), 0};
-    const int shape = shape_of(m, n);
-    if (bf16) return launch_shape<BF16, false>(shape, g, 1, static_cast<BF16*>(c), stream);
-    return accumulate ? launch_shape<float, true>(shape, g, 1, static_cast<float*>(c), stream)
-                      : launch_shape<float, false>(shape, g, 1, static_cast<float*>(c), stream);
+    const Choice w = choose(m, n, k);
+    const Args g = args_of(a, a_scales, b, b_scales, m, n, k, w.stages_per_split);
+    float* parts = static_cast<float*>(workspace);
+    if (bf16) return launch<BF16, false>(w, g, static_cast<BF16*>(c), ldc, parts, stream);
+    return accumulate ? launch<float, true>(w, g, static_cast<float*>(c), ldc, parts, stream)
+                      : launch<float, false>(w, g, static_cast<float*>(c), ldc, parts, stream);
 }
 
 // Codes of x, then their scales, each from a multiple of 256 bytes on; then the product's own.
-namespace {
-int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
-}  // namespace
-
 int64_t linear_mxfp4_workspace(int64_t m, int64_t n, int64_t k, bool x_bf16) {
     (void)x_bf16;
+    if (m <= kFew) return 0;
     return up256(m * ((k + 31) / 32 * 16)) + up256(m * ((k + 127) / 128 * 4)) + matmul_mxfp4_workspace(m, n, k);
 }
 
 hipError_t launch_linear_mxfp4(const void* x, bool x_bf16, int64_t ldx, const void* b, const void* b_scales, int64_t m,
                                int64_t n, int64_t k, void* c, bool bf16, int64_t ldc, void* workspace,
                                hipStream_t stream) {
+    if (m <= kFew) {
+        const Args g = args_of(nullptr, nullptr, b, b_scales, m, n, k, 0);
+        const X in{x, ldx, k};
+        if (bf16)
+            return x_bf16 ? fused<BF16, BF16>(g, in, static_cast<BF16*>(c), ldc, stream)
+                          : fused<BF16, float>(g, in, static_cast<BF16*>(c), ldc, stream);
+        return x_bf16 ? fused<float, BF16>(g, in, static_cast<float*>(c), ldc, stream)
+                      : fused<float, float>(g, in, static_cast<float*>(c), ldc, stream);
+    }
     uint8_t* codes = static_cast<uint8_t*>(workspace);
     uint8_t* scales = codes + up256(m * ((k + 31) / 32 * 16));
     uint8_t* rest = scales + up256(m * ((k + 127) / 128 * 4));

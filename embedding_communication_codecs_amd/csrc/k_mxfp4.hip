@@ -1,111 +1,352 @@
 // k_mxfp4.hip -- matrices to MXFP4 and back: codes and scale bytes of a matrix
-// and of its transpose.
+// and of its transpose (qc_mx.hpp has the format's rules).
+//
+// All of this is bound by HBM: 2 or 4 bytes a value on one side, 1/2 + 1/32 for
+// each of the encodings on the other.
 #include "qc_launch.hpp"
+#include "qc_lds.hpp"
 #include "qc_mx.hpp"
 
 namespace qc {
 namespace {
 
-// Thread (row, group): 32 values of a row, `step` elements apart.
-template <class T>
-__device__ __forceinline__ void encode_group(const T* __restrict__ x, int64_t step, int left,
-                                             uint8_t* __restrict__ codes, uint8_t* __restrict__ scale) {
-    float v[4][8];
-    uint32_t amax = 0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        v[i / 8][i % 8] = i < left ? to_f32(x[i * step]) : 0.0f;
-        amax = umax(amax, abs_bits(v[i / 8][i % 8]));
-    }
-    const uint32_t byte = mx_byte(amax);
-    u32x4 w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = byte == kMxNaN ? 0u : mx_codes8(v[i], mx_scale(byte));
-    *reinterpret_cast<u32x4*>(codes) = w;
-    *scale = (uint8_t)byte;
-}
-
-struct Outputs {
+struct Coded {  // an encoding's buffers
     uint8_t* codes;
     uint8_t* scales;
-    int64_t rows, dim;  // of the matrix that they hold
     int64_t pitch, spitch;
 };
 
-// ROWS: element (r, c) of the output is x[r * ldx + c], else x[c * ldx + r].
-template <class T, bool ROWS>
-__global__ void __launch_bounds__(256)
-k_enc_mxfp4(const T* __restrict__ x, int64_t ldx, Outputs o, int64_t total) {
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t groups = o.spitch;  // with those that only pad the scales
-        const int64_t r = ROWS ? i / groups : i % o.rows, q = ROWS ? i % groups : i / o.rows;
-        const int64_t c = q * kMxGroup;
-        if (c < o.dim)
-            encode_group(ROWS ? x + r * ldx + c : x + c * ldx + r, ROWS ? 1 : ldx,
-                         (int)(o.dim - c < kMxGroup ? o.dim - c : kMxGroup), o.codes + r * o.pitch + q * 16,
-                         o.scales + r * o.spitch + q);
-        else
-            o.scales[r * o.spitch + q] = 0;
+// ------------------------------------------------------------------- rows
+// 16 lanes are a unit of 128 columns, 8 values each: a group is four lanes, the
+// four scale bytes of a unit leave as one word.  A block of 256 threads holds
+// 16 units, 2^lx of them side by side and the others in rows below, so narrow
+// matrices fill blocks too; each thread takes two such tiles of rows at a time,
+// with the loads of both before the first use.
+constexpr int kUnroll = 2;
+struct Sizes {
+    int64_t rows, dim, row_tiles;
+    int lx;
+};
+struct Place {
+    int64_t row, col;
+    bool live;  // the unit has values (its lanes may still be past dim)
+};
+__device__ __forceinline__ Place place_of(int64_t rt, const Sizes& z) {
+    const int unit = threadIdx.x >> 4, l = threadIdx.x & 15;
+    const int64_t row = (rt << (4 - z.lx)) + (unit >> z.lx);
+    const int64_t u = ((int64_t)blockIdx.x << z.lx) + (unit & ((1 << z.lx) - 1));
+    return Place{row, u * 128 + 8 * l, row < z.rows && u * 128 < z.dim};
+}
+__device__ __forceinline__ int64_t left_of(const Place& p, const Sizes& z) { return p.live ? z.dim - p.col : 0; }
+
+// The bytes of a unit's four groups, gathered into lane 0 of its 16 (row_shl:n
+// reads lane i + n).
+__device__ __forceinline__ uint32_t gather_bytes(uint32_t b) {
+    const uint32_t b1 = (uint32_t)__builtin_amdgcn_mov_dpp((int)b, 0x104, 0xF, 0xF, true);
+    const uint32_t b2 = (uint32_t)__builtin_amdgcn_mov_dpp((int)b, 0x108, 0xF, 0xF, true);
+    const uint32_t b3 = (uint32_t)__builtin_amdgcn_mov_dpp((int)b, 0x10C, 0xF, 0xF, true);
+    return b | (b1 << 8) | (b2 << 16) | (b3 << 24);
+}
+
+// Eight values of a unit's lane; every lane of the wave calls this.
+template <class T>
+__device__ __forceinline__ void keep_row8(const Raw8<T>& v, int64_t row, int64_t col, bool live, int64_t dim,
+                                          const Coded& k) {
+    const uint32_t byte_here = mx_byte(quad_max(v.amax_bits()));
+    const bool group = live && (col & ~int64_t(31)) < dim;  // else: padding, byte 0
+    const uint32_t byte = group ? byte_here : 0u;
+    const uint32_t word = gather_bytes(byte);
+    if (live && (threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t*>(k.scales + row * k.spitch + col / 32) = word;
+    if (group) {
+        const uint32_t w = v.codes(mx_scale(byte));
+        *reinterpret_cast<uint32_t*>(k.codes + row * k.pitch + col / 2) = byte == kMxNaN ? 0u : w;
     }
 }
 
 template <class T>
 __global__ void __launch_bounds__(256)
-k_dec_mxfp4(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows, int64_t dim,
-            int64_t pitch, int64_t spitch, T* __restrict__ out, int64_t ldo, int64_t total) {
-    const int64_t words = pitch / 4;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / words, q = i % words, c = q * 8;
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + r * pitch + q * 4);
-        const uint32_t byte = scales[r * spitch + c / kMxGroup];
-        float v[8];
+k_enc_mxfp4(const T* __restrict__ x, int64_t ldx, Sizes z, Coded k) {
+    constexpr int U = kUnroll;
+    for (int64_t rt = (int64_t)blockIdx.y * U; rt < z.row_tiles; rt += (int64_t)gridDim.y * U) {
+        Raw8<T> v[U];
+        Place p[U];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t code = (w >> (4 * j)) & 15u, e = (code >> 1) & 3u;
-            // the values of the codes: 1 + half the low bit, times 2^(e - 1), and 0 and 0.5 below
-            const float mag = e ? __uint_as_float(((e + 126u) << 23) | ((code & 1u) << 22)) : (code & 1u) * 0.5f;
-            const float scale = byte == kMxNaN ? __uint_as_float(0x7FC00000u) : mx_scale(byte);
-            v[j] = (code & 8u ? -mag : mag) * scale;
+        for (int u = 0; u < U; ++u) {
+            p[u] = place_of(rt + u, z);
+            v[u].template load<true>(x + p[u].row * ldx + p[u].col, left_of(p[u], z));
         }
-        store8(out + r * ldo + c, dim - c, v);
+#pragma unroll
+        for (int u = 0; u < U; ++u) keep_row8(v[u], p[u].row, p[u].col, p[u].live, z.dim, k);
     }
 }
 
-unsigned grid_of(int64_t total) {
-    const int64_t g = (total + 255) / 256;
-    return (unsigned)(g < kMaxBlocks ? g : kMaxBlocks);
+// ---------------------------------------------------------------- columns
+// The transpose's encoding, with or without the matrix's own: tiles of 128 x
+// 128 through LDS.  A thread loads eight pieces of 8 values, 16 rows apart (and
+// encodes them by rows from its registers); then it takes 2 columns x 32 rows,
+// a whole group of each, and their codes leave through LDS again, 64 bytes of a
+// row of the transpose side by side.
+constexpr int kTile = 128;
+
+template <class T>
+struct Columns;  // two columns x 32 rows
+template <>
+struct Columns<BF16> {
+    uint32_t w[32];
+    __device__ __forceinline__ void read(const uint8_t* tile, int row0, int pair) {
+#pragma unroll
+        for (int r = 0; r < 32; ++r) w[r] = *reinterpret_cast<const uint32_t*>(tile + (row0 + r) * 256 + pair * 4);
+    }
+    __device__ __forceinline__ void amax_bits(uint32_t (&m)[2]) const {
+        uint32_t a = 0;
+#pragma unroll
+        for (int r = 0; r < 32; ++r) a = pair_max(a, w[r]);
+        m[0] = a << 16;
+        m[1] = a & 0xFFFF0000u;
+    }
+    __device__ __forceinline__ u32x4 codes(int c, float scale) const {
+        const uint32_t pick = c ? 0x07060302u : 0x05040100u;  // that column's halves of two words
+        u32x4 o;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            u32x4 v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_perm(w[8 * q + 2 * i + 1], w[8 * q + 2 * i], pick);
+            o[q] = mx_codes8(v, scale);
+        }
+        return o;
+    }
+};
+template <>
+struct Columns<float> {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    f32x2 w[32];
+    __device__ __forceinline__ void read(const uint8_t* tile, int row0, int pair) {
+#pragma unroll
+        for (int r = 0; r < 32; ++r) w[r] = *reinterpret_cast<const f32x2*>(tile + (row0 + r) * 512 + pair * 8);
+    }
+    __device__ __forceinline__ void amax_bits(uint32_t (&m)[2]) const {
+        m[0] = m[1] = 0;
+#pragma unroll
+        for (int r = 0; r < 32; ++r) {
+            m[0] = umax(m[0], abs_bits(w[r][0]));
+            m[1] = umax(m[1], abs_bits(w[r][1]));
+        }
+    }
+    __device__ __forceinline__ u32x4 codes(int c, float scale) const {
+        u32x4 o;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = w[8 * q + i][c];
+            o[q] = mx_codes8(v, scale);
+        }
+        return o;
+    }
+};
+
+__device__ __forceinline__ void put_raw8(uint8_t* p, const Raw8<BF16>& v) { *reinterpret_cast<u32x4*>(p) = v.w; }
+__device__ __forceinline__ void put_raw8(uint8_t* p, const Raw8<float>& v) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<f32x4*>(p + 16 * h) = f32x4{v.v[4 * h], v.v[4 * h + 1], v.v[4 * h + 2], v.v[4 * h + 3]};
 }
 
-Outputs outputs(void* codes, void* scales, int64_t rows, int64_t dim) {
-    return Outputs{static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales), rows, dim, (dim + 31) / 32 * 16,
-                   (dim + 127) / 128 * 4};
+template <class T, bool ROWS>
+__global__ void __launch_bounds__(256)
+k_enc_mxfp4_t(const T* __restrict__ x, int64_t ldx, int64_t rows, int64_t dim, Coded k, Coded kt) {
+    constexpr int RB = kTile * (int)sizeof(T);
+    __shared__ __align__(1024) uint8_t lds[kTile * RB];
+    const Tile2 tile = tile_of<4>(blockIdx.x, (uint32_t)((dim + kTile - 1) / kTile),
+                                  (uint32_t)((rows + kTile - 1) / kTile));
+    const int64_t r0 = (int64_t)tile.y * kTile, c0 = (int64_t)tile.x * kTile;
+    const int t = threadIdx.x;
+    {
+        const int64_t col = c0 + 8 * (t & 15);
+        Raw8<T> v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int64_t row = r0 + 16 * u + (t >> 4);
+            v[u].template load<true>(x + row * ldx + col, row < rows ? dim - col : 0);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int64_t row = r0 + 16 * u + (t >> 4);
+            if (ROWS) keep_row8(v[u], row, col, row < rows, dim, k);
+            put_raw8(lds + (16 * u + (t >> 4)) * RB + 8 * (t & 15) * (int)sizeof(T), v[u]);
+        }
+    }
+    __syncthreads();
+    const int pair = t & 63, part = t >> 6;  // columns 2 pair and 2 pair + 1, rows 32 part to 32 part + 31
+    Columns<T> v;
+    v.read(lds, 32 * part, pair);
+    uint32_t m[2];
+    v.amax_bits(m);
+    const bool group = r0 + 32 * part < rows;  // else: padding, byte 0
+    __syncthreads();
+    uint8_t* bytes = lds + kTile * 64;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const int col = 2 * pair + c;
+        const uint32_t byte = mx_byte(m[c]);
+        u32x4 w = v.codes(c, mx_scale(byte));
+        if (byte == kMxNaN) w = u32x4{0, 0, 0, 0};
+        *reinterpret_cast<u32x4*>(lds + col * 64 + ((part ^ ((col >> 2) & 3)) << 4)) = w;
+        bytes[col * 4 + part] = group ? (uint8_t)byte : 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int i = q * 256 + t, col = i >> 2, piece = i & 3;
+        if (c0 + col < dim && r0 + 32 * piece < rows)
+            *reinterpret_cast<u32x4*>(kt.codes + (c0 + col) * kt.pitch + r0 / 2 + piece * 16) =
+                *reinterpret_cast<const u32x4*>(lds + col * 64 + ((piece ^ ((col >> 2) & 3)) << 4));
+    }
+    if (t < kTile && c0 + t < dim)
+        *reinterpret_cast<uint32_t*>(kt.scales + (c0 + t) * kt.spitch + r0 / 32) =
+            *reinterpret_cast<const uint32_t*>(bytes + t * 4);
+}
+
+// ----------------------------------------------------------------- decode
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+template <int AT>
+__device__ __forceinline__ void mx_value_pair(uint32_t word, float scale, float& lo, float& hi) {
+    const f32x2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, scale, AT);
+    lo = v[0];
+    hi = v[1];
+}
+
+__device__ __forceinline__ float value_or_nan(float v, uint32_t byte) {
+    return byte == kMxNaN ? __uint_as_float(0x7FC00000u) : v;
+}
+
+// A lane's 8 values of a unit's 128: for bf16 neighbours, 16 bytes of output;
+// for fp32 four in each half of the unit, so that a store covers 256 bytes of a
+// row without gaps (8192 x 8192: eight neighbours in two stores 105 us).
+template <class T>
+struct Held8;
+template <>
+struct Held8<BF16> {
+    uint32_t word, byte;
+    __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, int64_t unit, int64_t dim) {
+        const int64_t col = unit + 8 * (threadIdx.x & 15);
+        const bool there = col < dim;
+        word = there ? ld_stream_u32(codes + col / 2) : 0u;
+        byte = there ? scales[col / 32] : 0u;
+    }
+    __device__ __forceinline__ void store(BF16* out, int64_t unit, int64_t dim) const {
+        const int64_t col = unit + 8 * (threadIdx.x & 15);
+        const float scale = mx_scale(byte);
+        float v[8];
+        mx_value_pair<0>(word, scale, v[0], v[1]);
+        mx_value_pair<1>(word, scale, v[2], v[3]);
+        mx_value_pair<2>(word, scale, v[4], v[5]);
+        mx_value_pair<3>(word, scale, v[6], v[7]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = value_or_nan(v[i], byte);
+        store8(out + col, dim - col, v);
+    }
+};
+template <>
+struct Held8<float> {
+    uint32_t word[2], byte[2];
+    __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, int64_t unit, int64_t dim) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t col = unit + 64 * h + 4 * (threadIdx.x & 15);
+            const bool there = col < dim;
+            word[h] = there ? ld_stream_u16(codes + col / 2) : 0u;
+            byte[h] = there ? scales[col / 32] : 0u;
+        }
+    }
+    __device__ __forceinline__ void store(float* out, int64_t unit, int64_t dim) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t col = unit + 64 * h + 4 * (threadIdx.x & 15), left = dim - col;
+            const float scale = mx_scale(byte[h]);
+            float v[4];
+            mx_value_pair<0>(word[h], scale, v[0], v[1]);
+            mx_value_pair<1>(word[h], scale, v[2], v[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = value_or_nan(v[i], byte[h]);
+            if (left >= 4) {
+                const u32x4 w = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                 __float_as_uint(v[3])};
+                __builtin_nontemporal_store(w, reinterpret_cast<u32x4_a2*>(out + col));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < left) out[col + i] = v[i];
+            }
+        }
+    }
+};
+
+template <class T>
+__global__ void __launch_bounds__(256)
+k_dec_mxfp4(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, Sizes z, int64_t pitch,
+            int64_t spitch, T* __restrict__ out, int64_t ldo) {
+    constexpr int U = kUnroll;
+    for (int64_t rt = (int64_t)blockIdx.y * U; rt < z.row_tiles; rt += (int64_t)gridDim.y * U) {
+        Held8<T> v[U];
+        Place p[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            p[u] = place_of(rt + u, z);
+            p[u].col &= ~int64_t(127);
+            v[u].load(codes + p[u].row * pitch, scales + p[u].row * spitch, p[u].col, p[u].live ? z.dim : 0);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u].store(out + p[u].row * ldo, p[u].col, p[u].live ? z.dim : 0);
+    }
+}
+
+struct Launch {
+    Sizes z;
+    dim3 grid;
+};
+
+Launch launch_of(int64_t rows, int64_t dim) {
+    Launch n;
+    const int64_t units = (dim + 127) / 128;
+    n.z.rows = rows;
+    n.z.dim = dim;
+    n.z.lx = units >= 16 ? 4 : log2_exact(units);
+    n.z.row_tiles = (rows + (16 >> n.z.lx) - 1) >> (4 - n.z.lx);
+    const int64_t y = (n.z.row_tiles + kUnroll - 1) / kUnroll;
+    n.grid = dim3((unsigned)((units + (1 << n.z.lx) - 1) >> n.z.lx), (unsigned)(y < 65535 ? y : 65535));
+    return n;
+}
+
+Coded coded(void* codes, void* scales, int64_t dim) {
+    return Coded{static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales), (dim + 31) / 32 * 16,
+                 (dim + 127) / 128 * 4};
 }
 
 template <class T>
 hipError_t encode(const T* x, int64_t rows, int64_t dim, int64_t ldx, void* codes, void* scales, void* codes_t,
                   void* scales_t, hipStream_t stream) {
-    if (codes) {
-        const Outputs o = outputs(codes, scales, rows, dim);
-        const int64_t total = rows * o.spitch;
-        hipLaunchKernelGGL((k_enc_mxfp4<T, true>), dim3(grid_of(total)), dim3(256), 0, stream, x, ldx, o, total);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    if (codes_t) {
-        const Outputs o = outputs(codes_t, scales_t, dim, rows);
-        const int64_t total = dim * o.spitch;
-        hipLaunchKernelGGL((k_enc_mxfp4<T, false>), dim3(grid_of(total)), dim3(256), 0, stream, x, ldx, o, total);
+    const Coded k = coded(codes, scales, dim), kt = coded(codes_t, scales_t, rows);
+    if (!codes_t) {
+        const Launch n = launch_of(rows, dim);
+        hipLaunchKernelGGL(k_enc_mxfp4<T>, n.grid, dim3(256), 0, stream, x, ldx, n.z, k);
         return hipGetLastError();
     }
-    return hipSuccess;
+    const dim3 grid((unsigned)(((dim + kTile - 1) / kTile) * ((rows + kTile - 1) / kTile)));
+    if (codes) hipLaunchKernelGGL((k_enc_mxfp4_t<T, true>), grid, dim3(256), 0, stream, x, ldx, rows, dim, k, kt);
+    else hipLaunchKernelGGL((k_enc_mxfp4_t<T, false>), grid, dim3(256), 0, stream, x, ldx, rows, dim, k, kt);
+    return hipGetLastError();
 }
 
 template <class T>
-hipError_t decode(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t dim, T* out, int64_t ldo,
+hipError_t decode(const void* codes, const void* scales, int64_t rows, int64_t dim, T* out, int64_t ldo,
                   hipStream_t stream) {
-    const int64_t pitch = (dim + 31) / 32 * 16, spitch = (dim + 127) / 128 * 4, total = rows * (pitch / 4);
-    hipLaunchKernelGGL(k_dec_mxfp4<T>, dim3(grid_of(total)), dim3(256), 0, stream, codes, scales, rows, dim, pitch,
-                       spitch, out, ldo, total);
+    const Launch n = launch_of(rows, dim);
+    hipLaunchKernelGGL(k_dec_mxfp4<T>, n.grid, dim3(256), 0, stream, static_cast<const uint8_t*>(codes),
+                       static_cast<const uint8_t*>(scales), n.z, (dim + 31) / 32 * 16, (dim + 127) / 128 * 4, out, ldo);
     return hipGetLastError();
 }
 
@@ -119,10 +360,8 @@ hipError_t launch_encode_mxfp4(const void* x, bool bf16, int64_t rows, int64_t d
 
 hipError_t launch_decode_mxfp4(const void* codes, const void* scales, int64_t rows, int64_t dim, void* out, bool bf16,
                                int64_t ldo, hipStream_t stream) {
-    const uint8_t* c = static_cast<const uint8_t*>(codes);
-    const uint8_t* s = static_cast<const uint8_t*>(scales);
-    return bf16 ? decode(c, s, rows, dim, static_cast<BF16*>(out), ldo, stream)
-                : decode(c, s, rows, dim, static_cast<float*>(out), ldo, stream);
+    return bf16 ? decode(codes, scales, rows, dim, static_cast<BF16*>(out), ldo, stream)
+                : decode(codes, scales, rows, dim, static_cast<float*>(out), ldo, stream);
 }
 
 }  // namespace qc

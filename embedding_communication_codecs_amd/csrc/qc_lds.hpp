@@ -28,6 +28,22 @@ __device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t rsrc, uint32_t 
                  : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(voff), "s"(rsrc), "s"(soff)
                  : "memory");
 }
+// The two for some waves of a block without a branch: `mask` is -1, or 0
+// for a wave that loads nothing.  Every lane of the wave is active.
+__device__ __forceinline__ void load_lds16_if(int mask, __amdgpu_buffer_rsrc_t rsrc, uint32_t lds, int voff) {
+    asm volatile("s_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %3\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds\n\t"
+                 "s_mov_b64 exec, -1"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(mask))
+                 : "memory");
+}
+__device__ __forceinline__ void load_lds4_if(int mask, __amdgpu_buffer_rsrc_t rsrc, uint32_t lds, int voff) {
+    asm volatile("s_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %3\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds\n\t"
+                 "s_mov_b64 exec, -1"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane((int)lds)), "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(mask))
+                 : "memory");
+}
 // This wave's loads into LDS have landed and its LDS accesses are done; then
 // every wave's are.
 __device__ __forceinline__ void lds_landed() {

@@ -17,21 +17,98 @@ __device__ __forceinline__ uint32_t mx_byte(uint32_t amax_bits) {
     const int e = (int)((amax_bits + 0x200000u) >> 23) - 2;
     return amax_bits >= kInfBits ? kMxNaN : (uint32_t)min(max(e, 1), 253);
 }
-
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-
-// Codes of eight values of a group: the conversion divides by the power of two
-// exactly, rounds to nearest even and keeps signs (of zeros too).
-__device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8], float scale) {
-    uint32_t w = 0;
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], scale, 0);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], scale, 1);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], scale, 2);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], scale, 3);
-    return w;
+// The scale as a number; of a group of NaNs 1, as its codes are replaced.
+__device__ __forceinline__ float mx_scale(uint32_t byte) {
+    return __uint_as_float((byte == kMxNaN ? 127u : byte) << 23);
 }
 
-// The scale as a number (byte 255: only asked for with its codes dropped).
-__device__ __forceinline__ float mx_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
+// Values as a group's codes are made from them: fp32, or bf16 two a word.  The
+// conversions divide by the power of two exactly, round to nearest even, take
+// what is above 6 (below 7) for 6 and keep signs, of zeros too.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+
+template <int AT>
+__device__ __forceinline__ uint32_t mx_code_pair(uint32_t word, float lo, float hi, float scale) {
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, lo, hi, scale, AT);
+}
+template <int AT>
+__device__ __forceinline__ uint32_t mx_code_pair(uint32_t word, uint32_t pair, float scale) {
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(word, __builtin_bit_cast(bf16x2, pair), scale, AT);
+}
+
+// Eight codes; v: values, or words of two.
+__device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8], float scale) {
+    uint32_t w = mx_code_pair<0>(0u, v[0], v[1], scale);
+    w = mx_code_pair<1>(w, v[2], v[3], scale);
+    w = mx_code_pair<2>(w, v[4], v[5], scale);
+    return mx_code_pair<3>(w, v[6], v[7], scale);
+}
+__device__ __forceinline__ uint32_t mx_codes8(u32x4 v, float scale) {
+    uint32_t w = mx_code_pair<0>(0u, v[0], scale);
+    w = mx_code_pair<1>(w, v[1], scale);
+    w = mx_code_pair<2>(w, v[2], scale);
+    return mx_code_pair<3>(w, v[3], scale);
+}
+
+// The larger magnitudes of two bf16 values a word, m those so far; and the
+// largest of both as fp32 bits.
+__device__ __forceinline__ uint32_t pair_max(uint32_t m, uint32_t w) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, m),
+                                                                  __builtin_bit_cast(u16x2, w & 0x7FFF7FFFu)));
+}
+__device__ __forceinline__ uint32_t amax_of_pair(uint32_t m) { return umax(m << 16, m & 0xFFFF0000u); }
+
+// Eight neighbouring values of a row as they lie in memory, zeros where there are none.
+template <class T>
+struct Raw8;
+template <>
+struct Raw8<BF16> {
+    u32x4 w;
+    // m: magnitudes so far, from 0; bits_of(m): the largest as fp32 bits
+    __device__ __forceinline__ uint32_t max_with(uint32_t m) const {
+        return pair_max(pair_max(pair_max(pair_max(m, w[0]), w[1]), w[2]), w[3]);
+    }
+    __device__ __forceinline__ static uint32_t bits_of(uint32_t m) { return amax_of_pair(m); }
+    __device__ __forceinline__ uint32_t amax_bits() const { return bits_of(max_with(0u)); }
+    __device__ __forceinline__ uint32_t codes(float scale) const { return mx_codes8(w, scale); }
+    template <bool STREAM>
+    __device__ __forceinline__ void load(const BF16* p, int64_t left) {
+        if (left >= 8) {
+            const u32x4_a2* q = reinterpret_cast<const u32x4_a2*>(p);
+            w = STREAM ? (u32x4)__builtin_nontemporal_load(q) : (u32x4)*q;
+        } else {
+            float v[8];
+            load_some(p, left, v);
+            w = u32x4{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
+        }
+    }
+};
+template <>
+struct Raw8<float> {
+    float v[8];
+    __device__ __forceinline__ uint32_t max_with(uint32_t m) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = umax(m, abs_bits(v[i]));
+        return m;
+    }
+    __device__ __forceinline__ static uint32_t bits_of(uint32_t m) { return m; }
+    __device__ __forceinline__ uint32_t amax_bits() const { return max_with(0u); }
+    __device__ __forceinline__ uint32_t codes(float scale) const { return mx_codes8(v, scale); }
+    template <bool STREAM>
+    __device__ __forceinline__ void load(const float* p, int64_t left) {
+        if (left >= 8) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const u32x4_a2* q = reinterpret_cast<const u32x4_a2*>(p + 4 * h);
+                const u32x4 w = STREAM ? (u32x4)__builtin_nontemporal_load(q) : (u32x4)*q;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[4 * h + i] = __uint_as_float(w[i]);
+            }
+        } else {
+            load_some(p, left, v);
+        }
+    }
+};
 
 }  // namespace qc
