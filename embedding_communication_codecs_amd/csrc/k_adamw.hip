@@ -15,89 +15,196 @@ namespace qc {
 namespace {
 
 // --------------------------------------------------------- tensor lists
-// A block of 256 threads works on one segment of 2^QC_INDEX_SHIFT = 4096
-// elements at a time, so that the index names the tensors of the whole
-// segment with two loads.  Where that is one tensor, the address is the
-// block's; elsewhere each lane searches the few tensors between, and eight
-// elements that lie in more than one are taken one by one.
-constexpr int kSeg = 1 << QC_INDEX_SHIFT;
-constexpr int kThreads = 256, kEach = 8, kPass = kThreads * kEach, kPasses = kSeg / kPass;
+// A block of 256 threads takes a run of passes of 2048 elements.  It keeps the
+// tensor that it is in, so a pass inside one tensor loads no table (with the
+// index looked up for each segment of 4096, three loads before the first value,
+// the norm of 268 M bf16 gradients took 274 us).  Where a pass reaches into
+// another tensor each lane searches the few between, and where its four
+// elements lie in more than one, each element's.
+//
+// 32 lanes hold 256 elements, a block of the 8-bit states; a lane four in each
+// half of them, so that an access of fp32 covers 512 bytes without gaps.
+constexpr int kThreads = 256, kPass = kThreads * 8, kFour = 4;
+constexpr int kMaxRuns = 2048;  // blocks of the norm: eight for each compute unit
+
+__device__ __forceinline__ int lane_first() { return (threadIdx.x >> 5) * 256 + (threadIdx.x & 31) * kFour; }
+constexpr int kHalf = 128;  // from a lane's first four to its second
+
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+
+// Four neighbouring values, `left` of which exist (the rest read as +0).
+__device__ __forceinline__ void load4(const float* p, int64_t left, float (&v)[4]) {
+    if (left >= 4) {
+        const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(p));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = i < left ? p[i] : 0.0f;
+    }
+}
+__device__ __forceinline__ void load4(const BF16* p, int64_t left, float (&v)[4]) {
+    if (left >= 4) {
+        const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const u32x2_a2*>(p));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            v[2 * i] = bf16_to_f32(w[i] & 0xFFFFu);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = i < left ? to_f32(p[i]) : 0.0f;
+    }
+}
+__device__ __forceinline__ void store4(float* p, int64_t left, const float (&v)[4]) {
+    if (left >= 4) {
+        const u32x4 w = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x4_a2*>(p));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < left) p[i] = v[i];
+    }
+}
+__device__ __forceinline__ void store4(BF16* p, int64_t left, const float (&v)[4]) {
+    if (left >= 4) {
+        const u32x2 w = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x2_a2*>(p));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < left) put(p + i, v[i]);
+    }
+}
 
 struct Tables {
     const int64_t* off;
     const int32_t* seg;
     int32_t T;
     int64_t n;
+    int64_t passes_per_run;
 };
 
-// The tensors of segment j, first and last; index values are clamped, so that
-// a corrupt index cannot send an access outside the tables.
-__device__ __forceinline__ void tensors_of(const Tables& l, int64_t j, int32_t& lo, int32_t& hi) {
-    const int32_t a = l.seg[j], b = l.seg[j + 1];
-    lo = __builtin_amdgcn_readfirstlane(min(max(a, 0), l.T - 1));
-    hi = __builtin_amdgcn_readfirstlane(min(max(b, lo), l.T - 1));
-}
+// Index values are clamped, so that a corrupt index cannot send an access
+// outside the tables.
+__device__ __forceinline__ int32_t clamped(int32_t t, int32_t lo, int32_t hi) { return min(max(t, lo), hi); }
 
-// Where eight elements from i of the concatenation lie.
-struct Span {
-    int32_t t;     // the tensor of the first
-    int64_t at;    // its index there
-    bool whole;    // all eight are in tensor t
-};
-
-__device__ __forceinline__ Span span_of(const Tables& l, int32_t lo, int32_t hi, int64_t i) {
-    int32_t a = lo, b = hi;
+// The tensor of element i, between tensors a and b.
+__device__ __forceinline__ int32_t tensor_at(const Tables& l, int32_t a, int32_t b, int64_t i) {
     while (a < b) {
         const int32_t mid = (a + b + 1) >> 1;
         if (l.off[mid] <= i) a = mid;
         else b = mid - 1;
     }
-    const int64_t o = l.off[a];
-    return Span{a, i - o, i >= o && i + kEach <= min(l.off[a + 1], l.n)};
+    return a;
 }
 
-// Calls f(j, tensor, index) for those of the eight elements from i that exist.
-template <class F>
-__device__ __forceinline__ void each_of(const Tables& l, int32_t t, int32_t hi, int64_t i, F f) {
-#pragma unroll 1
-    for (int j = 0; j < kEach; ++j) {
-        const int64_t g = i + j;
-        if (g >= l.n) break;
-        while (t < hi && g >= l.off[t + 1]) ++t;
-        const int64_t o = l.off[t];
-        if (g >= o && g < l.off[t + 1]) f(j, t, g - o);
+struct Cursor {  // the block's tensor, and where it begins and ends
+    int32_t t;
+    int64_t from, to;
+};
+__device__ __forceinline__ void move_to(Cursor& c, const Tables& l, int64_t i) {
+    const int32_t lo = clamped(l.seg[i >> QC_INDEX_SHIFT], 0, l.T - 1);
+    const int32_t hi = clamped(l.seg[(i >> QC_INDEX_SHIFT) + 1], lo, l.T - 1);
+    c.t = tensor_at(l, lo, hi, i);
+    c.from = l.off[c.t];
+    c.to = min(l.off[c.t + 1], l.n);
+}
+// The last tensor that a pass from element i may reach into.
+__device__ __forceinline__ int32_t last_of(const Cursor& c, const Tables& l, int64_t i) {
+    const int64_t last = min(i + kPass, l.n) - 1;
+    return clamped(l.seg[(last >> QC_INDEX_SHIFT) + 1], c.t, l.T - 1);
+}
+
+// The tensors (of a to b) of N elements, i(j) the index of element j.  Their
+// searches go on side by side, so that as many loads are on their way at a time:
+// what a pass over several tensors costs is one load after the other.
+template <int N, class I>
+__device__ __forceinline__ void tensors_of(const Tables& l, int32_t a, int32_t b, I i, int32_t (&t)[N]) {
+    int32_t last[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        t[j] = a;
+        last[j] = b;
+    }
+    // every one halves the same range, first to last, so they end together
+    for (int32_t span = b - a; span > 0; span >>= 1) {
+        int32_t mid[N];
+        int64_t v[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            mid[j] = (t[j] + last[j] + 1) >> 1;
+            v[j] = l.off[mid[j]];
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            if (v[j] <= i(j)) t[j] = mid[j];
+            else last[j] = mid[j] - 1;
+        }
     }
 }
 
+// Where a lane's two fours lie: each in one tensor, or over several.
+struct Fours {
+    int32_t t[2];
+    int64_t at[2];  // index of the first in tensor t
+    bool whole[2];
+};
+__device__ __forceinline__ Fours fours_of(const Tables& l, int32_t a, int32_t b, int64_t i, int half) {
+    Fours f;
+    tensors_of<2>(l, a, b, [&](int q) { return i + q * half; }, f.t);
+    int64_t from[2], to[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        from[q] = l.off[f.t[q]];
+        to[q] = min(l.off[f.t[q] + 1], l.n);
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        f.at[q] = i + q * half - from[q];
+        f.whole[q] = f.at[q] >= 0 && i + q * half + kFour <= to[q];
+    }
+    return f;
+}
+
+// Four elements that lie over several tensors.  Elements past the end, and those
+// of tables that contradict each other, are nowhere.
+struct Places {
+    int32_t t[kFour];
+    int64_t at[kFour];  // index in tensor t, or -1
+};
+__device__ __forceinline__ Places places_of(const Tables& l, int32_t a, int32_t b, int64_t i) {
+    Places s;
+    tensors_of<kFour>(l, a, b, [&](int j) { return i + j; }, s.t);
+#pragma unroll
+    for (int j = 0; j < kFour; ++j) {
+        const int64_t from = l.off[s.t[j]], to = l.off[s.t[j] + 1], g = i + j;
+        s.at[j] = g >= from && g < to && g < l.n ? g - from : -1;
+    }
+    return s;
+}
 template <class T>
-__device__ __forceinline__ void load_span(const Tables& l, T* const* xs, const Span& s, int32_t hi, int64_t i,
-                                          float (&v)[kEach]) {
-    if (s.whole) {
-        load8(const_cast<const T*>(xs[s.t]) + s.at, kEach, v);
-    } else {
+__device__ __forceinline__ void load_places(T* const* xs, const Places& s, float (&v)[kFour]) {
+    const T* p[kFour];
 #pragma unroll
-        for (int j = 0; j < kEach; ++j) v[j] = 0.0f;
-        each_of(l, s.t, hi, i, [&](int j, int32_t t, int64_t at) {
-            const float x = to_f32(const_cast<const T*>(xs[t])[at]);
+    for (int j = 0; j < kFour; ++j) p[j] = xs[s.t[j]];
+    T raw[kFour];
 #pragma unroll
-            for (int q = 0; q < kEach; ++q) v[q] = q == j ? x : v[q];
-        });
+    for (int j = 0; j < kFour; ++j) {
+        raw[j] = T{};
+        if (s.at[j] >= 0) raw[j] = p[j][s.at[j]];
     }
+#pragma unroll
+    for (int j = 0; j < kFour; ++j) v[j] = to_f32(raw[j]);
 }
-
 template <class T>
-__device__ __forceinline__ void store_span(const Tables& l, T* const* xs, const Span& s, int32_t hi, int64_t i,
-                                           const float (&v)[kEach]) {
-    if (s.whole) {
-        store8(xs[s.t] + s.at, kEach, v);
-    } else {
-        each_of(l, s.t, hi, i, [&](int j, int32_t t, int64_t at) {
-            float x = 0.0f;
+__device__ __forceinline__ void store_places(T* const* xs, const Places& s, const float (&v)[kFour]) {
+    T* p[kFour];
 #pragma unroll
-            for (int q = 0; q < kEach; ++q) x = q == j ? v[q] : x;
-            put(xs[t] + at, x);
-        });
-    }
+    for (int j = 0; j < kFour; ++j) p[j] = xs[s.t[j]];
+#pragma unroll
+    for (int j = 0; j < kFour; ++j)
+        if (s.at[j] >= 0) put(p[j] + s.at[j], v[j]);
 }
 
 // ------------------------------------------------------------ 8-bit states
@@ -147,60 +254,67 @@ __device__ __forceinline__ uint32_t state_code(float x, float inv, uint32_t u) {
     return c;
 }
 
-__device__ __forceinline__ u32x2 load_codes(const uint8_t* p, int64_t left) {
-    if (left >= 8) return ld_stream_u2(p);
-    u32x2 w = {0, 0};
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t left) {
+    if (left >= 4) return ld_stream_u32(p);
+    uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < left) w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+    for (int i = 0; i < 4; ++i)
+        if (i < left) w |= (uint32_t)p[i] << (8 * i);
     return w;
 }
-__device__ __forceinline__ void store_codes(uint8_t* p, int64_t left, u32x2 w) {
-    if (left >= 8) {
-        __builtin_nontemporal_store(w, reinterpret_cast<u32x2*>(p));
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t left, uint32_t w) {
+    if (left >= 4) {
+        st_u32(p, w);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < left) p[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+        for (int i = 0; i < 4; ++i)
+            if (i < left) p[i] = (uint8_t)(w >> (8 * i));
     }
 }
 
 template <int KIND>
-__device__ __forceinline__ void state_values(u32x2 codes, float scale, float (&v)[8]) {
+__device__ __forceinline__ void state_values(uint32_t codes, float scale, float (&v)[4]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = state_value<KIND>((codes[i >> 2] >> (8 * (i & 3))) & 255u) * scale;
+    for (int i = 0; i < 4; ++i) v[i] = state_value<KIND>((codes >> (8 * i)) & 255u) * scale;
 }
 
-// Codes of eight values; 32 neighbouring lanes hold a block, all of them call this.
+// Codes of a lane's two fours, `u` the threshold of the first; 32 neighbouring
+// lanes hold a block, all of them call this.
 template <int KIND>
-__device__ __forceinline__ u32x2 state_codes(const float (&x)[8], uint32_t u, uint32_t each, float& scale) {
+__device__ __forceinline__ float state_codes(const float (&x)[2][4], uint32_t u, uint32_t each, uint32_t (&w)[2]) {
     uint32_t amax = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = umax(amax, abs_bits(x[i]));
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) amax = umax(amax, abs_bits(x[q][i]));
     amax = group_max_u32<32>(amax);
     float inv;
-    scale = state_scale<KIND>(amax, inv);
-    u32x2 w = {0, 0};
+    const float scale = state_scale<KIND>(amax, inv);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        w[i >> 2] |= state_code<KIND>(x[i], inv, u + State<KIND>::SHIFT + (uint32_t)i * each) << (8 * (i & 3));
-    return w;
+    for (int q = 0; q < 2; ++q) {
+        w[q] = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[q] |= state_code<KIND>(x[q][i], inv, u + State<KIND>::SHIFT + (uint32_t)(q * kHalf + i) * each) << (8 * i);
+    }
+    return scale;
 }
 
-// Kernels over n elements of flat arrays, eight a thread: blocks of 256
-// elements are half waves, and every lane of a wave runs the same passes.
+// Flat arrays of n elements, laid out over lanes as above; every lane of a wave
+// runs the same passes.
 template <int KIND>
 __global__ void __launch_bounds__(kThreads)
 k_enc_state8(const float* __restrict__ x, int64_t n, uint8_t* __restrict__ codes, float* __restrict__ scale) {
     for (int64_t first = (int64_t)blockIdx.x * kPass; first < n; first += (int64_t)gridDim.x * kPass) {
-        const int64_t i = first + threadIdx.x * kEach;
-        float v[8], s;
-        load8(x + i, n - i, v);
-        const u32x2 w = state_codes<KIND>(v, 0x80000000u - State<KIND>::SHIFT, 0u, s);
-        if (i < n) {
-            store_codes(codes + i, n - i, w);
-            if ((threadIdx.x & 31) == 0) scale[i / QC_STATE_BLOCK] = s;
-        }
+        const int64_t i = first + lane_first();
+        float v[2][4];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) load4(x + i + q * kHalf, n - i - q * kHalf, v[q]);
+        uint32_t w[2];
+        const float s = state_codes<KIND>(v, 0x80000000u - State<KIND>::SHIFT, 0u, w);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) store_codes(codes + i + q * kHalf, n - i - q * kHalf, w[q]);
+        if (i < n && (threadIdx.x & 31) == 0) scale[i / QC_STATE_BLOCK] = s;
     }
 }
 
@@ -208,11 +322,16 @@ template <int KIND, class T>
 __global__ void __launch_bounds__(kThreads)
 k_dec_state8(const uint8_t* __restrict__ codes, const float* __restrict__ scale, int64_t n, T* __restrict__ out) {
     for (int64_t first = (int64_t)blockIdx.x * kPass; first < n; first += (int64_t)gridDim.x * kPass) {
-        const int64_t i = first + threadIdx.x * kEach;
-        if (i < n) {
-            float v[8];
-            state_values<KIND>(load_codes(codes + i, n - i), scale[i / QC_STATE_BLOCK], v);
-            store8(out + i, n - i, v);
+        const int64_t i = first + lane_first();
+        const float s = i < n ? scale[i / QC_STATE_BLOCK] : 0.0f;
+        uint32_t w[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) w[q] = load_codes(codes + i + q * kHalf, n - i - q * kHalf);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            float v[4];
+            state_values<KIND>(w[q], s, v);
+            store4(out + i + q * kHalf, n - i - q * kHalf, v);
         }
     }
 }
@@ -254,72 +373,130 @@ k_adamw(Tables l, P* const* __restrict__ params, G* const* __restrict__ grads, f
         AdamwStep step) {
     constexpr bool WIDE = std::is_same<S, Wide>::value;
     const Rates k = rates_of(step);
-    const int64_t segs = (l.n + kSeg - 1) / kSeg;
-    for (int64_t j = blockIdx.x; j < segs; j += gridDim.x) {
-        int32_t lo, hi;
-        tensors_of(l, j, lo, hi);
+    const int64_t first = (int64_t)blockIdx.x * l.passes_per_run * kPass;
+    const int64_t end = min(first + l.passes_per_run * kPass, l.n);
+    Cursor cur{0, 0, 0};
+    P* pp = nullptr;
+    G* gp = nullptr;
 #pragma unroll 1
-        for (int c = 0; c < kPasses; ++c) {
-            const int64_t i = j * kSeg + c * kPass + threadIdx.x * kEach, left = l.n - i;
-            float m[8] = {}, v[8] = {}, p[8] = {}, g[8] = {};
-            Span at{lo, 0, false};
-            if (left > 0) {
-                if constexpr (WIDE) {
-                    load8(st.m + i, left, m);
-                    load8(st.v + i, left, v);
-                } else {
-                    state_values<QC_STATE_M>(load_codes(st.mc + i, left), st.ms[i / QC_STATE_BLOCK], m);
-                    state_values<QC_STATE_R>(load_codes(st.rc + i, left), st.rs[i / QC_STATE_BLOCK], v);
-                }
-                if (MASTER) load8(master + i, left, p);
-                at = span_of(l, lo, hi, i);
-                load_span(l, grads, at, hi, i, g);
-                if (!MASTER) load_span(l, params, at, hi, i, p);
-            }
-            float r[8];
+    for (int64_t i0 = first; i0 < end; i0 += kPass) {
+        const int64_t i = i0 + lane_first();
+        // the states' places need no table: their loads go first
+        float m[2][4], v[2][4], p[2][4], g[2][4];
+        uint32_t mc[2], rc[2];
+        float ms = 0.0f, rs = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float x = g[e] * k.scale, old = WIDE ? v[e] : v[e] * v[e];
-                m[e] = __builtin_fmaf(m[e], step.beta1, x * step.rest1);
-                v[e] = __builtin_fmaf(old, step.beta2, x * x * step.rest2);
-                r[e] = sqrtf(v[e]);
-                const float den = __builtin_fmaf(r[e], k.root, step.eps);
-                p[e] = p[e] * k.decay - k.rate * m[e] / den;
-            }
+        for (int q = 0; q < 2; ++q) {
+            const int64_t at = i + q * kHalf, left = l.n - at;
             if constexpr (WIDE) {
-                if (left > 0) {
-                    store8(st.m + i, left, m);
-                    store8(st.v + i, left, v);
-                }
+                load4(st.m + at, left, m[q]);
+                load4(st.v + at, left, v[q]);
             } else {
-                // every lane of the wave takes part; those past the end hold zeros
-                const uint32_t u = (uint32_t)i * kDitherElem + k.t * kDitherStep;
-                float ms, rs;
-                const u32x2 mw = state_codes<QC_STATE_M>(m, u, kDitherElem, ms);
-                const u32x2 rw = state_codes<QC_STATE_R>(r, u, kDitherElem, rs);
-                if (left > 0) {
-                    store_codes(st.mc + i, left, mw);
-                    store_codes(st.rc + i, left, rw);
-                    if ((threadIdx.x & 31) == 0) {
-                        st.ms[i / QC_STATE_BLOCK] = ms;
-                        st.rs[i / QC_STATE_BLOCK] = rs;
-                    }
+                mc[q] = load_codes(st.mc + at, left);
+                rc[q] = load_codes(st.rc + at, left);
+            }
+            if (MASTER) load4(master + at, left, p[q]);
+        }
+        if constexpr (!WIDE) {
+            if (i < l.n) {
+                ms = st.ms[i / QC_STATE_BLOCK];
+                rs = st.rs[i / QC_STATE_BLOCK];
+            }
+        }
+        if (i0 >= cur.to) {
+            move_to(cur, l, i0);
+            pp = params[cur.t];
+            gp = grads[cur.t];
+        }
+        const bool one = i0 >= cur.from && i0 + kPass <= cur.to;  // the pass is in one tensor
+        Fours f;
+        P* pq[2];
+        int32_t last = 0;
+        if (one) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int64_t at = i + q * kHalf - cur.from;
+                load4(const_cast<const G*>(gp) + at, kFour, g[q]);
+                if (!MASTER) load4(const_cast<const P*>(pp) + at, kFour, p[q]);
+            }
+        } else {
+            last = last_of(cur, l, i0);
+            f = fours_of(l, cur.t, last, i, kHalf);
+            const G* gq[2] = {grads[f.t[0]], grads[f.t[1]]};
+            if (!MASTER) {
+                pq[0] = params[f.t[0]];
+                pq[1] = params[f.t[1]];
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                if (f.whole[q]) {
+                    load4(gq[q] + f.at[q], kFour, g[q]);
+                    if (!MASTER) load4(const_cast<const P*>(pq[q]) + f.at[q], kFour, p[q]);
                 }
             }
-            if (left > 0) {
-                if (MASTER) store8(master + i, left, p);
-                store_span(l, params, at, hi, i, p);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                if (!f.whole[q]) {
+                    const Places s = places_of(l, cur.t, last, i + q * kHalf);
+                    load_places(grads, s, g[q]);
+                    if (!MASTER) load_places(params, s, p[q]);
+                }
             }
+            if (MASTER) {
+                pq[0] = params[f.t[0]];
+                pq[1] = params[f.t[1]];
+            }
+        }
+        float r[2][4];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            if constexpr (!WIDE) {
+                state_values<QC_STATE_M>(mc[q], ms, m[q]);
+                state_values<QC_STATE_R>(rc[q], rs, v[q]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x = g[q][e] * k.scale, old = WIDE ? v[q][e] : v[q][e] * v[q][e];
+                m[q][e] = __builtin_fmaf(m[q][e], step.beta1, x * step.rest1);
+                v[q][e] = __builtin_fmaf(old, step.beta2, x * x * step.rest2);
+                r[q][e] = sqrtf(v[q][e]);
+                const float den = __builtin_fmaf(r[q][e], k.root, step.eps);
+                // the hardware's reciprocal is off by an ulp; den is 0 or a normal number
+                p[q][e] = p[q][e] * k.decay - k.rate * m[q][e] * __builtin_amdgcn_rcpf(den);
+            }
+        }
+        if constexpr (!WIDE) {
+            // every lane of the wave takes part; those past the end hold zeros
+            const uint32_t u = (uint32_t)i * kDitherElem + k.t * kDitherStep;
+            ms = state_codes<QC_STATE_M>(m, u, kDitherElem, mc);
+            rs = state_codes<QC_STATE_R>(r, u, kDitherElem, rc);
+            if (i < l.n && (threadIdx.x & 31) == 0) {
+                st.ms[i / QC_STATE_BLOCK] = ms;
+                st.rs[i / QC_STATE_BLOCK] = rs;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int64_t at = i + q * kHalf, left = l.n - at;
+            if constexpr (WIDE) {
+                store4(st.m + at, left, m[q]);
+                store4(st.v + at, left, v[q]);
+            } else {
+                store_codes(st.mc + at, left, mc[q]);
+                store_codes(st.rc + at, left, rc[q]);
+            }
+            if (MASTER) store4(master + at, left, p[q]);
+            if (one) store4(pp + (at - cur.from), kFour, p[q]);
+            else if (f.whole[q]) store4(pq[q] + f.at[q], kFour, p[q]);
+            else store_places(params, places_of(l, cur.t, last, at), p[q]);
         }
     }
 }
 
 // ------------------------------------------------------------------- norm
 // Squares are summed in 64 bits, so none overflows or vanishes.  Each block
-// takes every gridDim-th segment and leaves its sum; a second kernel adds those
-// up, always in the same order.
-constexpr int kNormBlocks = 2048;
-
+// leaves the sum of its run; a second kernel adds those up, always in the same
+// order.  Inside a tensor a thread has the loads of four passes on their way.
 __device__ __forceinline__ double block_sum(double v, double* lds) {
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
@@ -328,25 +505,57 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
     return (lds[0] + lds[1]) + (lds[2] + lds[3]);
 }
 
+__device__ __forceinline__ double add_squares(double sum, const float (&g)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum = __builtin_fma((double)g[e], (double)g[e], sum);
+    return sum;
+}
+
 template <class G>
 __global__ void __launch_bounds__(kThreads)
 k_norm_parts(Tables l, G* const* __restrict__ grads, double* __restrict__ parts) {
     __shared__ double lds[4];
-    const int64_t segs = (l.n + kSeg - 1) / kSeg;
+    constexpr int U = 8;  // fours: of four passes
+    const int64_t first = (int64_t)blockIdx.x * l.passes_per_run * kPass;
+    const int64_t end = min(first + l.passes_per_run * kPass, l.n);
+    Cursor cur{0, 0, 0};
+    const G* gp = nullptr;
     double sum = 0.0;
-    for (int64_t j = blockIdx.x; j < segs; j += gridDim.x) {
-        int32_t lo, hi;
-        tensors_of(l, j, lo, hi);
-#pragma unroll
-        for (int c = 0; c < kPasses; ++c) {
-            const int64_t i = j * kSeg + c * kPass + threadIdx.x * kEach;
-            if (i < l.n) {
-                float g[8];
-                load_span(l, grads, span_of(l, lo, hi, i), hi, i, g);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum = __builtin_fma((double)g[e], (double)g[e], sum);
-            }
+#pragma unroll 1
+    for (int64_t i0 = first; i0 < end;) {
+        if (i0 >= cur.to) {
+            move_to(cur, l, i0);
+            gp = grads[cur.t];
         }
+        if (i0 >= cur.from && i0 + U / 2 * kPass <= min(cur.to, end)) {
+            const G* p = gp + (i0 + threadIdx.x * kFour - cur.from);
+            float g[U][4];
+#pragma unroll
+            for (int u = 0; u < U; ++u) load4(p + u * (kPass / 2), kFour, g[u]);
+#pragma unroll
+            for (int u = 0; u < U; ++u) sum = add_squares(sum, g[u]);
+            i0 += U / 2 * kPass;
+            continue;
+        }
+        const int64_t i = i0 + threadIdx.x * kFour;
+        float g[2][4];
+        if (i0 >= cur.from && i0 + kPass <= cur.to) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) load4(gp + (i + q * (kPass / 2) - cur.from), kFour, g[q]);
+        } else {
+            const int32_t last = last_of(cur, l, i0);
+            const Fours f = fours_of(l, cur.t, last, i, kPass / 2);
+            const G* gq[2] = {grads[f.t[0]], grads[f.t[1]]};
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                if (f.whole[q]) load4(gq[q] + f.at[q], kFour, g[q]);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                if (!f.whole[q]) load_places(grads, places_of(l, cur.t, last, i + q * (kPass / 2)), g[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) sum = add_squares(sum, g[q]);
+        i0 += kPass;
     }
     sum = block_sum(sum, lds);
     if (threadIdx.x == 0) parts[blockIdx.x] = sum;
@@ -366,22 +575,33 @@ k_norm_join(const double* __restrict__ parts, int blocks, double max_norm, float
     }
 }
 
-int norm_blocks(int64_t n) {
-    const int64_t segs = (n + kSeg - 1) / kSeg;
-    return (int)(segs < kNormBlocks ? segs : kNormBlocks);
+// Runs of equal length, at most kMaxRuns.
+struct Runs {
+    int64_t passes;
+    int blocks;
+};
+Runs runs_of(int64_t n, int64_t most) {
+    const int64_t all = (n + kPass - 1) / kPass, each = (all + most - 1) / most;
+    return Runs{each, (int)((all + each - 1) / each)};
 }
+Runs norm_runs(int64_t n) { return runs_of(n, kMaxRuns); }
+// One pass a block, as far as a grid goes: all blocks at work then read and
+// write a few places that move on together (268 M elements, fp32 states, with 1,
+// 2, 4 and 8 passes 1530, 1551, 1605 and 1667 us; 8-bit 812, 855, 872, 907).
+Runs step_runs(int64_t n) { return runs_of(n, kMaxBlocks); }
 
 unsigned grid_of(int64_t n, int64_t each) {
     const int64_t g = (n + each - 1) / each;
     return (unsigned)(g < kMaxBlocks ? g : kMaxBlocks);
 }
 
-Tables tables_of(const ListSrc& l) { return Tables{l.offsets, l.seg_first, l.ntensors, l.n}; }
+Tables tables_of(const ListSrc& l, const Runs& r) { return Tables{l.offsets, l.seg_first, l.ntensors, l.n, r.passes}; }
 
 template <class P, class G, class S, bool MASTER>
 hipError_t launch_step(const AdamwList& l, const S& st, const AdamwStep& s, hipStream_t stream) {
-    hipLaunchKernelGGL((k_adamw<P, G, S, MASTER>), dim3(grid_of(l.grads.n, kSeg)), dim3(kThreads), 0, stream,
-                       tables_of(l.grads), reinterpret_cast<P* const*>(l.params),
+    const Runs r = step_runs(l.grads.n);
+    hipLaunchKernelGGL((k_adamw<P, G, S, MASTER>), dim3(r.blocks), dim3(kThreads), 0, stream, tables_of(l.grads, r),
+                       reinterpret_cast<P* const*>(l.params),
                        reinterpret_cast<G* const*>(const_cast<void* const*>(
                            reinterpret_cast<const void* const*>(l.grads.xs))),
                        l.master, st, s);
@@ -444,18 +664,19 @@ hipError_t launch_decode_state8(int32_t kind, const uint8_t* codes, const float*
                               : launch_dec_as<QC_STATE_R>(codes, scale, n, out, bf16, stream);
 }
 
-int64_t grad_norm_workspace(int64_t n) { return 8 * (int64_t)norm_blocks(n); }
+int64_t grad_norm_workspace(int64_t n) { return n > 0 ? 8 * (int64_t)norm_runs(n).blocks : 0; }
 
 hipError_t launch_grad_norm(const ListSrc& l, bool bf16, double max_norm, void* workspace, float* out,
                             hipStream_t stream) {
-    const int blocks = norm_blocks(l.n);
+    const Runs r = norm_runs(l.n);
+    const int blocks = r.blocks;
     double* parts = static_cast<double*>(workspace);
     auto xs = const_cast<void* const*>(reinterpret_cast<const void* const*>(l.xs));
     if (bf16)
-        hipLaunchKernelGGL(k_norm_parts<BF16>, dim3(blocks), dim3(kThreads), 0, stream, tables_of(l),
+        hipLaunchKernelGGL(k_norm_parts<BF16>, dim3(blocks), dim3(kThreads), 0, stream, tables_of(l, r),
                            reinterpret_cast<BF16* const*>(xs), parts);
     else
-        hipLaunchKernelGGL(k_norm_parts<float>, dim3(blocks), dim3(kThreads), 0, stream, tables_of(l),
+        hipLaunchKernelGGL(k_norm_parts<float>, dim3(blocks), dim3(kThreads), 0, stream, tables_of(l, r),
                            reinterpret_cast<float* const*>(xs), parts);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -5,8 +5,9 @@ states, and those states' codes.
 Tolerances, in half steps of fp32 (2^-24 of the value): with x = g * scale
 rounded once, m = fma(m, b1, x * (1 - b1)) is off by 4 of its two terms'
 magnitudes (x, 1 - b1, b1, the product and the sum round); v by 6 of its own;
-r = sqrt(v) by 4; the update rate * m / (r * root + eps) by 14 of the update
-that |m|'s two terms would give; p by one for each of its factor, product and
+r = sqrt(v) by 4; the update rate * m / (r * root + eps) by 16 of the update
+that |m|'s two terms would give (m 4; rate, root and their products 4; r 4; the
+sum with eps 1; a reciprocal within an ulp 2, the product with it 1); p by one for each of its factor, product and
 difference.  Where v falls below 2^-126 it may be off by 2^-149, and r with it
 by 2^-74."""
 import math
@@ -91,7 +92,7 @@ def tolerances(p, g, m, v, new_v, upd, t, scale, hyper=HYPER):
     den = np.sqrt(new_v / (1 - b2 ** t)) + hyper["eps"]
     upd_size = hyper["lr"] / (1 - b1 ** t) * m_size / np.maximum(den, 1e-300)
     upd_size = np.where(den > 0, upd_size, 0.0)
-    tol_p = 3 * U * np.abs(p) + 14 * U * upd_size + U * upd + 2.0 ** -149
+    tol_p = 3 * U * np.abs(p) + 16 * U * upd_size + U * upd + 2.0 ** -149
     return tol_m, tol_v, tol_p
 
 
