@@ -476,20 +476,29 @@ def _typed(t, kind, name):
         raise ValueError(f"{name} is a tensor of {t.dtype}, the call takes {' or '.join(map(str, want))}")
 
 
-def _mat(t, rows, cols, ld, kind, name, padding=0):
+def _placed(t, here, name):
+    """Refuses a tensor of another device than the current one, whose stream and
+    kernels the call would use."""
+    if here is not None and t.is_cuda and t.get_device() != here:
+        raise ValueError(f"{name} is on GPU {t.get_device()}, the current one is {here}")
+
+
+def _mat(t, rows, cols, ld, kind, name, padding=0, here=None):
     """Device address of a [rows][cols] matrix with row stride ld (elements),
     checking that the tensor has elements of that kind (QC_F32, QC_BF16,
     "codes") and holds all of it; it may be a view into a wider matrix.  The
-    padding after each row's cols may lie behind a view, in the same rows."""
+    padding after each row's cols may lie behind a view, in the same rows.
+    here: the device that it has to be on, None for any."""
     if t is None:
         return None
     if isinstance(t, int):
         return t
     s = t.shape
-    if (len(s) == 2 and t.is_cuda and t.stride() == (ld, 1) and s[0] >= rows and s[1] >= cols + padding
-            and t.dtype in _dtypes[kind]):
+    if (len(s) == 2 and (t.is_cuda if here is None else t.get_device() == here) and t.stride() == (ld, 1)
+            and s[0] >= rows and s[1] >= cols + padding and t.dtype in _dtypes[kind]):
         return t.data_ptr()  # the common case; what follows finds out what is wrong, or that nothing is
     _typed(t, kind, name)
+    _placed(t, here, name)
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if t.dim() > 2 and not t.is_contiguous():
@@ -511,13 +520,15 @@ def _mat(t, rows, cols, ld, kind, name, padding=0):
     return t.data_ptr()
 
 
-def _vec(t, nbytes, kind, name):
+def _vec(t, nbytes, kind, name, here=None):
     """Device address of nbytes contiguous bytes of elements of that kind."""
     if t is None or isinstance(t, int):
         return t
-    if t.is_cuda and t.dtype in _dtypes[kind] and t.is_contiguous() and t.nbytes >= nbytes:
+    if ((t.is_cuda if here is None else t.get_device() == here) and t.dtype in _dtypes[kind] and t.is_contiguous()
+            and t.nbytes >= nbytes):
         return t.data_ptr()
     _typed(t, kind, name)
+    _placed(t, here, name)
     return _ptr(t, nbytes, name)
 
 
@@ -612,28 +623,27 @@ def _now():
     return _device()
 
 
-def _here(*tensors):
-    """Refuses tensors of another device than the current one, whose stream and
-    kernels the call would use."""
-    now = _now()
-    for t in tensors:
-        if t is not None and t.__class__ is not int and t.get_device() != now and t.is_cuda:
-            raise ValueError(f"a tensor is on GPU {t.get_device()}, the current one is {now}")
-
-
-def _space(workspace):
+def _space(workspace, here):
     """Address and bytes of a workspace (a GPU tensor or None)."""
     if workspace is None:
         return None, 0
     if isinstance(workspace, int):
         raise ValueError("workspace must be a GPU tensor")
-    return _ptr(workspace, None, "workspace"), _bytes(workspace)
+    _placed(workspace, here, "workspace")
+    return _ptr(workspace, None, "workspace"), workspace.nbytes
 
 
-def _mx(codes, scales, rows, dim, name):
+def _table(t, nbytes, name, here):
+    """Address of a device table of pointers, offsets or indices."""
+    if t is not None and not isinstance(t, int):
+        _placed(t, here, name)
+    return _ptr(t, nbytes, name)
+
+
+def _mx(codes, scales, rows, dim, name, here):
     cb = rows * (-(-dim // QC_MX_GROUP) * (QC_MX_GROUP // 2))
     sb = rows * (-(-dim // (4 * QC_MX_GROUP)) * 4)
-    return _vec(codes, cb, "codes", name + "codes"), _vec(scales, sb, "codes", name + "scales")
+    return _vec(codes, cb, "codes", name + "codes", here), _vec(scales, sb, "codes", name + "scales", here)
 
 
 def mxfp4_bytes(rows: int, dim: int) -> tuple[int, int]:
@@ -647,16 +657,16 @@ qc_mxfp4_bytes = mxfp4_bytes
 
 
 def qc_encode_mxfp4(x, xtype, rows, dim, ldx, codes, scales, codes_t=None, scales_t=None, stream=None):
-    _here(x, codes, scales, codes_t, scales_t)
+    here = _now()
     _check(lib().qc_encode_mxfp4(
-        _mat(x, rows, dim, ldx, xtype, "x"), xtype, rows, dim, ldx, *_mx(codes, scales, rows, dim, ""),
-        *_mx(codes_t, scales_t, dim, rows, "transposed "), _stream(stream)))
+        _mat(x, rows, dim, ldx, xtype, "x", 0, here), xtype, rows, dim, ldx, *_mx(codes, scales, rows, dim, "", here),
+        *_mx(codes_t, scales_t, dim, rows, "transposed ", here), _stream(stream)))
 
 
 def qc_decode_mxfp4(codes, scales, rows, dim, out, otype, ldo, stream=None):
-    _here(codes, scales, out)
-    _check(lib().qc_decode_mxfp4(*_mx(codes, scales, rows, dim, ""), rows, dim,
-                                 _mat(out, rows, dim, ldo, otype, "out"), otype, ldo, _stream(stream)))
+    here = _now()
+    _check(lib().qc_decode_mxfp4(*_mx(codes, scales, rows, dim, "", here), rows, dim,
+                                 _mat(out, rows, dim, ldo, otype, "out", 0, here), otype, ldo, _stream(stream)))
 
 
 def qc_matmul_mxfp4_workspace(m, n, k) -> int:
@@ -670,10 +680,11 @@ def qc_matmul_mxfp4_workspace(m, n, k) -> int:
 def qc_matmul_mxfp4(a, a_scales, b, b_scales, m, n, k, c, ctype, ldc, accumulate=False, workspace=None, stream=None):
     """workspace: a GPU tensor of at least qc_matmul_mxfp4_workspace() bytes, or
     None where that is 0."""
-    _here(a, a_scales, b, b_scales, c, workspace)
+    here = _now()
     _check(lib().qc_matmul_mxfp4(
-        *_mx(a, a_scales, m, k, "a "), *_mx(b, b_scales, n, k, "b "), m, n, k, _mat(c, m, n, ldc, ctype, "c"), ctype,
-        ldc, 1 if accumulate else 0, *_space(workspace), _stream(stream)))
+        *_mx(a, a_scales, m, k, "a ", here), *_mx(b, b_scales, n, k, "b ", here), m, n, k,
+        _mat(c, m, n, ldc, ctype, "c", 0, here), ctype, ldc, 1 if accumulate else 0, *_space(workspace, here),
+        _stream(stream)))
 
 
 def qc_linear_mxfp4_workspace(m, n, k, xtype) -> int:
@@ -687,10 +698,10 @@ def qc_linear_mxfp4_workspace(m, n, k, xtype) -> int:
 def qc_linear_mxfp4(x, xtype, ldx, b, b_scales, m, n, k, c, ctype, ldc, workspace=None, stream=None):
     """workspace: a GPU tensor of at least qc_linear_mxfp4_workspace() bytes, or
     None where that is 0."""
-    _here(x, b, b_scales, c, workspace)
+    here = _now()
     _check(lib().qc_linear_mxfp4(
-        _mat(x, m, k, ldx, xtype, "x"), xtype, ldx, *_mx(b, b_scales, n, k, "b "), m, n, k,
-        _mat(c, m, n, ldc, ctype, "c"), ctype, ldc, *_space(workspace), _stream(stream)))
+        _mat(x, m, k, ldx, xtype, "x", 0, here), xtype, ldx, *_mx(b, b_scales, n, k, "b ", here), m, n, k,
+        _mat(c, m, n, ldc, ctype, "c", 0, here), ctype, ldc, *_space(workspace, here), _stream(stream)))
 
 
 # --------------------------------------------------------------- optimizer
@@ -708,20 +719,23 @@ def qc_grad_norm_multi(grads, gtype, offsets, seg_first, ntensors, n, max_norm, 
     """grads/offsets/seg_first: device tables (see TensorTable) or raw
     addresses; workspace: a GPU tensor of at least qc_grad_norm_workspace()
     bytes."""
-    _here(grads, offsets, seg_first, workspace, out)
-    g = _list_args(grads, offsets, seg_first, ntensors, n)
-    _check(lib().qc_grad_norm_multi(g[0], gtype, *g[1:], max_norm, *_space(workspace), _vec(out, 8, QC_F32, "out"),
-                                    _stream(stream)))
+    here = _now()
+    _check(lib().qc_grad_norm_multi(
+        _table(grads, 8 * max(ntensors, 0), "grads", here), gtype,
+        _table(offsets, 8 * (max(ntensors, 0) + 1), "offsets", here), _table(seg_first, 4 * _nseg(n), "seg_first", here),
+        ntensors, n, max_norm, *_space(workspace, here), _vec(out, 8, QC_F32, "out", here), _stream(stream)))
 
 
 def _adamw(fn, params, ptype, grads, gtype, offsets, seg_first, ntensors, n, master, states, hyper, grad_scale,
            schedule, stream):
-    _here(params, grads, offsets, seg_first, master, grad_scale, schedule, *(t for t, _, _, _ in states))
-    g = _list_args(grads, offsets, seg_first, ntensors, n)
+    here = _now()
+    pointers = 8 * max(ntensors, 0)
     _check(fn(
-        _ptr(params, 8 * max(ntensors, 0), "params"), ptype, g[0], gtype, *g[1:],
-        _vec(master, 4 * n, QC_F32, "master"), *(_vec(*s) for s in states), *hyper,
-        _vec(grad_scale, 4, QC_F32, "grad_scale"), _vec(schedule, 8, QC_F32, "schedule"), _stream(stream)))
+        _table(params, pointers, "params", here), ptype, _table(grads, pointers, "grads", here), gtype,
+        _table(offsets, pointers + 8, "offsets", here), _table(seg_first, 4 * _nseg(n), "seg_first", here), ntensors, n,
+        _vec(master, 4 * n, QC_F32, "master", here), *(_vec(*s, here) for s in states), *hyper,
+        _vec(grad_scale, 4, QC_F32, "grad_scale", here), _vec(schedule, 8, QC_F32, "schedule", here),
+        _stream(stream)))
 
 
 def qc_adamw_multi(params, ptype, grads, gtype, offsets, seg_first, ntensors, n, master, m, v, lr, beta1, beta2, eps,
@@ -743,22 +757,19 @@ def qc_adamw8_multi(params, ptype, grads, gtype, offsets, seg_first, ntensors, n
            (lr, beta1, beta2, eps, weight_decay, step), grad_scale, schedule, stream)
 
 
-def _typed_flat(t, kind, n, name):
-    return _vec(t, n * (2 if kind == QC_BF16 else 4), kind, name)
-
-
 def qc_encode_state8(kind, x, n, codes, scale, stream=None):
-    _here(x, codes, scale)
+    here = _now()
     _check(lib().qc_encode_state8(
-        kind, _vec(x, 4 * n, QC_F32, "x"), n, _vec(codes, n, "codes", "codes"),
-        _vec(scale, 4 * nbuckets(n, QC_STATE_BLOCK), QC_F32, "scale"), _stream(stream)))
+        kind, _vec(x, 4 * n, QC_F32, "x", here), n, _vec(codes, n, "codes", "codes", here),
+        _vec(scale, 4 * nbuckets(n, QC_STATE_BLOCK), QC_F32, "scale", here), _stream(stream)))
 
 
 def qc_decode_state8(kind, codes, scale, n, out, otype, stream=None):
-    _here(codes, scale, out)
+    here = _now()
     _check(lib().qc_decode_state8(
-        kind, _vec(codes, n, "codes", "codes"), _vec(scale, 4 * nbuckets(n, QC_STATE_BLOCK), QC_F32, "scale"), n,
-        _typed_flat(out, otype, n, "out"), otype, _stream(stream)))
+        kind, _vec(codes, n, "codes", "codes", here),
+        _vec(scale, 4 * nbuckets(n, QC_STATE_BLOCK), QC_F32, "scale", here), n,
+        _vec(out, n * (2 if otype == QC_BF16 else 4), otype, "out", here), otype, _stream(stream)))
 
 
 def qc_payload_bytes(fmt, n, group, bits) -> int:

@@ -695,23 +695,25 @@ k_mm_mx_join(const float* __restrict__ parts, int splits, int64_t stride, int64_
 
 // ------------------------------------------------------------------ choice
 // Which tile, and in how many parts k: the least of
-//   rounds of blocks over the 256 compute units * (once + per_k * k) + join,
-// `once` and `per_k` (for 1,024 values) the measured time of a further round,
-// with n = 4096 (us; the shape's 256 blocks twice and eight times).  Of all shapes
-// at k = 256, 1024, 4096 and 8192 with m = 16 to 32768 the one taken was within 8%
-// of the best.  Against the next best, whole calls, weights from HBM, n = k = 4096:
+//   first + first_k * k + (rounds - 1) * (more + more_k * k) + join,
+// rounds of blocks over the 256 compute units.  `first` and `first_k` (for 1,024
+// values) fit the whole time of a call of 256 blocks, weights from HBM, `more`
+// and `more_k` that of a further round, of all shapes at k = 256, 1024, 4096 and
+// 8192 with n = 4096 and m = 16 to 32768 (us).  Against the next best, n = k =
+// 4096:
 //   m   16: 16 x 16 4.4 us (32 x 16 5.2)     m   64: 32 x 32 5.9 (32 x 64 7.4)
 //   m  128: 32 x 64 7.5 (32 x 32 8.9)        m  256: 64 x 64 11.0 (32 x 64 11.9)
 //   m  512: 64 x 128 14.1 (64 x 64 14.3)     m 1024: 128 x 128 19.3 (128 x 256 23.6)
 //   m 2048: 128 x 256 27.6 (256 x 256 32.0)  m 4096: 256 x 256 42.0 (128 x 256 53.6)
 struct Shape {
     int bn, bm;  // channels, tokens
-    float once, per_k;
+    float first, first_k, more, more_k;
 };
 constexpr int kUnits = 256;  // compute units, each with one block at work
 constexpr Shape kShapes[] = {
-    {16, 16, 1.2f, 0.2f},   {32, 16, 1.3f, 0.33f},   {32, 32, 1.5f, 0.47f},  {32, 64, 2.2f, 0.65f},  {64, 64, 1.5f, 1.07f},
-    {64, 128, 3.6f, 1.93f}, {128, 128, 4.5f, 2.75f}, {128, 256, 4.0f, 5.1f}, {256, 256, 8.3f, 7.5f},
+    {16, 16, 2.4f, 0.52f, 1.2f, 0.2f},   {32, 16, 2.6f, 0.63f, 1.3f, 0.33f},   {32, 32, 2.9f, 0.8f, 1.5f, 0.47f},
+    {32, 64, 3.6f, 0.97f, 2.2f, 0.65f},  {64, 64, 5.0f, 1.43f, 1.5f, 1.07f},   {64, 128, 5.6f, 2.05f, 3.6f, 1.93f},
+    {128, 128, 7.2f, 2.9f, 4.5f, 2.75f}, {128, 256, 7.4f, 5.0f, 4.0f, 5.1f},   {256, 256, 10.8f, 7.6f, 8.3f, 7.5f},
 };
 constexpr int kAll = sizeof(kShapes) / sizeof(kShapes[0]), kFirstPipe = 4;
 // Parts are joined by a launch of its own (2.5 us) that reads them at 4 TB/s.
@@ -738,7 +740,8 @@ Choice choose(int64_t m, int64_t n, int64_t k) {
             if (splits > 1 && (each < kLeastStages || blocks * splits > 2 * kUnits)) break;
             const int parts = (stages + each - 1) / each;
             const double kk = splits == 1 ? (double)k : (double)each * 2 * kStage;
-            double us = (double)((blocks * parts + kUnits - 1) / kUnits) * (s.once + s.per_k * kk / 1024.0);
+            const double more = (double)((blocks * parts - 1) / kUnits);
+            double us = s.first + s.first_k * kk / 1024.0 + more * (s.more + s.more_k * kk / 1024.0);
             if (parts > 1) us += 2.5 + (double)m * n * 4 * 2 * parts / 4e6;
             if (us < least) {
                 best = Choice{i, parts, each};

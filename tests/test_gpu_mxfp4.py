@@ -194,8 +194,11 @@ def test_scales_at_their_ends(qc):
         check_product(c.get(), ref.held(ac, as_, k), ref.held(bc, bs, k))
 
 
+WIDE = [(1, 5003, 700), (3, 4100, 1030), (5, 4200, 2043), (8, 8190, 515), (9, 4100, 600)]
+
+
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
-@pytest.mark.parametrize("m,n,k", SIZES)
+@pytest.mark.parametrize("m,n,k", SIZES + WIDE + [(4, 48, 4700), (8, 64, 9000), (1, 20, 20000)])
 def test_linear(qc, m, n, k, dtype):
     bc, bs = ref.random_mx(n, k, 9)
     x = matrix(m, k, 10, dtype)
