@@ -364,8 +364,17 @@ k_mm_mx_pipe(Args g, T* __restrict__ c) {
     uint8_t* own = lds + w * (32 * RB);
     c += (int64_t)blockIdx.y * g.split_stride;
     const bool inside = n0 + BN <= g.b.rows && m0 + BM <= g.a.rows;
+    constexpr int STORES = RB / 32;
 #pragma unroll
     for (int j = 0; j < OM; ++j) {
+        const int64_t row0 = m0 + (wm * FM + wk * OM + j) * 32, col0 = n0 + wn * COLS;
+        // where store q of this lane goes, and how many columns there are
+        auto place = [&](int q, T*& to) {
+            const int r = (q * WAVE + l) / PR, p = (q * WAVE + l) % PR;
+            const int64_t row = row0 + r, col = col0 + p * E;
+            to = c + row * g.ldc + col;
+            return inside || row < g.a.rows ? g.b.rows - col : (int64_t)0;
+        };
 #pragma unroll
         for (int i = 0; i < FN; ++i) {
 #pragma unroll
@@ -380,25 +389,44 @@ k_mm_mx_pipe(Args g, T* __restrict__ c) {
             }
         }
         wave_lds_sync();
-        const int64_t row0 = m0 + (wm * FM + wk * OM + j) * 32, col0 = n0 + wn * COLS;
-#pragma unroll
-        for (int q = 0; q < RB / 32; ++q) {
+        auto piece = [&](int q) {
             const int r = (q * WAVE + l) / PR, p = (q * WAVE + l) % PR;
-            const uint8_t* from = own + r * RB + ((p ^ (r & (PR - 1))) << 4);
-            const int64_t row = row0 + r, col = col0 + p * E, left = inside || row < g.a.rows ? g.b.rows - col : 0;
-            T* to = c + row * g.ldc + col;
-            if (inside || left >= E) {
-                u32x4 v = *reinterpret_cast<const u32x4*>(from);
-                if constexpr (ADD) {
-                    const u32x4 old = *reinterpret_cast<const u32x4_a2*>(to);
+            return own + r * RB + ((p ^ (r & (PR - 1))) << 4);
+        };
+        if (ADD && inside) {
+            // what is there: eight loads before the first store, which the compiler
+            // could move no load ahead of (4096 x 4096 x 4096: 65 us with each load
+            // before its store)
+            constexpr int AT = STORES < 8 ? STORES : 8;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        v[e] = __float_as_uint(__uint_as_float(old[e]) + __uint_as_float(v[e]));
+            for (int q = 0; q < STORES; q += AT) {
+                u32x4 old[AT];
+                T* to[AT];
+#pragma unroll
+                for (int e = 0; e < AT; ++e) {
+                    place(q + e, to[e]);
+                    old[e] = *reinterpret_cast<const u32x4_a2*>(to[e]);
                 }
-                *reinterpret_cast<u32x4_a2*>(to) = v;
-            } else {
-                for (int e = 0; e < E; ++e)
-                    if (e < left) put_result<ADD>(to + e, to_f32(reinterpret_cast<const T*>(from)[e]));
+#pragma unroll
+                for (int e = 0; e < AT; ++e) {
+                    u32x4 v = *reinterpret_cast<const u32x4*>(piece(q + e));
+#pragma unroll
+                    for (int f = 0; f < 4; ++f)
+                        v[f] = __float_as_uint(__uint_as_float(old[e][f]) + __uint_as_float(v[f]));
+                    *reinterpret_cast<u32x4_a2*>(to[e]) = v;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < STORES; ++q) {
+                T* to;
+                const int64_t left = place(q, to);
+                if (!ADD && (inside || left >= E)) {
+                    *reinterpret_cast<u32x4_a2*>(to) = *reinterpret_cast<const u32x4*>(piece(q));
+                } else {
+                    for (int e = 0; e < E; ++e)
+                        if (e < left) put_result<ADD>(to + e, to_f32(reinterpret_cast<const T*>(piece(q))[e]));
+                }
             }
         }
         wave_lds_sync();
@@ -538,9 +566,13 @@ k_mm_mx_few(Args g, T* __restrict__ c) {
         const int64_t col = n0 + (f / MT) * 16 + 4 * quad;
         if (row < g.a.rows) {
             T* to = c + row * g.ldc + col;
+            if constexpr (ADD) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[e] += to[min((int64_t)e, g.b.rows - 1 - col)];
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (col + e < g.b.rows) put_result<ADD>(to + e, sum[e]);
+                if (col + e < g.b.rows) put_result<false>(to + e, sum[e]);
         }
     }
 }
@@ -592,14 +624,16 @@ k_mm_mx_fused(Args g, X x, T* __restrict__ c) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int64_t row = min((int64_t)r, g.a.rows - 1);
-            v[r].template load<false>(static_cast<const V*>(x.x) + row * x.ldx + at, x.k - at);
+            v[r].template load<false>(static_cast<const V*>(x.x) + row * x.ldx + at, x.k - at, at > 0);
         }
     };
     if (mine > 0) load_values(w);
     for (int it = 0; it < mine; ++it) {
         const int slab = w + it * WS, buf = it % NB;
+        const int64_t first = (int64_t)slab * (2 * kSlab) + 8 * l;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
+            v[r].settle(x.k - first, first > 0);
             const uint32_t byte = mx_byte(quad_max(v[r].amax_bits()));
             const uint32_t word = v[r].codes(mx_scale(byte));
             *reinterpret_cast<uint32_t*>(tokens + r * kSlab + (((l >> 2) ^ r) << 4) + (l & 3) * 4) =

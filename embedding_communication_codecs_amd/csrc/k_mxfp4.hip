@@ -73,8 +73,10 @@ k_enc_mxfp4(const T* __restrict__ x, int64_t ldx, Sizes z, Coded k) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             p[u] = place_of(rt + u, z);
-            v[u].template load<true>(x + p[u].row * ldx + p[u].col, left_of(p[u], z));
+            v[u].template load<true>(x + p[u].row * ldx + p[u].col, left_of(p[u], z), p[u].col > 0);
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u].settle(left_of(p[u], z), p[u].col > 0);
 #pragma unroll
         for (int u = 0; u < U; ++u) keep_row8(v[u], p[u].row, p[u].col, p[u].live, z.dim, k);
     }
@@ -168,11 +170,12 @@ k_enc_mxfp4_t(const T* __restrict__ x, int64_t ldx, int64_t rows, int64_t dim, C
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             const int64_t row = r0 + 16 * u + (t >> 4);
-            v[u].template load<true>(x + row * ldx + col, row < rows ? dim - col : 0);
+            v[u].template load<true>(x + row * ldx + col, row < rows ? dim - col : 0, col > 0);
         }
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             const int64_t row = r0 + 16 * u + (t >> 4);
+            v[u].settle(row < rows ? dim - col : 0, col > 0);
             if (ROWS) keep_row8(v[u], row, col, row < rows, dim, k);
             put_raw8(lds + (16 * u + (t >> 4)) * RB + 8 * (t & 15) * (int)sizeof(T), v[u]);
         }
