@@ -21,6 +21,8 @@ namespace {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
+constexpr int kUnits = 256;  // compute units
+
 struct Side {
     const uint8_t* codes;
     const uint8_t* scales;
@@ -101,19 +103,21 @@ struct Loader {
     int off[N];
     __amdgpu_buffer_rsrc_t rsrc;
     __device__ __forceinline__ void init(const uint8_t* codes, int64_t pitch, int64_t row0, int64_t rows, int len,
-                                         int wave) {
+                                         int wave, int lane) {
         const int64_t left = rows - 1 - row0;
         const int last = left < ROWS - 1 ? (int)left : ROWS - 1;
 #pragma unroll
-        for (int i = 0; i < N; ++i) off[i] = min(row(wave, i), last) * (int)pitch + piece(wave, i) * 16;
+        for (int i = 0; i < N; ++i) off[i] = min(row(wave, i, lane), last) * (int)pitch + piece(wave, i, lane) * 16;
         rsrc = buffer_of(codes + row0 * pitch, last * (int)pitch + len);
     }
-    __device__ __forceinline__ static int row(int wave, int i) { return (wave * N + i) * 8 + lane_id() / 8; }
-    __device__ __forceinline__ static int piece(int wave, int i) { return piece_slot(row(wave, i), lane_id() % 8); }
+    __device__ __forceinline__ static int row(int wave, int i, int lane) { return (wave * N + i) * 8 + lane / 8; }
+    __device__ __forceinline__ static int piece(int wave, int i, int lane) {
+        return piece_slot(row(wave, i, lane), lane % 8);
+    }
     // load `i` of N of stage s.  WHOLE: the rows reach the stage's end.
     template <bool WHOLE>
     __device__ __forceinline__ void load(int i, uint32_t lds, int wave, int s, int len) const {
-        const int over = WHOLE ? 0 : max(s * kStage + piece(wave, i) * 16 - (len - 16), 0);
+        const int over = WHOLE ? 0 : max(s * kStage + piece(wave, i, lane_id()) * 16 - (len - 16), 0);
         load_lds16(rsrc, lds + (wave * N + i) * 1024, off[i] - over, s * kStage);
     }
 };
@@ -167,10 +171,18 @@ struct ScaleLoader {
 // their operands would fill the registers.  So loads are issued past the end
 // too (they repeat the last pieces), and those of the scales by fewer waves
 // than there are with an empty mask in the others.
+//
+// The two largest tiles, of whose blocks a compute unit holds one, go on to
+// further tiles (LOOP): the scales and the first stage of the next one are on
+// their way while the results of this one leave through the other stage's
+// buffer (16384 x 8192 x 8192 501 us against 508 with a block for each tile,
+// with tiles of 128 x 256 646 against 661).  More would need their stores out of
+// the way of the waits for loads, which count both in one order.
 template <class T, bool ADD, int BN, int BM, int WN, int WM, int KW, int NB>
 __global__ void __launch_bounds__(WN * WM * KW * WAVE)
 k_mm_mx_pipe(Args g, T* __restrict__ c) {
     constexpr int NW = WN * WM * KW, STEPS = 4 / KW;
+    constexpr bool LOOP = KW == 1 && NB == 2;
     constexpr int FN = BN / WN / 32, FM = BM / WM / 32;
     constexpr int TB = BN * kStage, STAGE = (BN + BM) * kStage;  // weights first, then tokens
     constexpr int NC = NB == 2 ? 2 : 3;                          // chunks in LDS
@@ -179,14 +191,19 @@ k_mm_mx_pipe(Args g, T* __restrict__ c) {
     static_assert(NB * STAGE + NC * BLOCKS * 1024 <= 160 * 1024 && NB >= 2 && NB <= 4, "LDS");
     __shared__ __align__(1024) uint8_t lds[NB * STAGE + NC * BLOCKS * 1024];
 
+    // results, 32 tokens x FS * 32 columns at a time: bytes of a row, its 16-byte pieces, elements of one, stores
+    constexpr int OM = FM / KW, SPACE = (LOOP ? 1 : NB) * STAGE;
+    constexpr int FS = NW * 32 * FN * 32 * (int)sizeof(T) <= SPACE ? FN : FN / 2;
+    constexpr int RB = FS * 32 * (int)sizeof(T), PR = RB / 16, E = 16 / (int)sizeof(T), STORES = RB / 32;
+    static_assert((PR & (PR - 1)) == 0 && PR <= WAVE && NW * 32 * RB <= SPACE && FN % FS == 0, "a wave's part of LDS");
+
     const uint32_t tn = (uint32_t)((g.b.rows + BN - 1) / BN), tm = (uint32_t)((g.a.rows + BM - 1) / BM);
-    const Tile2 tile = tile_of<4>(blockIdx.x, tn, tm);
-    const int64_t n0 = (int64_t)tile.x * BN, m0 = (int64_t)tile.y * BM;
     const int w = __builtin_amdgcn_readfirstlane(wave_id());
     const int wk = w % KW, wn = w / KW % WN, wm = w / KW / WN;
     const int l = lane_id(), half = l >> 5;
     // this split's part of a row
     const int first = (int)blockIdx.y * g.stages_per_split;
+    c += (int64_t)blockIdx.y * g.split_stride;
     const int len = min((int)g.pitch - first * kStage, g.stages_per_split * kStage);
     const int slen = (int)g.spitch - first * 8;
     const int stages = (len + kStage - 1) / kStage, whole = len / kStage;
@@ -194,11 +211,19 @@ k_mm_mx_pipe(Args g, T* __restrict__ c) {
     Loader<BM, NW> la;
     constexpr int LOADS = lb.N + la.N, SOON = LOADS / 4;
     constexpr int SLOTS = (STEPS - 1) * FN, LATER = (LOADS - SOON + SLOTS - 1) / SLOTS;  // of the others at a time
-    lb.init(g.b.codes + first * kStage, g.pitch, n0, g.b.rows, len, w);
-    la.init(g.a.codes + first * kStage, g.pitch, m0, g.a.rows, len, w);
     ScaleLoader xb, xa;
-    xb.init(g.b.scales + first * 8, g.spitch, n0, g.b.rows, BN, slen);
-    xa.init(g.a.scales + first * 8, g.spitch, m0, g.a.rows, BM, slen);
+    int64_t n0, m0;
+    auto go_to = [&](uint32_t id) {
+        const Tile2 tile = tile_of<4>(id, tn, tm);
+        n0 = (int64_t)tile.x * BN;
+        m0 = (int64_t)tile.y * BM;
+        int lane = lane_id();  // opaque: what follows from it is not kept over the loop of stages
+        asm volatile("" : "+v"(lane));
+        lb.init(g.b.codes + first * kStage, g.pitch, n0, g.b.rows, len, w, lane);
+        la.init(g.a.codes + first * kStage, g.pitch, m0, g.a.rows, len, w, lane);
+        xb.init(g.b.scales + first * 8, g.spitch, n0, g.b.rows, BN, slen);
+        xa.init(g.a.scales + first * 8, g.spitch, m0, g.a.rows, BM, slen);
+    };
 
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(lds));
     auto fetch_part = [&](auto fast, int part, int buf, int s) {  // one of LOADS
@@ -254,7 +279,7 @@ k_mm_mx_pipe(Args g, T* __restrict__ c) {
         }
     };
 
-    f32x16 acc[FN][FM] = {};
+    f32x16 acc[FN][FM];
     i32x4 fb[2][FN], fa[2][FM];
     // Stage s in buffer `buf`, the next one in `next`.  Fast: stages up to s +
     // NB exist and are whole.
@@ -297,145 +322,170 @@ k_mm_mx_pipe(Args g, T* __restrict__ c) {
         for (int j = 0; j < FM; ++j) sa[j] = na[j];
     };
 
+    // A tile's first loads: scales and all stages but the last of NB.  Stage s
+    // lies in buffer (s + 1) % NB, so that these leave buffer 0 alone.
+    auto begin = [&]() {
 #pragma unroll
-    for (int x = 0; x < kChunk + NB - 1; ++x) fetch_scales(std::false_type{}, x / kChunk, x % kChunk);
+        for (int x = 0; x < kChunk + NB - 1; ++x) fetch_scales(std::false_type{}, x / kChunk, x % kChunk);
 #pragma unroll
-    for (int s = 0; s < NB; ++s) {
+        for (int s = 0; s + 1 < NB; ++s) {
 #pragma unroll
-        for (int part = 0; part < (s + 1 < NB ? LOADS : SOON); ++part) fetch_part(std::false_type{}, part, s, s);
-    }
-    lds_landed_but<(NB - 2) * LOADS + SOON>();
-    read_scales(0, sb, sa);
-    mine(sb, sa);
+            for (int part = 0; part < LOADS; ++part) fetch_part(std::false_type{}, part, s + 1, s);
+        }
+    };
+    go_to(blockIdx.x);
+    begin();
+    int stores = 0;  // of the tile before, behind the loads of begin()
+    for (uint32_t id = blockIdx.x;;) {
 #pragma unroll
-    for (int j = 0; j < FM; ++j) fa[0][j] = read_a(0, wk * STEPS, j);
+        for (int part = 0; part < SOON; ++part) fetch_part(std::false_type{}, part, 0, NB - 1);
+        if (LOOP && stores) lds_landed_but<SOON + OM * (FN / FS) * STORES>();
+        else lds_landed_but<(NB - 2) * LOADS + SOON>();
+        read_scales(0, sb, sa);
+        mine(sb, sa);
 #pragma unroll
-    for (int i = 0; i < FN; ++i) fb[0][i] = read_b(std::false_type{}, 0, wk * STEPS, i, 0);
-    // fast stages: where rows of scales end inside a piece, those whose chunks are whole
-    const int fast_end = min(whole, slen % 16 == 0 ? whole : slen / kScaleBytes * kChunk - kChunk + 1);
-    int s = 0;
-    for (; s + 2 * NB - 1 < fast_end; s += NB) {
+        for (int i = 0; i < FN; ++i)
 #pragma unroll
-        for (int u = 0; u < NB; ++u) stage(u, (u + 1) % NB, std::true_type{}, s + u);
-    }
+            for (int j = 0; j < FM; ++j) acc[i][j] = f32x16{};
+#pragma unroll
+        for (int j = 0; j < FM; ++j) fa[0][j] = read_a(1 % NB, wk * STEPS, j);
+#pragma unroll
+        for (int i = 0; i < FN; ++i) fb[0][i] = read_b(std::false_type{}, 1 % NB, wk * STEPS, i, 0);
+        // fast stages: where rows of scales end inside a piece, those whose chunks are whole
+        const int fast_end = min(whole, slen % 16 == 0 ? whole : slen / kScaleBytes * kChunk - kChunk + 1);
+        int s = 0;
+        for (; s + 2 * NB - 1 < fast_end; s += NB) {
+#pragma unroll
+            for (int u = 0; u < NB; ++u) stage((u + 1) % NB, (u + 2) % NB, std::true_type{}, s + u);
+        }
 #pragma unroll 1
-    for (; s < stages; ++s) stage(s % NB, (s + 1) % NB, std::false_type{}, s);
-    lds_landed();  // every wave has read its last fragments, and no load is on its way
+        for (; s < stages; ++s) stage((s + 1) % NB, (s + 2) % NB, std::false_type{}, s);
+        lds_landed();  // every wave has read its last fragments, and no load is on its way
+        const int64_t n_here = n0, m_here = m0;
+        id += gridDim.x;
+        const bool more = LOOP && id < tn * tm;
+        if (more) {  // the next tile's first loads, on their way while this one is stored
+            go_to(id);
+            begin();
+        }
 
-    // Two waves with parts of one sum exchange halves of it, tokens by tokens.
-    constexpr int OM = FM / KW;
-    if constexpr (KW == 2) {
-        static_assert(NW * FN * OM * 4096 <= NB * STAGE, "exchange");
-        f32x4* out = reinterpret_cast<f32x4*>(lds + w * (FN * OM * 4096)) + l;
-        const f32x4* in = reinterpret_cast<const f32x4*>(lds + (w ^ 1) * (FN * OM * 4096)) + l;
+        // Two waves with parts of one sum exchange halves of it, tokens by tokens.
+        if constexpr (KW == 2) {
+            static_assert(NW * FN * OM * 4096 <= NB * STAGE, "exchange");
+            f32x4* out = reinterpret_cast<f32x4*>(lds + w * (FN * OM * 4096)) + l;
+            const f32x4* in = reinterpret_cast<const f32x4*>(lds + (w ^ 1) * (FN * OM * 4096)) + l;
 #pragma unroll
-        for (int j = 0; j < OM; ++j)
+            for (int j = 0; j < OM; ++j)
 #pragma unroll
-            for (int i = 0; i < FN; ++i) {
-                f32x16 give;
+                for (int i = 0; i < FN; ++i) {
+                    f32x16 give;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    give[e] = wk ? acc[i][j][e] : acc[i][j + OM][e];
-                    acc[i][j][e] = wk ? acc[i][j + OM][e] : acc[i][j][e];
+                    for (int e = 0; e < 16; ++e) {
+                        give[e] = wk ? acc[i][j][e] : acc[i][j + OM][e];
+                        acc[i][j][e] = wk ? acc[i][j + OM][e] : acc[i][j][e];
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        out[((j * FN + i) * 4 + q) * WAVE] =
+                            f32x4{give[4 * q], give[4 * q + 1], give[4 * q + 2], give[4 * q + 3]};
                 }
+            __syncthreads();
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    out[((j * FN + i) * 4 + q) * WAVE] =
-                        f32x4{give[4 * q], give[4 * q + 1], give[4 * q + 2], give[4 * q + 3]};
-            }
-        __syncthreads();
+            for (int j = 0; j < OM; ++j)
 #pragma unroll
-        for (int j = 0; j < OM; ++j)
+                for (int i = 0; i < FN; ++i)
 #pragma unroll
-            for (int i = 0; i < FN; ++i)
+                    for (int q = 0; q < 4; ++q) {
+                        const f32x4 v = in[((j * FN + i) * 4 + q) * WAVE];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
+                    }
+            __syncthreads();
+        }
+
+        // 32 tokens at a time through the wave's part of LDS, so that a store takes
+        // whole 16-byte pieces of a few rows of C.  Piece p of row r in slot p ^ r.
+        uint8_t* own = lds + w * (32 * RB);
+        int lane = l;  // opaque, as in go_to
+        asm volatile("" : "+v"(lane));
+        const bool inside = n_here + BN <= g.b.rows && m_here + BM <= g.a.rows;
+#pragma unroll
+        for (int ji = 0; ji < OM * (FN / FS); ++ji) {
+            const int j = ji / (FN / FS), i0 = ji % (FN / FS) * FS;
+            const int64_t row0 = m_here + (wm * FM + wk * OM + j) * 32, col0 = n_here + (wn * FN + i0) * 32;
+            // where store q of this lane goes, and how many columns there are
+            auto place = [&](int q, T*& to) {
+                const int r = (q * WAVE + lane) / PR, p = (q * WAVE + lane) % PR;
+                const int64_t row = row0 + r, col = col0 + p * E;
+                to = c + row * g.ldc + col;
+                return inside || row < g.a.rows ? g.b.rows - col : (int64_t)0;
+            };
+#pragma unroll
+            for (int i = 0; i < FS; ++i) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const f32x4 v = in[((j * FN + i) * 4 + q) * WAVE];
+                    float v[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += v[e];
+                    for (int e = 0; e < 4; ++e) v[e] = acc[i0 + i][j][4 * q + e];
+                    const int at = (i * 32 + q * 8 + 4 * (lane >> 5)) * (int)sizeof(T), r = lane & 31;
+                    const auto four = packed4(c, v);
+                    *reinterpret_cast<std::remove_const_t<decltype(four)>*>(
+                        own + r * RB + (((at >> 4) ^ (r & (PR - 1))) << 4) + (at & 15)) = four;
                 }
-        __syncthreads();
-    }
-
-    // 32 tokens at a time through the wave's part of LDS, so that a store takes
-    // whole 16-byte pieces of a few rows of C.  Piece p of row r in slot p ^ r.
-    constexpr int COLS = FN * 32, RB = COLS * (int)sizeof(T), PR = RB / 16, E = 16 / (int)sizeof(T);
-    static_assert((PR & (PR - 1)) == 0 && PR <= WAVE && NW * 32 * RB <= NB * STAGE, "a wave's part of LDS");
-    uint8_t* own = lds + w * (32 * RB);
-    c += (int64_t)blockIdx.y * g.split_stride;
-    const bool inside = n0 + BN <= g.b.rows && m0 + BM <= g.a.rows;
-    constexpr int STORES = RB / 32;
-#pragma unroll
-    for (int j = 0; j < OM; ++j) {
-        const int64_t row0 = m0 + (wm * FM + wk * OM + j) * 32, col0 = n0 + wn * COLS;
-        // where store q of this lane goes, and how many columns there are
-        auto place = [&](int q, T*& to) {
-            const int r = (q * WAVE + l) / PR, p = (q * WAVE + l) % PR;
-            const int64_t row = row0 + r, col = col0 + p * E;
-            to = c + row * g.ldc + col;
-            return inside || row < g.a.rows ? g.b.rows - col : (int64_t)0;
-        };
-#pragma unroll
-        for (int i = 0; i < FN; ++i) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e];
-                const int at = (i * 32 + q * 8 + 4 * half) * (int)sizeof(T), r = l & 31;
-                const auto four = packed4(c, v);
-                *reinterpret_cast<std::remove_const_t<decltype(four)>*>(
-                    own + r * RB + (((at >> 4) ^ (r & (PR - 1))) << 4) + (at & 15)) = four;
             }
+            wave_lds_sync();
+            auto piece = [&](int q) {
+                const int r = (q * WAVE + lane) / PR, p = (q * WAVE + lane) % PR;
+                return own + r * RB + ((p ^ (r & (PR - 1))) << 4);
+            };
+            if (ADD && inside) {
+                // what is there: eight loads before the first store, which the compiler
+                // could move no load ahead of (4096 x 4096 x 4096: 65 us with each load
+                // before its store)
+                constexpr int AT = STORES < 8 ? STORES : 8;
+#pragma unroll
+                for (int q = 0; q < STORES; q += AT) {
+                    u32x4 old[AT];
+                    T* to[AT];
+#pragma unroll
+                    for (int e = 0; e < AT; ++e) {
+                        place(q + e, to[e]);
+                        old[e] = *reinterpret_cast<const u32x4_a2*>(to[e]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < AT; ++e) {
+                        u32x4 v = *reinterpret_cast<const u32x4*>(piece(q + e));
+#pragma unroll
+                        for (int f = 0; f < 4; ++f)
+                            v[f] = __float_as_uint(__uint_as_float(old[e][f]) + __uint_as_float(v[f]));
+                        *reinterpret_cast<u32x4_a2*>(to[e]) = v;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < STORES; ++q) {
+                    T* to;
+                    const int64_t left = place(q, to);
+                    if (!ADD && (inside || left >= E)) {
+                        *reinterpret_cast<u32x4_a2*>(to) = *reinterpret_cast<const u32x4*>(piece(q));
+                    } else {
+                        for (int e = 0; e < E; ++e)
+                            if (e < left) put_result<ADD>(to + e, to_f32(reinterpret_cast<const T*>(piece(q))[e]));
+                    }
+                }
+            }
+            wave_lds_sync();
         }
-        wave_lds_sync();
-        auto piece = [&](int q) {
-            const int r = (q * WAVE + l) / PR, p = (q * WAVE + l) % PR;
-            return own + r * RB + ((p ^ (r & (PR - 1))) << 4);
-        };
-        if (ADD && inside) {
-            // what is there: eight loads before the first store, which the compiler
-            // could move no load ahead of (4096 x 4096 x 4096: 65 us with each load
-            // before its store)
-            constexpr int AT = STORES < 8 ? STORES : 8;
-#pragma unroll
-            for (int q = 0; q < STORES; q += AT) {
-                u32x4 old[AT];
-                T* to[AT];
-#pragma unroll
-                for (int e = 0; e < AT; ++e) {
-                    place(q + e, to[e]);
-                    old[e] = *reinterpret_cast<const u32x4_a2*>(to[e]);
-                }
-#pragma unroll
-                for (int e = 0; e < AT; ++e) {
-                    u32x4 v = *reinterpret_cast<const u32x4*>(piece(q + e));
-#pragma unroll
-                    for (int f = 0; f < 4; ++f)
-                        v[f] = __float_as_uint(__uint_as_float(old[e][f]) + __uint_as_float(v[f]));
-                    *reinterpret_cast<u32x4_a2*>(to[e]) = v;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int q = 0; q < STORES; ++q) {
-                T* to;
-                const int64_t left = place(q, to);
-                if (!ADD && (inside || left >= E)) {
-                    *reinterpret_cast<u32x4_a2*>(to) = *reinterpret_cast<const u32x4*>(piece(q));
-                } else {
-                    for (int e = 0; e < E; ++e)
-                        if (e < left) put_result<ADD>(to + e, to_f32(reinterpret_cast<const T*>(piece(q))[e]));
-                }
-            }
-        }
-        wave_lds_sync();
+        if (!more) break;
+        stores = inside;
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // buffer 0 is free
     }
 }
 
 template <class T, bool ADD, int BN, int BM, int WN, int WM, int KW, int NB>
 hipError_t launch_pipe(const Args& g, int splits, T* c, hipStream_t stream) {
-    const int64_t tiles = ((g.b.rows + BN - 1) / BN) * ((g.a.rows + BM - 1) / BM);
+    int64_t tiles = ((g.b.rows + BN - 1) / BN) * ((g.a.rows + BM - 1) / BM);
+    if (KW == 1 && NB == 2 && splits == 1 && tiles > kUnits) tiles = kUnits;  // the blocks go on to the others
     hipLaunchKernelGGL((k_mm_mx_pipe<T, ADD, BN, BM, WN, WM, KW, NB>), dim3((unsigned)tiles, splits),
                        dim3(WN * WM * KW * WAVE), 0, stream, g, c);
     return hipGetLastError();
@@ -743,7 +793,6 @@ struct Shape {
     int bn, bm;  // channels, tokens
     float first, first_k, more, more_k;
 };
-constexpr int kUnits = 256;  // compute units, each with one block at work
 constexpr Shape kShapes[] = {
     {16, 16, 2.4f, 0.52f, 1.2f, 0.2f},   {32, 16, 2.6f, 0.63f, 1.3f, 0.33f},   {32, 32, 2.9f, 0.8f, 1.5f, 0.47f},
     {32, 64, 3.6f, 0.97f, 2.2f, 0.65f},  {64, 64, 5.0f, 1.43f, 1.5f, 1.07f},   {64, 128, 5.6f, 2.05f, 3.6f, 1.93f},

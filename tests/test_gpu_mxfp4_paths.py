@@ -22,6 +22,8 @@ SIZES = [
     (2100, 2050, 5000), (2040, 4090, 3225), (4330, 41, 38264),
     (4090, 4090, 4111), (4096, 4096, 4224), (4000, 3900, 1500), (130, 2938, 65302),
     (257, 255, 512), (300, 520, 1030), (1024, 70, 300), (300, 8847, 385), (162, 19082, 993),
+    # blocks that go on to a second and a third tile
+    (4300, 4353, 300), (2100, 8500, 3001), (5000, 8200, 33), (8150, 4090, 1500), (4095, 8190, 4000),
 ]
 
 

@@ -36,5 +36,14 @@ def test_every_path_is_reached():
             assert (shape, 2, True) in loops, shape
             assert any(s == shape and t == 0 for s, t, _ in loops) or any(s == shape and t == 1 for s, t, _ in loops)
     assert any(t == 2 and not ragged for _, t, ragged in loops)
+    further = set()
+    for m, n, k in paths.SIZES:
+        shape, parts, each = plan.product(m, n, k)
+        bn, bm = (int(v) for v in plan.SHAPES[shape][:2])
+        tiles = -(-n // bn) * -(-m // bm)
+        if parts == 1 and tiles > 256:
+            further.add((shape, min(-(-tiles // 256), 3), min(plan.fast_turns(k, shape), 1)))
+    last = len(plan.SHAPES) - 1
+    assert {(last, 2, 1), (last, 3, 0), (last - 1, 3, 0), (last - 1, 3, 1)} <= further, further
     assert {m for m, _, _ in small.SIZES} >= {1, 2, 7}  # encoded by the blocks that multiply them
     assert any(4 < m <= plan.FEW and n > 4096 for m, n, _ in small.WIDE)
