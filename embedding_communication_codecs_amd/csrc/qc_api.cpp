@@ -692,7 +692,8 @@ int qc_decode_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, i
 
 int64_t qc_matmul_mxfp4_workspace(int64_t m, int64_t n, int64_t k) {
     if (k < 1 || bad_mx_product(m, n, k)) return -1;
-    return m == 0 || n == 0 ? 0 : qc::matmul_mxfp4_workspace(m, n, k);
+    if (m == 0 || n == 0) return 0;
+    return k > kMaxProductStride ? -1 : qc::matmul_mxfp4_workspace(m, n, k);
 }
 
 int qc_matmul_mxfp4(const uint8_t* a, const uint8_t* a_scales, const uint8_t* b, const uint8_t* b_scales, int64_t m,
@@ -714,7 +715,8 @@ int qc_matmul_mxfp4(const uint8_t* a, const uint8_t* a_scales, const uint8_t* b,
 
 int64_t qc_linear_mxfp4_workspace(int64_t m, int64_t n, int64_t k, int32_t xtype) {
     if (bad_type(xtype) || k < 1 || bad_mx_product(m, n, k)) return -1;
-    return m == 0 || n == 0 ? 0 : qc::linear_mxfp4_workspace(m, n, k, xtype == QC_BF16);
+    if (m == 0 || n == 0) return 0;
+    return k > kMaxProductStride ? -1 : qc::linear_mxfp4_workspace(m, n, k, xtype == QC_BF16);
 }
 
 int qc_linear_mxfp4(const void* x, int32_t xtype, int64_t ldx, const uint8_t* b, const uint8_t* b_scales, int64_t m,

@@ -720,7 +720,7 @@ int qc_decode_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, i
  *                 are held there until they are joined.  Calls that may run
  *                 at the same time, from two streams or two captured graphs,
  *                 need one each.  qc_matmul_mxfp4_workspace() is -1, no
- *                 status, for bad sizes.
+ *                 status, for sizes that the product refuses.
  * Errors: ARG (NULL pointer, bad type, m or n < 0, k < 1, a stride below its
  *         row, too little workspace, 2^23 tiles of 256 x 256 or more), ALIGN,
  *         UNSUPPORTED (accumulate with a bf16 c, k above 2^23).

@@ -136,6 +136,15 @@ class Elsewhere(OnGpu):
         return 0
 
 
+def test_workspace_of_rows_that_are_too_long(qc):  # noqa: F811
+    """As many bytes as the product would refuse to use: none, and no arithmetic on a length past 32 bits."""
+    L = qc.lib()
+    for k in ((1 << 23) + 1, 1 << 32, 1 << 45, 1 << 56):
+        assert L.qc_matmul_mxfp4_workspace(1, 1, k) == L.qc_linear_mxfp4_workspace(1, 1, k, 0) == -1, k
+        assert L.qc_matmul_mxfp4_workspace(0, 1, k) == L.qc_linear_mxfp4_workspace(1, 0, k, 0) == 0
+    assert L.qc_matmul_mxfp4_workspace(1, 1, 1 << 23) >= 0
+
+
 def T(shape, dtype, device=0):
     t = Elsewhere(torch.zeros(shape, dtype=dtype))
     t.get_device = lambda: device
