@@ -803,6 +803,7 @@ constexpr int kAll = sizeof(kShapes) / sizeof(kShapes[0]), kFirstPipe = 4;
 // Only the pipelined tiles are split, as the others share k among their waves;
 // a part has at least four stages.
 constexpr int kMaxSplits = 16, kLeastStages = 4;
+constexpr int64_t kMaxGrid = (int64_t(1) << 23) - 1;  // of 512 threads: a launch has fewer than 2^32
 
 struct Choice {
     int shape, splits, stages_per_split;
@@ -817,7 +818,7 @@ Choice choose(int64_t m, int64_t n, int64_t k) {
     for (int i = 0; i < kAll; ++i) {
         const Shape& s = kShapes[i];
         const int64_t blocks = ((n + s.bn - 1) / s.bn) * ((m + s.bm - 1) / s.bm);
-        if (blocks >= int64_t(1) << 23) continue;  // a grid has fewer than 2^32 threads; the last shape has
+        if (blocks > kMaxGrid) continue;  // the last shape has no more
         for (int splits = 1; splits <= (i >= kFirstPipe ? kMaxSplits : 1); splits *= 2) {
             const int each = (stages + splits - 1) / splits;
             if (splits > 1 && (each < kLeastStages || blocks * splits > 2 * kUnits)) break;
@@ -883,6 +884,7 @@ Args args_of(const void* a, const void* a_scales, const void* b, const void* b_s
 // channels where those of 16 are more than the compute units and each encodes
 // eight tokens (8 x 8192 x 8192 11.0 us against 15.5).
 constexpr int kFew = 8;
+bool takes_fused(int64_t m, int64_t n) { return m <= kFew && (n + 15) / 16 <= kMaxGrid; }
 
 template <class T, class V>
 hipError_t fused(Args g, const X& x, T* c, int64_t ldc, hipStream_t stream) {
@@ -916,14 +918,14 @@ hipError_t launch_matmul_mxfp4(const void* a, const void* a_scales, const void* 
 // Codes of x, then their scales, each from a multiple of 256 bytes on; then the product's own.
 int64_t linear_mxfp4_workspace(int64_t m, int64_t n, int64_t k, bool x_bf16) {
     (void)x_bf16;
-    if (m <= kFew) return 0;
+    if (takes_fused(m, n)) return 0;
     return up256(m * ((k + 31) / 32 * 16)) + up256(m * ((k + 127) / 128 * 4)) + matmul_mxfp4_workspace(m, n, k);
 }
 
 hipError_t launch_linear_mxfp4(const void* x, bool x_bf16, int64_t ldx, const void* b, const void* b_scales, int64_t m,
                                int64_t n, int64_t k, void* c, bool bf16, int64_t ldc, void* workspace,
                                hipStream_t stream) {
-    if (m <= kFew) {
+    if (takes_fused(m, n)) {
         const Args g = args_of(nullptr, nullptr, b, b_scales, m, n, k, 0);
         const X in{x, ldx, k};
         if (bf16)

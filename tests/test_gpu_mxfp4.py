@@ -322,6 +322,25 @@ def test_captured_and_replayed(qc, m, n, k):
         check_product(c1.cpu(), ref.held(*ref.encode(xs), k), ref.held(bc, bs, k))
 
 
+def test_more_channels_than_one_launch_encodes_tokens_for(qc):
+    """2^27 channels: 16 a block of 512 threads would be a launch of 2^32."""
+    m, n, k, period = 2, (1 << 27) + 5, 32, 4099
+    (bc, bs), x = ref.random_mx(period, k, 1), matrix(m, k, 2, F32)
+    whole = n // period * period
+    b = Held(qc, n, k)
+    for t, v in ((b.codes.view(n, -1), bc), (b.scales.view(n, -1), bs)):
+        v = torch.from_numpy(v).cuda().view(period, -1)
+        t[:whole].view(-1, *v.shape)[:] = v
+        t[whole:] = v[: n - whole]
+    c = torch.full((m, n), float("nan"), device="cuda")
+    w = space(qc.qc_linear_mxfp4_workspace(m, n, k, qc.QC_F32))
+    qc.qc_linear_mxfp4(x.cuda(), qc.QC_F32, k, *b.pair(), m, n, k, c, qc.QC_F32, n, w)
+    check_product(c[:, :period].cpu(), ref.held(*ref.encode(x), k), ref.held(bc, bs, k))
+    for row in c:
+        assert bool((row[:whole].view(-1, period) == row[:period]).all())
+        assert torch.equal(row[whole:], row[: n - whole])
+
+
 def test_codes_past_32_bit_offsets(qc):
     """A tall matrix: codes of its last rows lie more than 2^32 bytes behind
     its first ones, its values further."""

@@ -145,6 +145,15 @@ def test_workspace_of_rows_that_are_too_long(qc):  # noqa: F811
     assert L.qc_matmul_mxfp4_workspace(1, 1, 1 << 23) >= 0
 
 
+def test_one_launch_takes_fewer_than_2_to_the_32_threads(qc):  # noqa: F811
+    """A few tokens are encoded by the blocks that multiply them, 512 threads
+    for 16 channels, as far as one launch goes; then by a launch of their own."""
+    most = 16 * ((1 << 23) - 1)
+    for m in (1, 4, 8):
+        assert qc.qc_linear_mxfp4_workspace(m, most, 32, 1) == 0
+        assert qc.qc_linear_mxfp4_workspace(m, most + 1, 32, 1) == 512
+
+
 def T(shape, dtype, device=0):
     t = Elsewhere(torch.zeros(shape, dtype=dtype))
     t.get_device = lambda: device
