@@ -9,6 +9,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <limits>
 
 #include "qc_launch.hpp"
 
@@ -774,6 +775,8 @@ int check_adamw(const AdamwArgs& a, qc::AdamwList& l, qc::AdamwStep& s) {
     if (!finite_from_0(a.lr) || !finite_from_0(a.eps) || !finite_from_0(a.weight_decay) || !(a.beta1 >= 0.0) ||
         !(a.beta1 < 1.0) || !(a.beta2 >= 0.0) || !(a.beta2 < 1.0) || a.step < 1)
         return QC_ERR_ARG;
+    // the kernel's reciprocal takes a denominator below the normal numbers for zero
+    if (a.eps > 0.0 && a.eps < std::numeric_limits<float>::min()) return QC_ERR_ARG;
     const int st = check_optimizer_list(a.grads, a.gtype, a.offsets, a.seg_first, a.ntensors, a.n, l.grads);
     if (st != QC_OK || a.n == 0) return st;
     if (!a.params) return QC_ERR_ARG;

@@ -783,6 +783,7 @@ int qc_grad_norm_multi(const void* const* grads, int32_t gtype, const int64_t* o
  *   m = beta1 m + (1 - beta1) g,    v = beta2 v + (1 - beta2) g^2,
  *   p = p (1 - lr weight_decay)
  *       - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps).
+ * With an eps of 0 an element whose gradients were all zero becomes 0 / 0.
  *
  *   params      read (unless master is given) and written, rounded once.
  *   master      fp32[n] or NULL: with bf16 parameters, the weights proper,
@@ -796,8 +797,9 @@ int qc_grad_norm_multi(const void* const* grads, int32_t gtype, const int64_t* o
  *               place of its arguments, so that a captured graph can be
  *               replayed for other steps (t a whole number from 1 to 2^24).
  * Errors: ARG (NULL pointer, bad type, n < 0, ntensors < 1, master with fp32
- *         parameters, lr, eps or weight_decay negative or not finite, beta1
- *         or beta2 outside [0, 1), step < 1), ALIGN.
+ *         parameters, lr, eps or weight_decay negative or not finite, eps
+ *         above 0 and below 2^-126, beta1 or beta2 outside [0, 1), step < 1),
+ *         ALIGN.
  */
 int qc_adamw_multi(void* const* params, int32_t ptype, const void* const* grads, int32_t gtype,
                    const int64_t* offsets, const int32_t* seg_first, int32_t ntensors, int64_t n, float* master,

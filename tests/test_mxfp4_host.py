@@ -88,11 +88,11 @@ REFUSED = {
 STEP = [
     (ARG, [dict(params=None), dict(grads=None), dict(off=None), dict(seg=None), dict(pt=2), dict(gt=-1), dict(n=-1),
            dict(T=0), dict(pt=0), dict(lr=-1.0), dict(lr=math.inf), dict(lr=math.nan), dict(b1=1.0), dict(b1=-0.1),
-           dict(b2=1.0), dict(b2=math.nan), dict(eps=-1e-9), dict(eps=math.inf), dict(wd=-0.1), dict(wd=math.nan),
+           dict(b2=1.0), dict(b2=math.nan), dict(eps=-1e-9), dict(eps=math.inf), dict(eps=1e-39), dict(eps=5e-324), dict(wd=-0.1), dict(wd=math.nan),
            dict(step=0), dict(step=-5), dict(n=BIG), dict(m=None)]),
     (ALIGN, [dict(params=MIS), dict(grads=MIS), dict(off=MIS), dict(seg=A + 2), dict(master=MIS), dict(m=MIS),
              dict(scale=A + 2), dict(sched=A + 2)]),
-    (OK, [dict(n=0), dict(n=0, params=None, m=None)])]
+    (OK, [dict(n=0), dict(n=0, params=None, m=None), dict(n=0, eps=0.0), dict(n=0, eps=2.0 ** -126)])]
 REFUSED["qc_adamw_multi", ADAMW] = STEP + [(ARG, [dict(v=None)]), (ALIGN, [dict(v=MIS)])]
 REFUSED["qc_adamw8_multi", ADAMW8] = STEP + [(ARG, [dict(ms=None), dict(r=None), dict(rs=None)]),
                                              (ALIGN, [dict(ms=MIS), dict(r=MIS), dict(rs=MIS)])]
