@@ -6,6 +6,11 @@
 //   p = p (1 - lr wd) - rate * m / (sqrt(v) * root + eps)
 //
 // with rate = lr / (1 - b1^t) and root = 1 / sqrt(1 - b2^t).
+//
+// Bound by HBM where n is large: the norm reads g once, the step g, p, m and v
+// and writes the last three (268 M elements: norm of fp32 170 us, 6.3 TB/s, as
+// part of it still lies in the last cache; the step in fp32 1400 us, 5.4 TB/s).
+// Short lists are bound by loads that wait for each other.
 #include "qc_matrix.hpp"
 #include "qc_launch.hpp"
 
@@ -18,9 +23,9 @@ namespace {
 // A block of 256 threads takes a run of passes of 2048 elements.  It keeps the
 // tensor that it is in, so a pass inside one tensor loads no table (with the
 // index looked up for each segment of 4096, three loads before the first value,
-// the norm of 268 M bf16 gradients took 274 us).  Where a pass reaches into
-// another tensor each lane searches the few between, and where its four
-// elements lie in more than one, each element's.
+// the norm of 268 M bf16 gradients took 274 us).  Where a pass may reach into
+// another tensor each lane searches the few of its segment for its fours, and
+// where a four lies in more than one, for each element.
 //
 // 32 lanes hold 256 elements, a block of the 8-bit states; a lane four in each
 // half of them, so that an access of fp32 covers 512 bytes without gaps.
@@ -33,7 +38,7 @@ constexpr int kHalf = 128;  // from a lane's first four to its second
 typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
 
 // Four neighbouring values, `left` of which exist (the rest read as +0).
-__device__ __forceinline__ void load4(const float* p, int64_t left, float (&v)[4]) {
+__device__ __forceinline__ void load4(const float* p, int left, float (&v)[4]) {
     if (left >= 4) {
         const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(p));
 #pragma unroll
@@ -43,7 +48,7 @@ __device__ __forceinline__ void load4(const float* p, int64_t left, float (&v)[4
         for (int i = 0; i < 4; ++i) v[i] = i < left ? p[i] : 0.0f;
     }
 }
-__device__ __forceinline__ void load4(const BF16* p, int64_t left, float (&v)[4]) {
+__device__ __forceinline__ void load4(const BF16* p, int left, float (&v)[4]) {
     if (left >= 4) {
         const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const u32x2_a2*>(p));
 #pragma unroll
@@ -56,7 +61,7 @@ __device__ __forceinline__ void load4(const BF16* p, int64_t left, float (&v)[4]
         for (int i = 0; i < 4; ++i) v[i] = i < left ? to_f32(p[i]) : 0.0f;
     }
 }
-__device__ __forceinline__ void store4(float* p, int64_t left, const float (&v)[4]) {
+__device__ __forceinline__ void store4(float* p, int left, const float (&v)[4]) {
     if (left >= 4) {
         const u32x4 w = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
         __builtin_nontemporal_store(w, reinterpret_cast<u32x4_a2*>(p));
@@ -66,7 +71,7 @@ __device__ __forceinline__ void store4(float* p, int64_t left, const float (&v)[
             if (i < left) p[i] = v[i];
     }
 }
-__device__ __forceinline__ void store4(BF16* p, int64_t left, const float (&v)[4]) {
+__device__ __forceinline__ void store4(BF16* p, int left, const float (&v)[4]) {
     if (left >= 4) {
         const u32x2 w = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
         __builtin_nontemporal_store(w, reinterpret_cast<u32x2_a2*>(p));
@@ -85,127 +90,160 @@ struct Tables {
     int64_t passes_per_run;
 };
 
-// Index values are clamped, so that a corrupt index cannot send an access
-// outside the tables.
-__device__ __forceinline__ int32_t clamped(int32_t t, int32_t lo, int32_t hi) { return min(max(t, lo), hi); }
-
-// The tensor of element i, between tensors a and b.
-__device__ __forceinline__ int32_t tensor_at(const Tables& l, int32_t a, int32_t b, int64_t i) {
-    while (a < b) {
-        const int32_t mid = (a + b + 1) >> 1;
-        if (l.off[mid] <= i) a = mid;
-        else b = mid - 1;
-    }
-    return a;
-}
-
-struct Cursor {  // the block's tensor, and where it begins and ends
-    int32_t t;
-    int64_t from, to;
+// The tensors that the pass from element i0 may reach into (a pass lies in one
+// segment).  Index values are clamped, so that a corrupt index cannot send an
+// access outside the tables.
+struct Range {
+    int32_t lo, hi;
 };
-__device__ __forceinline__ void move_to(Cursor& c, const Tables& l, int64_t i) {
-    const int32_t lo = clamped(l.seg[i >> QC_INDEX_SHIFT], 0, l.T - 1);
-    const int32_t hi = clamped(l.seg[(i >> QC_INDEX_SHIFT) + 1], lo, l.T - 1);
-    c.t = tensor_at(l, lo, hi, i);
-    c.from = l.off[c.t];
-    c.to = min(l.off[c.t + 1], l.n);
-}
-// The last tensor that a pass from element i may reach into.
-__device__ __forceinline__ int32_t last_of(const Cursor& c, const Tables& l, int64_t i) {
-    const int64_t last = min(i + kPass, l.n) - 1;
-    return clamped(l.seg[(last >> QC_INDEX_SHIFT) + 1], c.t, l.T - 1);
+__device__ __forceinline__ int32_t clamped(int32_t t, int32_t lo, int32_t hi) { return min(max(t, lo), hi); }
+__device__ __forceinline__ Range range_at(const Tables& l, int64_t i0) {
+    const int32_t* seg = l.seg + (i0 >> QC_INDEX_SHIFT);
+    const int32_t first = seg[0], next = seg[1], lo = clamped(first, 0, l.T - 1);
+    return Range{lo, clamped(next, lo, l.T - 1)};
 }
 
-// The tensors (of a to b) of N elements, i(j) the index of element j.  Their
-// searches go on side by side, so that as many loads are on their way at a time:
-// what a pass over several tensors costs is one load after the other.
-template <int N, class I>
-__device__ __forceinline__ void tensors_of(const Tables& l, int32_t a, int32_t b, I i, int32_t (&t)[N]) {
+// A tensor begins and ends at these elements of the pass (those before and
+// behind it made one), and element 0 of the pass would lie at `param`, `grad`.
+__device__ __forceinline__ int32_t in_pass(const Tables& l, int64_t i0, int64_t off) {
+    return (int32_t)max(min(min(off, l.n) - i0, (int64_t)kPass), (int64_t)-1);
+}
+template <class T>
+__device__ __forceinline__ T* from_pass(T* p, int64_t i0, int64_t off) {
+    return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(p) + (uintptr_t)(i0 - off) * sizeof(T));
+}
+
+// Up to kNear of the range's tensors at a time, read side by side, a thread a
+// tensor, so that the searches wait for LDS and not for one load from memory
+// after the other (24 tensors of 40,000 elements in all: the step 9.5 us with
+// searches in memory, 7.3 here, the norm 5.6 and 4.7; 77 of 3,000,000, bf16 and
+// 8-bit states: 19.4 and 17.6 us, the norm 9.5 and 6.8).
+constexpr int kNear = kThreads - 1;
+template <class P, class G>
+struct Near {
+    int32_t begins[kNear + 1];
+    P* params[kNear];
+    G* grads[kNear];
+};
+template <class P, class G>
+struct Part {
+    const Near<P, G>& near;
+    int32_t lo, hi;
+    __device__ __forceinline__ int32_t begin(int32_t t) const { return near.begins[t - lo]; }
+    __device__ __forceinline__ P* param(int32_t t) const { return near.params[t - lo]; }
+    __device__ __forceinline__ G* grad(int32_t t) const { return near.grads[t - lo]; }
+};
+// f(part) for each part of the range; every thread of the block calls this.
+// `filled`: the last call was for the same pass, and there is one part.
+template <class P, class G, class F>
+__device__ __forceinline__ void for_parts(Near<P, G>& near, const Tables& l, int64_t i0, const Range& r, P* const* ps,
+                                          G* const* gs, bool filled, F f) {
+    for (int32_t lo = r.lo;; lo += kNear) {
+        const int32_t i = threadIdx.x, count = min(r.hi - lo + 1, kNear);
+        if (!filled) {
+            int64_t off = 0;
+            P* p = nullptr;
+            G* g = nullptr;
+            if (i <= count) off = l.off[lo + i];
+            if (i < count) {
+                if (ps) p = ps[lo + i];
+                g = gs[lo + i];
+            }
+            __syncthreads();  // of the part before no thread reads any more
+            if (i <= count) near.begins[i] = in_pass(l, i0, off);
+            if (i < count) {
+                near.params[i] = from_pass(p, i0, off);
+                near.grads[i] = from_pass(g, i0, off);
+            }
+            __syncthreads();
+        }
+        f(Part<P, G>{near, lo, lo + count - 1});
+        if (r.hi - lo < kNear) break;
+    }
+}
+
+// The tensors of N elements, e(j) the place of element j in the pass: of those
+// of the part, the last that begins at the element or before it, else the first.
+// The searches go on side by side.
+template <int N, class L, class E>
+__device__ __forceinline__ void tensors_of(const L& l, E e, int32_t (&t)[N]) {
     int32_t last[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        t[j] = a;
-        last[j] = b;
+        t[j] = l.lo;
+        last[j] = l.hi;
     }
     // every one halves the same range, first to last, so they end together
-    for (int32_t span = b - a; span > 0; span >>= 1) {
-        int32_t mid[N];
-        int64_t v[N];
+    for (int32_t span = l.hi - l.lo; span > 0; span >>= 1) {
+        int32_t mid[N], v[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             mid[j] = (t[j] + last[j] + 1) >> 1;
-            v[j] = l.off[mid[j]];
+            v[j] = l.begin(mid[j]);
         }
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            if (v[j] <= i(j)) t[j] = mid[j];
+            if (v[j] <= e(j)) t[j] = mid[j];
             else last[j] = mid[j] - 1;
         }
     }
 }
 
-// Where a lane's two fours lie: each in one tensor, or over several.
+// A lane's two fours, from e and e + half: each in one tensor, or over several.
 struct Fours {
     int32_t t[2];
-    int64_t at[2];  // index of the first in tensor t
     bool whole[2];
 };
-__device__ __forceinline__ Fours fours_of(const Tables& l, int32_t a, int32_t b, int64_t i, int half) {
+template <class L>
+__device__ __forceinline__ Fours fours_of(const L& l, int e, int half) {
     Fours f;
-    tensors_of<2>(l, a, b, [&](int q) { return i + q * half; }, f.t);
-    int64_t from[2], to[2];
+    tensors_of<2>(l, [&](int q) { return e + q * half; }, f.t);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        from[q] = l.off[f.t[q]];
-        to[q] = min(l.off[f.t[q] + 1], l.n);
-    }
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        f.at[q] = i + q * half - from[q];
-        f.whole[q] = f.at[q] >= 0 && i + q * half + kFour <= to[q];
+        const int first = e + q * half;
+        f.whole[q] = l.begin(f.t[q]) <= first && first + kFour <= l.begin(f.t[q] + 1);
     }
     return f;
 }
 
-// Four elements that lie over several tensors.  Elements past the end, and those
-// of tables that contradict each other, are nowhere.
+// Four elements that lie over several tensors.  Those of another part, past the
+// end, or of tables that contradict each other are not there.
 struct Places {
     int32_t t[kFour];
-    int64_t at[kFour];  // index in tensor t, or -1
+    bool there[kFour];
 };
-__device__ __forceinline__ Places places_of(const Tables& l, int32_t a, int32_t b, int64_t i) {
+template <class L>
+__device__ __forceinline__ Places places_of(const L& l, int e) {
     Places s;
-    tensors_of<kFour>(l, a, b, [&](int j) { return i + j; }, s.t);
+    tensors_of<kFour>(l, [&](int j) { return e + j; }, s.t);
 #pragma unroll
-    for (int j = 0; j < kFour; ++j) {
-        const int64_t from = l.off[s.t[j]], to = l.off[s.t[j] + 1], g = i + j;
-        s.at[j] = g >= from && g < to && g < l.n ? g - from : -1;
-    }
+    for (int j = 0; j < kFour; ++j) s.there[j] = l.begin(s.t[j]) <= e + j && e + j < l.begin(s.t[j] + 1);
     return s;
 }
-template <class T>
-__device__ __forceinline__ void load_places(T* const* xs, const Places& s, float (&v)[kFour]) {
-    const T* p[kFour];
-#pragma unroll
-    for (int j = 0; j < kFour; ++j) p[j] = xs[s.t[j]];
-    T raw[kFour];
+// p(t): where element 0 of the pass would lie in tensor t
+template <class F>
+__device__ __forceinline__ void load_places(F p, const Places& s, int e, float (&v)[kFour]) {
 #pragma unroll
     for (int j = 0; j < kFour; ++j) {
-        raw[j] = T{};
-        if (s.at[j] >= 0) raw[j] = p[j][s.at[j]];
+        const auto at = p(s.t[j]);
+        if (s.there[j]) v[j] = to_f32(at[e + j]);
     }
-#pragma unroll
-    for (int j = 0; j < kFour; ++j) v[j] = to_f32(raw[j]);
 }
-template <class T>
-__device__ __forceinline__ void store_places(T* const* xs, const Places& s, const float (&v)[kFour]) {
-    T* p[kFour];
+template <class F>
+__device__ __forceinline__ void store_places(F p, const Places& s, int e, const float (&v)[kFour]) {
 #pragma unroll
-    for (int j = 0; j < kFour; ++j) p[j] = xs[s.t[j]];
-#pragma unroll
-    for (int j = 0; j < kFour; ++j)
-        if (s.at[j] >= 0) put(p[j] + s.at[j], v[j]);
+    for (int j = 0; j < kFour; ++j) {
+        const auto at = p(s.t[j]);
+        if (s.there[j]) put(at + e + j, v[j]);
+    }
 }
+
+// The tensor that the last pass of a block lay in entirely.
+struct Cursor {
+    int32_t t;
+    int64_t from, to;
+    __device__ __forceinline__ bool holds(int64_t i0, int64_t end) const { return i0 >= from && end <= to; }
+};
 
 // ------------------------------------------------------------ 8-bit states
 // A code is the top bits of the fp32 number y = |x| / scale, whose exponent
@@ -254,7 +292,7 @@ __device__ __forceinline__ uint32_t state_code(float x, float inv, uint32_t u) {
     return c;
 }
 
-__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t left) {
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int left) {
     if (left >= 4) return ld_stream_u32(p);
     uint32_t w = 0;
 #pragma unroll
@@ -262,7 +300,7 @@ __device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t left) {
         if (i < left) w |= (uint32_t)p[i] << (8 * i);
     return w;
 }
-__device__ __forceinline__ void store_codes(uint8_t* p, int64_t left, uint32_t w) {
+__device__ __forceinline__ void store_codes(uint8_t* p, int left, uint32_t w) {
     if (left >= 4) {
         st_u32(p, w);
     } else {
@@ -306,15 +344,15 @@ template <int KIND>
 __global__ void __launch_bounds__(kThreads)
 k_enc_state8(const float* __restrict__ x, int64_t n, uint8_t* __restrict__ codes, float* __restrict__ scale) {
     for (int64_t first = (int64_t)blockIdx.x * kPass; first < n; first += (int64_t)gridDim.x * kPass) {
-        const int64_t i = first + lane_first();
+        const int e = lane_first(), left = (int)min(n - first, (int64_t)kPass) - e;
         float v[2][4];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) load4(x + i + q * kHalf, n - i - q * kHalf, v[q]);
+        for (int q = 0; q < 2; ++q) load4(x + first + e + q * kHalf, left - q * kHalf, v[q]);
         uint32_t w[2];
         const float s = state_codes<KIND>(v, 0x80000000u - State<KIND>::SHIFT, 0u, w);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) store_codes(codes + i + q * kHalf, n - i - q * kHalf, w[q]);
-        if (i < n && (threadIdx.x & 31) == 0) scale[i / QC_STATE_BLOCK] = s;
+        for (int q = 0; q < 2; ++q) store_codes(codes + first + e + q * kHalf, left - q * kHalf, w[q]);
+        if (left > 0 && (threadIdx.x & 31) == 0) scale[first / QC_STATE_BLOCK + threadIdx.x / 32] = s;
     }
 }
 
@@ -322,16 +360,16 @@ template <int KIND, class T>
 __global__ void __launch_bounds__(kThreads)
 k_dec_state8(const uint8_t* __restrict__ codes, const float* __restrict__ scale, int64_t n, T* __restrict__ out) {
     for (int64_t first = (int64_t)blockIdx.x * kPass; first < n; first += (int64_t)gridDim.x * kPass) {
-        const int64_t i = first + lane_first();
-        const float s = i < n ? scale[i / QC_STATE_BLOCK] : 0.0f;
+        const int e = lane_first(), left = (int)min(n - first, (int64_t)kPass) - e;
+        const float s = left > 0 ? scale[first / QC_STATE_BLOCK + threadIdx.x / 32] : 0.0f;
         uint32_t w[2];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) w[q] = load_codes(codes + i + q * kHalf, n - i - q * kHalf);
+        for (int q = 0; q < 2; ++q) w[q] = load_codes(codes + first + e + q * kHalf, left - q * kHalf);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             float v[4];
             state_values<KIND>(w[q], s, v);
-            store4(out + i + q * kHalf, n - i - q * kHalf, v);
+            store4(out + first + e + q * kHalf, left - q * kHalf, v);
         }
     }
 }
@@ -375,77 +413,81 @@ k_adamw(Tables l, P* const* __restrict__ params, G* const* __restrict__ grads, f
     const Rates k = rates_of(step);
     const int64_t first = (int64_t)blockIdx.x * l.passes_per_run * kPass;
     const int64_t end = min(first + l.passes_per_run * kPass, l.n);
+    __shared__ Near<P, G> near;
+    const int e = lane_first();
     Cursor cur{0, 0, 0};
-    P* pp = nullptr;
-    G* gp = nullptr;
 #pragma unroll 1
     for (int64_t i0 = first; i0 < end; i0 += kPass) {
-        const int64_t i = i0 + lane_first();
+        const int left = (int)min(l.n - i0, (int64_t)kPass) - e;
         // the states' places need no table: their loads go first
         float m[2][4], v[2][4], p[2][4], g[2][4];
         uint32_t mc[2], rc[2];
         float ms = 0.0f, rs = 0.0f;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const int64_t at = i + q * kHalf, left = l.n - at;
+            const int at = e + q * kHalf, some = left - q * kHalf;
             if constexpr (WIDE) {
-                load4(st.m + at, left, m[q]);
-                load4(st.v + at, left, v[q]);
+                load4(st.m + i0 + at, some, m[q]);
+                load4(st.v + i0 + at, some, v[q]);
             } else {
-                mc[q] = load_codes(st.mc + at, left);
-                rc[q] = load_codes(st.rc + at, left);
+                mc[q] = load_codes(st.mc + i0 + at, some);
+                rc[q] = load_codes(st.rc + i0 + at, some);
             }
-            if (MASTER) load4(master + at, left, p[q]);
+            if (MASTER) load4(master + i0 + at, some, p[q]);
         }
+        const int64_t block = i0 / QC_STATE_BLOCK + threadIdx.x / 32;
         if constexpr (!WIDE) {
-            if (i < l.n) {
-                ms = st.ms[i / QC_STATE_BLOCK];
-                rs = st.rs[i / QC_STATE_BLOCK];
+            if (left > 0) {
+                ms = st.ms[block];
+                rs = st.rs[block];
             }
         }
-        if (i0 >= cur.to) {
-            move_to(cur, l, i0);
-            pp = params[cur.t];
-            gp = grads[cur.t];
+        Range range{0, 0};
+        if (!cur.holds(i0, i0 + kPass)) {
+            range = range_at(l, i0);
+            if (range.lo == range.hi) cur = Cursor{range.lo, l.off[range.lo], min(l.off[range.lo + 1], l.n)};
         }
-        const bool one = i0 >= cur.from && i0 + kPass <= cur.to;  // the pass is in one tensor
-        Fours f;
+        const bool one = cur.holds(i0, i0 + kPass);
+        bool whole[2] = {one, one};
         P* pq[2];
-        int32_t last = 0;
         if (one) {
+            pq[0] = pq[1] = from_pass(params[cur.t], i0, cur.from);
+            const G* gp = from_pass(grads[cur.t], i0, cur.from);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const int64_t at = i + q * kHalf - cur.from;
-                load4(const_cast<const G*>(gp) + at, kFour, g[q]);
-                if (!MASTER) load4(const_cast<const P*>(pp) + at, kFour, p[q]);
+                load4(gp + e + q * kHalf, kFour, g[q]);
+                if (!MASTER) load4(const_cast<const P*>(pq[q]) + e + q * kHalf, kFour, p[q]);
             }
         } else {
-            last = last_of(cur, l, i0);
-            f = fours_of(l, cur.t, last, i, kHalf);
-            const G* gq[2] = {grads[f.t[0]], grads[f.t[1]]};
-            if (!MASTER) {
-                pq[0] = params[f.t[0]];
-                pq[1] = params[f.t[1]];
-            }
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                if (f.whole[q]) {
-                    load4(gq[q] + f.at[q], kFour, g[q]);
-                    if (!MASTER) load4(const_cast<const P*>(pq[q]) + f.at[q], kFour, p[q]);
-                }
-            }
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                if (!f.whole[q]) {
-                    const Places s = places_of(l, cur.t, last, i + q * kHalf);
-                    load_places(grads, s, g[q]);
-                    if (!MASTER) load_places(params, s, p[q]);
+                for (int j = 0; j < kFour; ++j) {
+                    g[q][j] = 0.0f;
+                    if (!MASTER) p[q][j] = 0.0f;
                 }
-            }
-            if (MASTER) {
-                pq[0] = params[f.t[0]];
-                pq[1] = params[f.t[1]];
-            }
+            for_parts(near, l, i0, range, params, grads, false, [&](const auto& from) {
+                const Fours f = fours_of(from, e, kHalf);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int at = e + q * kHalf;
+                    if (f.whole[q]) {
+                        whole[q] = true;
+                        pq[q] = from.param(f.t[q]);
+                        load4(const_cast<const G*>(from.grad(f.t[q])) + at, kFour, g[q]);
+                        if (!MASTER) load4(const_cast<const P*>(pq[q]) + at, kFour, p[q]);
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int at = e + q * kHalf;
+                    if (!whole[q]) {
+                        const Places s = places_of(from, at);
+                        load_places([&](int t) { return from.grad(t); }, s, at, g[q]);
+                        if (!MASTER) load_places([&](int t) { return from.param(t); }, s, at, p[q]);
+                    }
+                }
+            });
         }
         float r[2][4];
 #pragma unroll
@@ -467,28 +509,35 @@ k_adamw(Tables l, P* const* __restrict__ params, G* const* __restrict__ grads, f
         }
         if constexpr (!WIDE) {
             // every lane of the wave takes part; those past the end hold zeros
-            const uint32_t u = (uint32_t)i * kDitherElem + k.t * kDitherStep;
+            const uint32_t u = ((uint32_t)i0 + e) * kDitherElem + k.t * kDitherStep;
             ms = state_codes<QC_STATE_M>(m, u, kDitherElem, mc);
             rs = state_codes<QC_STATE_R>(r, u, kDitherElem, rc);
-            if (i < l.n && (threadIdx.x & 31) == 0) {
-                st.ms[i / QC_STATE_BLOCK] = ms;
-                st.rs[i / QC_STATE_BLOCK] = rs;
+            if (left > 0 && (threadIdx.x & 31) == 0) {
+                st.ms[block] = ms;
+                st.rs[block] = rs;
             }
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const int64_t at = i + q * kHalf, left = l.n - at;
+            const int at = e + q * kHalf, some = left - q * kHalf;
             if constexpr (WIDE) {
-                store4(st.m + at, left, m[q]);
-                store4(st.v + at, left, v[q]);
+                store4(st.m + i0 + at, some, m[q]);
+                store4(st.v + i0 + at, some, v[q]);
             } else {
-                store_codes(st.mc + at, left, mc[q]);
-                store_codes(st.rc + at, left, rc[q]);
+                store_codes(st.mc + i0 + at, some, mc[q]);
+                store_codes(st.rc + i0 + at, some, rc[q]);
             }
-            if (MASTER) store4(master + at, left, p[q]);
-            if (one) store4(pp + (at - cur.from), kFour, p[q]);
-            else if (f.whole[q]) store4(pq[q] + f.at[q], kFour, p[q]);
-            else store_places(params, places_of(l, cur.t, last, at), p[q]);
+            if (MASTER) store4(master + i0 + at, some, p[q]);
+            if (whole[q]) store4(pq[q] + at, kFour, p[q]);
+        }
+        if (!one) {
+            for_parts(near, l, i0, range, params, grads, range.hi - range.lo < kNear, [&](const auto& to) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int at = e + q * kHalf;
+                    if (!whole[q]) store_places([&](int t) { return to.param(t); }, places_of(to, at), at, p[q]);
+                }
+            });
         }
     }
 }
@@ -518,40 +567,49 @@ k_norm_parts(Tables l, G* const* __restrict__ grads, double* __restrict__ parts)
     constexpr int U = 8;  // fours: of four passes
     const int64_t first = (int64_t)blockIdx.x * l.passes_per_run * kPass;
     const int64_t end = min(first + l.passes_per_run * kPass, l.n);
+    __shared__ Near<const G, G> near;
+    const int e = threadIdx.x * kFour;
     Cursor cur{0, 0, 0};
-    const G* gp = nullptr;
     double sum = 0.0;
 #pragma unroll 1
     for (int64_t i0 = first; i0 < end;) {
-        if (i0 >= cur.to) {
-            move_to(cur, l, i0);
-            gp = grads[cur.t];
+        Range range{0, 0};
+        if (!cur.holds(i0, i0 + kPass)) {
+            range = range_at(l, i0);
+            if (range.lo == range.hi) cur = Cursor{range.lo, l.off[range.lo], min(l.off[range.lo + 1], l.n)};
         }
-        if (i0 >= cur.from && i0 + U / 2 * kPass <= min(cur.to, end)) {
-            const G* p = gp + (i0 + threadIdx.x * kFour - cur.from);
+        const bool one = cur.holds(i0, i0 + kPass);
+        const G* gp = one ? from_pass(grads[cur.t], i0, cur.from) : nullptr;
+        if (one && cur.holds(i0, i0 + U / 2 * kPass) && i0 + U / 2 * kPass <= end) {
             float g[U][4];
 #pragma unroll
-            for (int u = 0; u < U; ++u) load4(p + u * (kPass / 2), kFour, g[u]);
+            for (int u = 0; u < U; ++u) load4(gp + e + u * (kPass / 2), kFour, g[u]);
 #pragma unroll
             for (int u = 0; u < U; ++u) sum = add_squares(sum, g[u]);
             i0 += U / 2 * kPass;
             continue;
         }
-        const int64_t i = i0 + threadIdx.x * kFour;
         float g[2][4];
-        if (i0 >= cur.from && i0 + kPass <= cur.to) {
+        if (one) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) load4(gp + (i + q * (kPass / 2) - cur.from), kFour, g[q]);
+            for (int q = 0; q < 2; ++q) load4(gp + e + q * (kPass / 2), kFour, g[q]);
         } else {
-            const int32_t last = last_of(cur, l, i0);
-            const Fours f = fours_of(l, cur.t, last, i, kPass / 2);
-            const G* gq[2] = {grads[f.t[0]], grads[f.t[1]]};
 #pragma unroll
             for (int q = 0; q < 2; ++q)
-                if (f.whole[q]) load4(gq[q] + f.at[q], kFour, g[q]);
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-                if (!f.whole[q]) load_places(grads, places_of(l, cur.t, last, i + q * (kPass / 2)), g[q]);
+                for (int j = 0; j < kFour; ++j) g[q][j] = 0.0f;
+            for_parts(near, l, i0, range, static_cast<const G* const*>(nullptr), grads, false, [&](const auto& from) {
+                const Fours f = fours_of(from, e, kPass / 2);
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    if (f.whole[q])
+                        load4(const_cast<const G*>(from.grad(f.t[q])) + e + q * (kPass / 2), kFour, g[q]);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int at = e + q * (kPass / 2);
+                    if (!f.whole[q]) load_places([&](int t) { return from.grad(t); }, places_of(from, at), at, g[q]);
+                }
+            });
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q) sum = add_squares(sum, g[q]);

@@ -68,6 +68,8 @@ LISTS = {
     "one": [1], "two_small": [3, 5], "eight": [8], "block": [256], "odd": [257, 255, 1], "empty_ones": [0, 7, 0, 0, 300, 0],
     "segment": [4096], "segments": [4096, 4096, 1], "tiny_many": [1, 2, 3, 4, 5, 6, 7, 8, 9] * 60,
     "mixed": [1000, 3, 4097, 64, 12345, 1, 1, 70000, 33], "large": [1 << 20, 4097, 300001],
+    # more tensors in a segment than a block holds at a time (255), ends of such parts and empty ones among them
+    "parts": [1] * 254 + [0] * 300 + [3] * 255 + [0] * 255 + [5000, 2, 2] + [1] * 2100 + [0] * 700 + [8],
 }
 
 
@@ -219,7 +221,7 @@ def test_infinities_and_nans_stay_visible(qc):
         assert list(np.nonzero(np.isnan(p))[0]) == [300, 1500] and (p[~np.isnan(p)] < 1).all()
 
 
-@pytest.mark.parametrize("name", ["one", "odd", "tiny_many", "mixed", "large"])
+@pytest.mark.parametrize("name", ["one", "odd", "tiny_many", "mixed", "large", "parts"])
 @pytest.mark.parametrize("gtype", [F32, BF16], ids=str)
 def test_norm(qc, name, gtype):
     sizes = LISTS[name]
