@@ -2,7 +2,9 @@
 // and of its transpose (qc_mx.hpp has the format's rules).
 //
 // All of this is bound by HBM: 2 or 4 bytes a value on one side, 1/2 + 1/32 for
-// each of the encodings on the other.
+// each of the encodings on the other.  8192 x 8192, where a copy moves 5.2 TB/s:
+// rows from bf16 30 us, 5.7 TB/s, from fp32 57 us, 5.3; decoded to bf16 28 us,
+// 6.1 (part of the codes lies in the last cache), to fp32 52 us, 5.8.
 #include "qc_launch.hpp"
 #include "qc_lds.hpp"
 #include "qc_mx.hpp"
@@ -84,106 +86,119 @@ k_enc_mxfp4(const T* __restrict__ x, int64_t ldx, Sizes z, Coded k) {
 
 // ---------------------------------------------------------------- columns
 // The transpose's encoding, with or without the matrix's own: tiles of 128 x
-// 128 through LDS.  A thread loads eight pieces of 8 values, 16 rows apart (and
-// encodes them by rows from its registers); then it takes 2 columns x 32 rows,
-// a whole group of each, and their codes leave through LDS again, 64 bytes of a
-// row of the transpose side by side.
-constexpr int kTile = 128;
+// 128 through LDS, 512 threads each.  A thread loads four pieces of 8 values
+// (and encodes them by rows from its registers); then it takes 2 columns x 16
+// rows, half a group of each, whose other half its neighbour has, and their
+// codes leave through LDS again, 64 bytes of a row of the transpose side by
+// side.  Both encodings of 8192 x 8192: bf16 49 us, 4.2 TB/s, fp32 72 us, 4.8.
+// (With 256 threads and whole groups, whose waves have twice the instructions, 50
+// and 75 us, and 1027 x 770 6.0 and 6.6 against 4.8 and 5.7; with 1024, 51 and
+// 67, and 4.7 and 5.9.)
+constexpr int kTile = 128, kHalfGroup = 16;
+
+// Byte of a row of the tile in LDS.  A wave reads 32 pairs of columns in two
+// rows, 16 apart, at a time: for bf16 the 128 bytes of one lie in the other
+// banks.
+template <class T>
+__device__ __forceinline__ int in_tile(int row, int byte) {
+    const int swap = sizeof(T) == 2 ? (row / kHalfGroup & 1) << 7 : 0;
+    return row * kTile * (int)sizeof(T) + (byte ^ swap);
+}
 
 template <class T>
-struct Columns;  // two columns x 32 rows
+struct Columns;  // two columns x 16 rows
 template <>
 struct Columns<BF16> {
-    uint32_t w[32];
+    uint32_t w[kHalfGroup];
     __device__ __forceinline__ void read(const uint8_t* tile, int row0, int pair) {
 #pragma unroll
-        for (int r = 0; r < 32; ++r) w[r] = *reinterpret_cast<const uint32_t*>(tile + (row0 + r) * 256 + pair * 4);
+        for (int r = 0; r < kHalfGroup; ++r)
+            w[r] = *reinterpret_cast<const uint32_t*>(tile + in_tile<BF16>(row0, pair * 4) + r * 256);
     }
     __device__ __forceinline__ void amax_bits(uint32_t (&m)[2]) const {
         uint32_t a = 0;
 #pragma unroll
-        for (int r = 0; r < 32; ++r) a = pair_max(a, w[r]);
+        for (int r = 0; r < kHalfGroup; ++r) a = pair_max(a, w[r]);
         m[0] = a << 16;
         m[1] = a & 0xFFFF0000u;
     }
-    __device__ __forceinline__ u32x4 codes(int c, float scale) const {
+    __device__ __forceinline__ uint32_t codes8(int q, int c, float scale) const {
         const uint32_t pick = c ? 0x07060302u : 0x05040100u;  // that column's halves of two words
-        u32x4 o;
+        u32x4 v;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            u32x4 v;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_perm(w[8 * q + 2 * i + 1], w[8 * q + 2 * i], pick);
-            o[q] = mx_codes8(v, scale);
-        }
-        return o;
+        for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_perm(w[8 * q + 2 * i + 1], w[8 * q + 2 * i], pick);
+        return mx_codes8(v, scale);
     }
 };
 template <>
 struct Columns<float> {
     typedef float f32x2 __attribute__((ext_vector_type(2)));
-    f32x2 w[32];
+    f32x2 w[kHalfGroup];
     __device__ __forceinline__ void read(const uint8_t* tile, int row0, int pair) {
 #pragma unroll
-        for (int r = 0; r < 32; ++r) w[r] = *reinterpret_cast<const f32x2*>(tile + (row0 + r) * 512 + pair * 8);
+        for (int r = 0; r < kHalfGroup; ++r)
+            w[r] = *reinterpret_cast<const f32x2*>(tile + in_tile<float>(row0, pair * 8) + r * 512);
     }
     __device__ __forceinline__ void amax_bits(uint32_t (&m)[2]) const {
         m[0] = m[1] = 0;
 #pragma unroll
-        for (int r = 0; r < 32; ++r) {
+        for (int r = 0; r < kHalfGroup; ++r) {
             m[0] = umax(m[0], abs_bits(w[r][0]));
             m[1] = umax(m[1], abs_bits(w[r][1]));
         }
     }
-    __device__ __forceinline__ u32x4 codes(int c, float scale) const {
-        u32x4 o;
+    __device__ __forceinline__ uint32_t codes8(int q, int c, float scale) const {
+        float v[8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = w[8 * q + i][c];
-            o[q] = mx_codes8(v, scale);
-        }
-        return o;
+        for (int i = 0; i < 8; ++i) v[i] = w[8 * q + i][c];
+        return mx_codes8(v, scale);
     }
 };
 
-__device__ __forceinline__ void put_raw8(uint8_t* p, const Raw8<BF16>& v) { *reinterpret_cast<u32x4*>(p) = v.w; }
-__device__ __forceinline__ void put_raw8(uint8_t* p, const Raw8<float>& v) {
+__device__ __forceinline__ uint32_t pair_of_lanes_max(uint32_t v) {
+    return umax(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));  // quad_perm 1 0 3 2
+}
+
+__device__ __forceinline__ void put_raw8(uint8_t* tile, int row, int col, const Raw8<BF16>& v) {
+    *reinterpret_cast<u32x4*>(tile + in_tile<BF16>(row, col * 2)) = v.w;
+}
+__device__ __forceinline__ void put_raw8(uint8_t* tile, int row, int col, const Raw8<float>& v) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<f32x4*>(p + 16 * h) = f32x4{v.v[4 * h], v.v[4 * h + 1], v.v[4 * h + 2], v.v[4 * h + 3]};
+        *reinterpret_cast<f32x4*>(tile + in_tile<float>(row, col * 4 + 16 * h)) =
+            f32x4{v.v[4 * h], v.v[4 * h + 1], v.v[4 * h + 2], v.v[4 * h + 3]};
 }
 
 template <class T, bool ROWS>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(512)
 k_enc_mxfp4_t(const T* __restrict__ x, int64_t ldx, int64_t rows, int64_t dim, Coded k, Coded kt) {
-    constexpr int RB = kTile * (int)sizeof(T);
-    __shared__ __align__(1024) uint8_t lds[kTile * RB];
+    constexpr int U = 4;
+    __shared__ __align__(1024) uint8_t lds[kTile * kTile * sizeof(T)];
     const Tile2 tile = tile_of<4>(blockIdx.x, (uint32_t)((dim + kTile - 1) / kTile),
                                   (uint32_t)((rows + kTile - 1) / kTile));
     const int64_t r0 = (int64_t)tile.y * kTile, c0 = (int64_t)tile.x * kTile;
     const int t = threadIdx.x;
     {
         const int64_t col = c0 + 8 * (t & 15);
-        Raw8<T> v[8];
+        Raw8<T> v[U];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int64_t row = r0 + 16 * u + (t >> 4);
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = r0 + 32 * u + (t >> 4);
             v[u].template load<true>(x + row * ldx + col, row < rows ? dim - col : 0, col > 0);
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int64_t row = r0 + 16 * u + (t >> 4);
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = r0 + 32 * u + (t >> 4);
             v[u].settle(row < rows ? dim - col : 0, col > 0);
             if (ROWS) keep_row8(v[u], row, col, row < rows, dim, k);
-            put_raw8(lds + (16 * u + (t >> 4)) * RB + 8 * (t & 15) * (int)sizeof(T), v[u]);
+            put_raw8(lds, 32 * u + (t >> 4), 8 * (t & 15), v[u]);
         }
     }
     __syncthreads();
-    const int pair = t & 63, part = t >> 6;  // columns 2 pair and 2 pair + 1, rows 32 part to 32 part + 31
+    // columns 2 pair and 2 pair + 1, rows 32 part + 16 half and on
+    const int half = t & 1, pair = t >> 1 & 63, part = t >> 7;
     Columns<T> v;
-    v.read(lds, 32 * part, pair);
+    v.read(lds, 32 * part + kHalfGroup * half, pair);
     uint32_t m[2];
     v.amax_bits(m);
     const bool group = r0 + 32 * part < rows;  // else: padding, byte 0
@@ -192,20 +207,18 @@ k_enc_mxfp4_t(const T* __restrict__ x, int64_t ldx, int64_t rows, int64_t dim, C
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         const int col = 2 * pair + c;
-        const uint32_t byte = mx_byte(m[c]);
-        u32x4 w = v.codes(c, mx_scale(byte));
-        if (byte == kMxNaN) w = u32x4{0, 0, 0, 0};
-        *reinterpret_cast<u32x4*>(lds + col * 64 + ((part ^ ((col >> 2) & 3)) << 4)) = w;
-        bytes[col * 4 + part] = group ? (uint8_t)byte : 0;
+        const uint32_t byte = mx_byte(pair_of_lanes_max(m[c]));
+        const float scale = mx_scale(byte);
+        u32x2 w = {v.codes8(0, c, scale), v.codes8(1, c, scale)};
+        if (byte == kMxNaN) w = u32x2{0, 0};
+        *reinterpret_cast<u32x2*>(lds + col * 64 + ((part ^ ((col >> 2) & 3)) << 4) + 8 * half) = w;
+        if (half == 0) bytes[col * 4 + part] = group ? (uint8_t)byte : 0;
     }
     __syncthreads();
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int i = q * 256 + t, col = i >> 2, piece = i & 3;
-        if (c0 + col < dim && r0 + 32 * piece < rows)
-            *reinterpret_cast<u32x4*>(kt.codes + (c0 + col) * kt.pitch + r0 / 2 + piece * 16) =
-                *reinterpret_cast<const u32x4*>(lds + col * 64 + ((piece ^ ((col >> 2) & 3)) << 4));
-    }
+    const int to = t >> 2, piece = t & 3;
+    if (c0 + to < dim && r0 + 32 * piece < rows)
+        *reinterpret_cast<u32x4*>(kt.codes + (c0 + to) * kt.pitch + r0 / 2 + piece * 16) =
+            *reinterpret_cast<const u32x4*>(lds + to * 64 + ((piece ^ ((to >> 2) & 3)) << 4));
     if (t < kTile && c0 + t < dim)
         *reinterpret_cast<uint32_t*>(kt.scales + (c0 + t) * kt.spitch + r0 / 32) =
             *reinterpret_cast<const uint32_t*>(bytes + t * 4);
@@ -339,8 +352,8 @@ hipError_t encode(const T* x, int64_t rows, int64_t dim, int64_t ldx, void* code
         return hipGetLastError();
     }
     const dim3 grid((unsigned)(((dim + kTile - 1) / kTile) * ((rows + kTile - 1) / kTile)));
-    if (codes) hipLaunchKernelGGL((k_enc_mxfp4_t<T, true>), grid, dim3(256), 0, stream, x, ldx, rows, dim, k, kt);
-    else hipLaunchKernelGGL((k_enc_mxfp4_t<T, false>), grid, dim3(256), 0, stream, x, ldx, rows, dim, k, kt);
+    if (codes) hipLaunchKernelGGL((k_enc_mxfp4_t<T, true>), grid, dim3(512), 0, stream, x, ldx, rows, dim, k, kt);
+    else hipLaunchKernelGGL((k_enc_mxfp4_t<T, false>), grid, dim3(512), 0, stream, x, ldx, rows, dim, k, kt);
     return hipGetLastError();
 }
 

@@ -646,8 +646,9 @@ int qc_swiglu_ckpt8_backward(const void* dh, int32_t dhtype, int64_t lddh, const
 
 namespace {
 
-// A launch has fewer than 2^32 threads: 256 for a tile of 128 x 128 values.
-constexpr int64_t kMaxMxTiles = (int64_t(1) << 24) - 1;
+// A launch has fewer than 2^32 threads: 256 for a tile of 128 x 128 values,
+// with the transpose 512.
+constexpr int64_t kMaxMxTiles = (int64_t(1) << 24) - 1, kMaxMxTilesT = (int64_t(1) << 23) - 1;
 
 bool bad_mx(int64_t rows, int64_t dim) {
     return rows < 0 || dim < 1 || dim > kMaxMatrixElems / (rows > 0 ? rows : 1);
@@ -673,7 +674,7 @@ int qc_encode_mxfp4(const void* x, int32_t xtype, int64_t rows, int64_t dim, int
     if (rows == 0) return QC_OK;
     if (!x || !codes != !scales || !codes_t != !scales_t || (!codes && !codes_t)) return QC_ERR_ARG;
     if (dim > kMaxCkptDim || (codes_t && rows > kMaxCkptDim)) return QC_ERR_UNSUPPORTED;
-    if (ceil_div(rows, 128) > kMaxMxTiles / ceil_div(dim, 128)) return QC_ERR_ARG;
+    if (ceil_div(rows, 128) > (codes_t ? kMaxMxTilesT : kMaxMxTiles) / ceil_div(dim, 128)) return QC_ERR_ARG;
     if (misaligned_for(x, xtype) || misaligned(codes) || misaligned(scales) || misaligned(codes_t) ||
         misaligned(scales_t))
         return QC_ERR_ALIGN;

@@ -690,8 +690,8 @@ int qc_swiglu_ckpt8_backward(const void* dh, int32_t dhtype, int64_t lddh, const
  * qc_decode_mxfp4 writes the values; they are exact in fp32 and in bf16.
  * Errors: ARG (NULL x or out, one of a pair NULL, both pairs NULL, bad type,
  *         rows < 0, dim < 1, a stride below its row, 2^24 tiles of 128 x 128
- *         values or more), ALIGN, UNSUPPORTED (rows, where transposed, or dim
- *         above 2^34, not for qc_mxfp4_bytes).
+ *         values or more, 2^23 with the transpose), ALIGN, UNSUPPORTED (rows,
+ *         where transposed, or dim above 2^34, not for qc_mxfp4_bytes).
  */
 #define QC_MX_GROUP 32
 int qc_mxfp4_bytes(int64_t rows, int64_t dim, int64_t* code_bytes, int64_t* scale_bytes);

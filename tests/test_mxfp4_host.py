@@ -51,7 +51,8 @@ REFUSED = {
         (ARG, [dict(x=None), dict(codes=None), dict(scales=None), dict(codes_t=None), dict(scales_t=None),
                dict(codes=None, scales=None, codes_t=None, scales_t=None), dict(t=2), dict(t=-1), dict(rows=-1),
                dict(dim=0), dict(ldx=39), dict(rows=BIG), dict(dim=BIG, ldx=BIG),
-               dict(rows=1 << 31, dim=1 << 10, ldx=1 << 10)]),
+               dict(rows=1 << 31, dim=1 << 10, ldx=1 << 10), dict(rows=1 << 30, dim=40, ldx=40),
+               dict(rows=1 << 31, dim=40, ldx=40, codes_t=None, scales_t=None)]),
         (ALIGN, [dict(x=A + 1), dict(t=0, x=A + 2), dict(codes=MIS), dict(scales=MIS), dict(codes_t=MIS),
                  dict(scales_t=MIS)]),
         (UNSUP, [dict(rows=1, dim=(1 << 34) + 1, ldx=(1 << 34) + 1), dict(rows=(1 << 34) + 1, dim=1, ldx=1)]),
