@@ -499,8 +499,10 @@ k_adamw(Tables l, P* const* __restrict__ params, G* const* __restrict__ grads, f
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float x = g[q][e] * k.scale, old = WIDE ? v[q][e] : v[q][e] * v[q][e];
-                m[q][e] = __builtin_fmaf(m[q][e], step.beta1, x * step.rest1);
-                v[q][e] = __builtin_fmaf(old, step.beta2, x * x * step.rest2);
+                // no fused multiply-add: the states' bits are those of the formula as it is
+                // written, or a code that hangs on the last bit would differ from the host's
+                m[q][e] = m[q][e] * step.beta1 + x * step.rest1;
+                v[q][e] = old * step.beta2 + x * x * step.rest2;
                 r[q][e] = sqrtf(v[q][e]);
                 const float den = __builtin_fmaf(r[q][e], k.root, step.eps);
                 // the hardware's reciprocal is off by an ulp; den is 0 or a normal number

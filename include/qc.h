@@ -783,6 +783,9 @@ int qc_grad_norm_multi(const void* const* grads, int32_t gtype, const int64_t* o
  *   m = beta1 m + (1 - beta1) g,    v = beta2 v + (1 - beta2) g^2,
  *   p = p (1 - lr weight_decay)
  *       - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps).
+ * m and v are formed by these products and sums in this order, (g g) (1 -
+ * beta2), each rounded to nearest, with beta and 1 - beta rounded to fp32: their
+ * bits, and the 8-bit states below, are the same on every host.
  * With an eps of 0 an element whose gradients were all zero becomes 0 / 0.
  *
  *   params      read (unless master is given) and written, rounded once.

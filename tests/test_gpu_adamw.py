@@ -3,8 +3,9 @@ form (mx_ref.py): the clipping norm, the AdamW step with fp32 and with 8-bit
 states, and those states' codes.
 
 Tolerances, in half steps of fp32 (2^-24 of the value): with x = g * scale
-rounded once, m = fma(m, b1, x * (1 - b1)) is off by 4 of its two terms'
-magnitudes (x, 1 - b1, b1, the product and the sum round); v by 6 of its own;
+rounded once, m = m * b1 + x * (1 - b1) is off by 4 of its two terms'
+magnitudes (x, 1 - b1, the product and the sum round; b1, the product and the
+sum); v by 6 of its own (x twice, its square, 1 - b2, the product and the sum);
 r = sqrt(v) by 4; the update rate * m / (r * root + eps) by 16 of the update
 that |m|'s two terms would give (m 4; rate, root and their products 4; r 4; the
 sum with eps 1; a reciprocal within an ulp 2, the product with it 1); p by one for each of its factor, product and
@@ -174,6 +175,62 @@ def check_some(kind, codes, scale, x, u, err, sure):
     if not sure.all():
         u = np.where(sure, u, 0.5)
     ref.check_codes(kind, codes, scale, x, u, err)
+
+
+def saved(kind, x, step):
+    """Codes and scales of fp32 values at a step, in fp32 arithmetic."""
+    low, first, top = (20, 896, 127) if kind.signed else (19, 1792, 255)
+    b = np.pad(x, (0, -x.size % 256)).reshape(-1, 256)
+    largest, least = (np.array([first + c], np.uint32) << low for c in (top, 1))
+    rest, least = np.float32(1) / largest.view(np.float32)[0], least.view(np.float32)[0]
+    amax = np.abs(b).max(1)
+    scale = np.where(amax > 0, np.maximum(amax * rest, np.float32(2.0 ** -100)), np.float32(0))
+    with np.errstate(divide="ignore"):
+        inv = np.where(scale > 0, np.float32(1) / scale, np.float32(0))
+    y = (np.abs(b) * inv[:, None]).reshape(-1)[: x.size]
+    u = (0x91E10DA5 * np.arange(x.size, dtype=np.uint64) + 0xC13FA9A9 * step + (0 if kind.signed else 1 << 31)) % (1 << 32)
+    code = ((y.view(np.uint32) + (u >> (32 - low))) >> low).astype(np.int64) - first
+    under = y > (u >> 8).astype(np.float32) * (least * np.float32(2.0 ** -24)) if kind.signed else y > 0
+    code = np.where(y < least, under, np.minimum(code, top))
+    return np.where(kind.signed & (x < 0) & (code > 0), code | 128, code).astype(np.uint8), scale
+
+
+@pytest.mark.parametrize("gtype", [F32, BF16], ids=str)
+@pytest.mark.parametrize("bits", [32, 8])
+def test_states_are_the_formulas_bits(qc, bits, gtype):
+    """Six steps of states, carried on by the host in fp32 on its own: no
+    rounding apart, where one code of one block's largest element would show."""
+    sizes = [40000, 3, 255, 100001]
+    n, nb = sum(sizes), -(-sum(sizes) // 256)
+    params, grads = Tensors(qc, sizes, F32, 1).set(values(n, 1)), Tensors(qc, sizes, gtype, 1)
+    b1, b2, rest1, rest2 = (np.float32(x) for x in (0.9, 0.999, 1 - 0.9, 1 - 0.999))
+    m, v = np.zeros(n, np.float32), np.zeros(n, np.float32)
+    if bits == 32:
+        state = [torch.zeros(n, device="cuda") for _ in range(2)]
+    else:
+        state = [torch.zeros(k, dtype=d, device="cuda") for k, d in ((n, torch.uint8), (nb, F32)) * 2]
+    call = qc.qc_adamw_multi if bits == 32 else qc.qc_adamw8_multi
+    t, c = params.table, torch.tensor([0.37], device="cuda")
+    for step in range(1, 7):
+        grads.set(values(n, 20 + step))
+        call(t.xs, 0, grads.table.xs, qt(qc, gtype), t.offsets, t.seg_first, t.ntensors, n, None, *state, step=step,
+             grad_scale=c, **HYPER)
+        x = grads.host().astype(np.float32) * np.float32(0.37)
+        m, v = m * b1 + x * rest1, v * b2 + x * x * rest2
+        got = [s.cpu().numpy() for s in state]
+        if bits == 32:
+            want = [m, v]
+        else:
+            want = [*saved(ref.M, m, step), *saved(ref.R, np.sqrt(v), step)]
+            back = []
+            for kind, (code, scale) in ((ref.M, want[:2]), (ref.R, want[2:])):
+                mag = (code & 127 if kind.signed else code).astype(np.uint32)
+                f = np.where(mag > 0, ((896 + mag << 20) if kind.signed else (1792 + mag << 19)).view(np.float32), np.float32(0))
+                f = np.where(kind.signed & (code > 127), -f, f)
+                back.append((np.pad(f, (0, nb * 256 - n)).reshape(nb, 256) * scale[:, None]).reshape(-1)[:n])
+            m, v = back[0], back[1] * back[1]
+        for g, w in zip(got, want):
+            assert np.array_equal(g, w), (step, int((g != w).sum()))
 
 
 @pytest.mark.parametrize("bits", [32, 8])
