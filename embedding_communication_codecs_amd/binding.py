@@ -629,6 +629,8 @@ def _space(workspace, here):
         return None, 0
     if isinstance(workspace, int):
         raise ValueError("workspace must be a GPU tensor")
+    if workspace.get_device() == here and workspace.is_contiguous():
+        return workspace.data_ptr(), workspace.nbytes
     _placed(workspace, here, "workspace")
     return _ptr(workspace, None, "workspace"), workspace.nbytes
 
@@ -636,6 +638,8 @@ def _space(workspace, here):
 def _table(t, nbytes, name, here):
     """Address of a device table of pointers, offsets or indices."""
     if t is not None and not isinstance(t, int):
+        if t.get_device() == here and t.is_contiguous() and t.nbytes >= nbytes:
+            return t.data_ptr()
         _placed(t, here, name)
     return _ptr(t, nbytes, name)
 
