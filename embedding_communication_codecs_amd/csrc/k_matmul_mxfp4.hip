@@ -158,19 +158,23 @@ struct ScaleLoader {
 };
 
 // WN x WM waves share the tile, and KW (1 or 2) of them each one's part: two
-// take the four instructions' worth of k of a stage between them, so that a
-// wave of a small tile has two fragments of either side to multiply, and
-// join their sums at the end.  A wave reads the fragments of its next step while it
+// take the four instructions' worth of k of a stage between them, so that a wave
+// of a small tile has two fragments of either side to multiply, and join their
+// sums at the end.  A wave reads the fragments of its next step while it
 // multiplies those of this one.  Before the last step of a stage has its turn,
-// all of the stage's fragments have been read: there stand the wait for the
-// next stage and the only barrier, and the matrix cores work on across it.
-// The loads of the stage NB further on follow, over the one just left: SOON of
-// them at once, the others with the steps of the next stage, as many at a time
-// would hold up the wave (16384 x 8192 x 8192: 487 us against 512).  A stage
-// has no branch: the compiler would move matrix instructions across it, and
-// their operands would fill the registers.  So loads are issued past the end
-// too (they repeat the last pieces), and those of the scales by fewer waves
-// than there are with an empty mask in the others.
+// all of the stage's fragments have been read: there stand the wait for the next
+// stage and the only barrier, and the matrix cores work on across it. The loads
+// of the stage NB further on follow, over the one just left: SOON of them at
+// once, the others with the steps of the next stage, as many at a time would
+// hold up the wave (16384 x 8192 x 8192: 487 us against 512).  The next stage's
+// scales, whose chunk was complete a stage ago, are read a step before the turn:
+// 32 bytes a row put four rows in a bank, a read takes 8 cycles of LDS, and six
+// of them from each wave, all at once behind the barrier, were ahead of the
+// fragments there (510 us against 520).  A stage has no branch: the compiler
+// would move matrix instructions across it, and their operands would fill the
+// registers.  So loads are issued past the end too (they repeat the last
+// pieces), and those of the scales by fewer waves than there are with an empty
+// mask in the others.
 //
 // The two largest tiles, of whose blocks a compute unit holds one, go on to
 // further tiles (LOOP): the scales and the first stage of the next one are on
@@ -290,9 +294,9 @@ k_mm_mx_pipe(Args g, T* __restrict__ c) {
             const bool turn = t + 1 == STEPS;
             if (turn) {
                 lds_landed_but<(NB - 2) * LOADS>();
-                fetch_scales(fast, (s + NB - 1) / kChunk + 1, (s + NB - 1) % kChunk);
-                read_scales(s + 1, nb, na);
+                fetch_scales(fast, (s + NB) / kChunk + 1, (s + NB) % kChunk);
             }
+            if (t + 2 == STEPS) read_scales(s + 1, nb, na);
             // the next step's fragments
             const int kk = turn ? wk * STEPS : wk * STEPS + t + 1, at = turn ? next : buf, ns = turn ? s + 1 : s;
 #pragma unroll
@@ -326,7 +330,7 @@ k_mm_mx_pipe(Args g, T* __restrict__ c) {
     // lies in buffer (s + 1) % NB, so that these leave buffer 0 alone.
     auto begin = [&]() {
 #pragma unroll
-        for (int x = 0; x < kChunk + NB - 1; ++x) fetch_scales(std::false_type{}, x / kChunk, x % kChunk);
+        for (int x = 0; x < kChunk + NB; ++x) fetch_scales(std::false_type{}, x / kChunk, x % kChunk);
 #pragma unroll
         for (int s = 0; s + 1 < NB; ++s) {
 #pragma unroll
@@ -352,7 +356,7 @@ k_mm_mx_pipe(Args g, T* __restrict__ c) {
 #pragma unroll
         for (int i = 0; i < FN; ++i) fb[0][i] = read_b(std::false_type{}, 1 % NB, wk * STEPS, i, 0);
         // fast stages: where rows of scales end inside a piece, those whose chunks are whole
-        const int fast_end = min(whole, slen % 16 == 0 ? whole : slen / kScaleBytes * kChunk - kChunk + 1);
+        const int fast_end = min(whole, slen % 16 == 0 ? whole : slen / kScaleBytes * kChunk - kChunk);
         int s = 0;
         for (; s + 2 * NB - 1 < fast_end; s += NB) {
 #pragma unroll

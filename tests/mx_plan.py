@@ -51,5 +51,5 @@ def fast_turns(k, shape, stages=None):
     pitch, spitch = -(-k // 32) * 16, -(-k // 128) * 4
     length = min(pitch, (stages or 1 << 40) * 128)
     whole = length // 128
-    end = min(whole, whole if spitch % 16 == 0 else spitch // 32 * 4 - 3)
+    end = min(whole, whole if spitch % 16 == 0 else spitch // 32 * 4 - 4)
     return max(-(-(end - 2 * nb + 1) // nb), 0)
