@@ -17,7 +17,8 @@ __device__ __forceinline__ uint32_t mx_byte(uint32_t amax_bits) {
     const int e = (int)((amax_bits + 0x200000u) >> 23) - 2;
     return amax_bits >= kInfBits ? kMxNaN : (uint32_t)min(max(e, 1), 253);
 }
-// The scale as a number; of a group of NaNs 1, as its codes are replaced.
+// The scale as a number; of a group of NaNs 1, as its codes are replaced.  The
+// conversions look at its exponent alone and take 0, of byte 0, for 2^-127.
 __device__ __forceinline__ float mx_scale(uint32_t byte) {
     return __uint_as_float((byte == kMxNaN ? 127u : byte) << 23);
 }

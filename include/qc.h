@@ -687,7 +687,9 @@ int qc_swiglu_ckpt8_backward(const void* dh, int32_t dhtype, int64_t lddh, const
  * of [n][k] enters the forward product as it is and that of the input's
  * gradient transposed; the gradient of the weights takes both its operands
  * transposed.  Unlike for the other calls, rows == 0 is empty for both pairs.
- * qc_decode_mxfp4 writes the values; they are exact in fp32 and in bf16.
+ * qc_decode_mxfp4 writes the values; they are exact in fp32 and in bf16.  It
+ * and the products read scale bytes 0 and 254 too (2^-127 and 2^127), which the
+ * encoder does not write.
  * Errors: ARG (NULL x or out, one of a pair NULL, both pairs NULL, bad type,
  *         rows < 0, dim < 1, a stride below its row, 2^24 tiles of 128 x 128
  *         values or more, 2^23 with the transpose), ALIGN, UNSUPPORTED (rows,
@@ -709,8 +711,8 @@ int qc_decode_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, i
  * count as zero.
  *
  *   a, a_scales   MXFP4 of [m][k]: tokens.   b, b_scales   of [n][k]: weights.
- *                 Codes past k in the last group are zeros, as the encoder
- *                 writes them.
+ *                 Codes past k in the last group and scale bytes past it are
+ *                 zeros, as the encoder writes them.
  *   c             [m][n] of type ctype, row stride ldc, written; with
  *                 accumulate != 0 (QC_F32 only) added to.
  *   k             at least 1.

@@ -194,6 +194,31 @@ def test_scales_at_their_ends(qc):
         check_product(c.get(), ref.held(ac, as_, k), ref.held(bc, bs, k))
 
 
+def test_scales_that_only_others_write(qc):
+    """Bytes 0 and 254, 2^-127 and 2^127, which the encoder does not need: decoded
+    (6 * 2^127 is no fp32 number) and multiplied."""
+    rows, dim = 255, 32
+    codes = np.tile(np.arange(16, dtype=np.uint8) * 16 + np.arange(16, dtype=np.uint8)[::-1], (rows, 1))
+    scales = np.zeros((rows, 4), np.uint8)
+    scales[:, 0] = np.arange(rows)
+    h = Held(qc, rows, dim).set(codes, scales)
+    for dtype in DTYPES:
+        out = torch.empty((rows, dim), dtype=dtype, device="cuda")
+        qc.qc_decode_mxfp4(*h.pair(), rows, dim, out, qt(qc, dtype), dim)
+        want = torch.from_numpy(ref.held(codes, scales, dim)).to(dtype)
+        assert torch.equal(out.cpu(), want)
+    m, n, k = 33, 70, 300
+    (ac, _), (bc, _) = ref.random_mx(m, k, 7), ref.random_mx(n, k, 8)
+    for sa, sb in ((254, 0), (0, 254), (254, 2)):
+        as_, bs = (np.zeros((r, 12), np.uint8) for r in (m, n))
+        as_[:, :10], bs[:, :10] = sa, sb
+        c = Buf(m, n, n, F32)
+        a, b = Held(qc, m, k).set(ac, as_), Held(qc, n, k).set(bc, bs)
+        qc.qc_matmul_mxfp4(*a.pair(), *b.pair(), m, n, k, c.t, qc.QC_F32, n, False,
+                           space(qc.qc_matmul_mxfp4_workspace(m, n, k)))
+        check_product(c.get(), ref.held(ac, as_, k), ref.held(bc, bs, k))
+
+
 WIDE = [(1, 5003, 700), (3, 4100, 1030), (5, 4200, 2043), (8, 8190, 515), (9, 4100, 600)]
 
 

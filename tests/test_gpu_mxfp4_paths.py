@@ -24,6 +24,8 @@ SIZES = [
     (257, 255, 512), (300, 520, 1030), (1024, 70, 300), (300, 8847, 385), (162, 19082, 993),
     # blocks that go on to a second and a third tile
     (4300, 4353, 300), (2100, 8500, 3001), (5000, 8200, 33), (8150, 4090, 1500), (4095, 8190, 4000),
+    # the longest rows
+    (20, 40, 1 << 23), (257, 300, (1 << 22) + 5),
 ]
 
 
