@@ -347,6 +347,34 @@ def test_captured_and_replayed(qc, m, n, k):
         check_product(c1.cpu(), ref.held(*ref.encode(xs), k), ref.held(bc, bs, k))
 
 
+def test_two_streams_at_once(qc):
+    """Calls that run beside each other, each with buffers and a workspace of its own."""
+    cases = [(40, 500, 9000), (64, 64, 9000), (1, 300, 700), (1003, 510, 2043)]
+    work = []
+    for i, (m, n, k) in enumerate(cases):
+        bc, bs = ref.random_mx(n, k, 20 + i)
+        x, b = matrix(m, k, 30 + i, BF16).cuda(), Held(qc, n, k).set(bc, bs)
+        need = qc.qc_linear_mxfp4_workspace(m, n, k, qc.QC_BF16)
+        work.append((x, b, m, n, k, torch.empty((m, n), device="cuda"), space(need), torch.cuda.Stream()))
+
+    def call(x, b, m, n, k, c, w):
+        qc.qc_linear_mxfp4(x, qc.QC_BF16, k, *b.pair(), m, n, k, c, qc.QC_F32, n, w)
+
+    alone = []
+    for *args, _ in work:
+        call(*args)
+        alone.append(args[5].clone())
+        args[5].fill_(7.0)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for *args, stream in work:
+            with torch.cuda.stream(stream):
+                call(*args)
+    torch.cuda.synchronize()
+    for want, (*args, _) in zip(alone, work):
+        assert torch.equal(args[5], want)
+
+
 def test_more_channels_than_one_launch_encodes_tokens_for(qc):
     """2^27 channels: 16 a block of 512 threads would be a launch of 2^32."""
     m, n, k, period = 2, (1 << 27) + 5, 32, 4099
