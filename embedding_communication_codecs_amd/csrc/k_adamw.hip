@@ -278,18 +278,18 @@ __device__ __forceinline__ float state_scale(uint32_t amax_bits, float& inv) {
     return nan ? __uint_as_float(0x7FC00000u) : (zero ? 0.0f : s);
 }
 
-// u: the 32 bits of the threshold.  inv == 0: code 0.
+// u: the 32 bits of the threshold.  inv == 0: code 0 (of NaNs too, as no
+// comparison holds).  Below the first code's value y + the threshold comes to
+// that code at most, and m becomes 0 where y is not above u of that value.
 template <int KIND>
 __device__ __forceinline__ uint32_t state_code(float x, float inv, uint32_t u) {
     using S = State<KIND>;
     constexpr float kLeast = __builtin_bit_cast(float, (S::FIRST + 1) << S::LOW);
     const float y = fabsf(x) * inv;
-    const uint32_t up = (__float_as_uint(y) + (u >> (32 - S::LOW))) >> S::LOW;
-    const bool low = S::SIGNED ? y > (float)(u >> 8) * (kLeast * 0x1p-24f) : y > 0.0f;
-    uint32_t c = y < kLeast ? (low ? 1u : 0u) : min(up - S::FIRST, (uint32_t)S::TOP);
-    if (!(inv > 0.0f)) c = 0u;
-    if (S::SIGNED && x < 0.0f && c) c |= 128u;
-    return c;
+    const int32_t up = (int32_t)(__float_as_uint(y) + (u >> (32 - S::LOW)) - (S::FIRST << S::LOW)) >> S::LOW;
+    uint32_t c = (uint32_t)min(max(up, 1), S::TOP);
+    if (S::SIGNED) c |= (__float_as_uint(x) >> 24) & 128u;
+    return y > (S::SIGNED ? (float)(u >> 8) * (kLeast * 0x1p-24f) : 0.0f) ? c : 0u;
 }
 
 __device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int left) {
@@ -405,8 +405,10 @@ __device__ __forceinline__ Rates rates_of(const AdamwStep& s) {
     return r;
 }
 
+// Five blocks a compute unit where the registers are enough (3 M elements, 8-bit
+// states: 17.2 us, with four 17.8); with master weights they would spill.
 template <class P, class G, class S, bool MASTER>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, MASTER ? 4 : 5)
 k_adamw(Tables l, P* const* __restrict__ params, G* const* __restrict__ grads, float* __restrict__ master, S st,
         AdamwStep step) {
     constexpr bool WIDE = std::is_same<S, Wide>::value;
