@@ -9,7 +9,7 @@
 //
 // Bound by HBM where n is large: the norm reads g once, the step g, p, m and v
 // and writes the last three (268 M elements: norm of fp32 170 us, 6.3 TB/s, as
-// part of it still lies in the last cache; the step in fp32 1400 us, 5.4 TB/s).
+// part of it still lies in the last cache; the step in fp32 1400–1430 us, 5.3 TB/s).
 // Short lists are bound by loads that wait for each other.
 #include "qc_matrix.hpp"
 #include "qc_launch.hpp"
@@ -657,7 +657,8 @@ Runs runs_of(int64_t n, int64_t most) {
 Runs norm_runs(int64_t n) { return runs_of(n, kMaxRuns); }
 // One pass a block, as far as a grid goes: all blocks at work then read and
 // write a few places that move on together (268 M elements, fp32 states, with 1,
-// 2, 4 and 8 passes 1530, 1551, 1605 and 1667 us; 8-bit 812, 855, 872, 907).
+// 2 and 4 passes 1430, 1445 and 1520 us; 8-bit 845, 840, 860; 3 M elements, 8-bit,
+// 17.1, 21.0, 29.7).
 Runs step_runs(int64_t n) { return runs_of(n, kMaxBlocks); }
 
 unsigned grid_of(int64_t n, int64_t each) {
