@@ -9,7 +9,7 @@
 //
 // Bound by HBM where n is large: the norm reads g once, the step g, p, m and v
 // and writes the last three (268 M elements: norm of fp32 170 us, 6.3 TB/s, as
-// part of it still lies in the last cache; the step in fp32 1400–1430 us, 5.3 TB/s).
+// part of it still lies in the last cache; the step in fp32 1400 to 1430 us, 5.3 TB/s).
 // Short lists are bound by loads that wait for each other.
 #include "qc_matrix.hpp"
 #include "qc_launch.hpp"

@@ -9,6 +9,8 @@
 #include "qc_lds.hpp"
 #include "qc_mx.hpp"
 
+#include <type_traits>
+
 namespace qc {
 namespace {
 
@@ -51,11 +53,12 @@ __device__ __forceinline__ uint32_t gather_bytes(uint32_t b) {
 }
 
 // Eight values of a unit's lane; every lane of the wave calls this.
-template <class T>
+template <bool ALL, class T>
 __device__ __forceinline__ void keep_row8(const Raw8<T>& v, int64_t row, int64_t col, bool live, int64_t dim,
                                           const Coded& k) {
     const uint32_t byte_here = mx_byte(quad_max(v.amax_bits()));
-    const bool group = live && (col & ~int64_t(31)) < dim;  // else: padding, byte 0
+    live = ALL || live;
+    const bool group = ALL || (live && (col & ~int64_t(31)) < dim);  // else: padding, byte 0
     const uint32_t byte = group ? byte_here : 0u;
     const uint32_t word = gather_bytes(byte);
     if (live && (threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t*>(k.scales + row * k.spitch + col / 32) = word;
@@ -80,20 +83,23 @@ k_enc_mxfp4(const T* __restrict__ x, int64_t ldx, Sizes z, Coded k) {
 #pragma unroll
         for (int u = 0; u < U; ++u) v[u].settle(left_of(p[u], z), p[u].col > 0);
 #pragma unroll
-        for (int u = 0; u < U; ++u) keep_row8(v[u], p[u].row, p[u].col, p[u].live, z.dim, k);
+        for (int u = 0; u < U; ++u) keep_row8<false>(v[u], p[u].row, p[u].col, p[u].live, z.dim, k);
     }
 }
 
 // ---------------------------------------------------------------- columns
-// The transpose's encoding, with or without the matrix's own: tiles of 128 x
-// 128 through LDS, 512 threads each.  A thread loads four pieces of 8 values
-// (and encodes them by rows from its registers); then it takes 2 columns x 16
-// rows, half a group of each, whose other half its neighbour has, and their
-// codes leave through LDS again, 64 bytes of a row of the transpose side by
-// side.  Both encodings of 8192 x 8192: bf16 49 us, 4.2 TB/s, fp32 72 us, 4.8.
-// (With 256 threads and whole groups, whose waves have twice the instructions, 50
-// and 75 us, and 1027 x 770 6.0 and 6.6 against 4.8 and 5.7; with 1024, 51 and
-// 67, and 4.7 and 5.9.)
+// The transpose's encoding, with or without the matrix's own: tiles of 128 x 128
+// through LDS, 512 threads each.  A thread loads four pieces of 8 values (and
+// encodes them by rows from its registers); then it takes 2 columns x 16 rows,
+// half a group of each, whose other half its neighbour has, and their codes
+// leave through LDS again, 64 bytes of a row of the transpose side by side.
+// Both encodings of 8192 x 8192: bf16 48 us, 4.3 TB/s, fp32 67 us, 5.1. (With
+// 256 threads and whole groups, whose waves have twice the instructions, 1 and 4
+// us more, and 1027 x 770 6.0 and 6.6 us against 4.8 and 5.5; with 1024 as long.
+// Tiles inside the matrix look at no bounds: 1.5 and 4.5 us.  Tiles of 256 rows,
+// whose codes leave 128 bytes side by side, take 44 us for this bf16 matrix, but
+// 34.2 against 33.6 for 8192 x 6144, 33.8 against 32.2 for 4096 x 11008, and
+// 16.0 against 13.6 for 4096 x 4096.)
 constexpr int kTile = 128, kHalfGroup = 16;
 
 // Byte of a row of the tile in LDS.  A wave reads 32 pairs of columns in two
@@ -178,22 +184,26 @@ k_enc_mxfp4_t(const T* __restrict__ x, int64_t ldx, int64_t rows, int64_t dim, C
                                   (uint32_t)((rows + kTile - 1) / kTile));
     const int64_t r0 = (int64_t)tile.y * kTile, c0 = (int64_t)tile.x * kTile;
     const int t = threadIdx.x;
-    {
+    const bool whole = r0 + kTile <= rows && c0 + kTile <= dim;
+    auto by_rows = [&](auto all) {
+        constexpr bool ALL = decltype(all)::value;
         const int64_t col = c0 + 8 * (t & 15);
         Raw8<T> v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t row = r0 + 32 * u + (t >> 4);
-            v[u].template load<true>(x + row * ldx + col, row < rows ? dim - col : 0, col > 0);
+            v[u].template load<true>(x + row * ldx + col, ALL ? 8 : row < rows ? dim - col : 0, col > 0);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t row = r0 + 32 * u + (t >> 4);
-            v[u].settle(row < rows ? dim - col : 0, col > 0);
-            if (ROWS) keep_row8(v[u], row, col, row < rows, dim, k);
+            if (!ALL) v[u].settle(row < rows ? dim - col : 0, col > 0);
+            if (ROWS) keep_row8<ALL>(v[u], row, col, row < rows, dim, k);
             put_raw8(lds, 32 * u + (t >> 4), 8 * (t & 15), v[u]);
         }
-    }
+    };
+    if (whole) by_rows(std::true_type{});
+    else by_rows(std::false_type{});
     __syncthreads();
     // columns 2 pair and 2 pair + 1, rows 32 part + 16 half and on
     const int half = t & 1, pair = t >> 1 & 63, part = t >> 7;
