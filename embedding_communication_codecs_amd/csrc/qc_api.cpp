@@ -807,7 +807,7 @@ int check_adamw(const AdamwArgs& a, qc::AdamwList& l, qc::AdamwStep& s) {
 
 }  // namespace
 
-int64_t qc_grad_norm_workspace(int64_t n) { return n < 0 ? -1 : qc::grad_norm_workspace(n); }
+int64_t qc_grad_norm_workspace(int64_t n) { return n < 0 || n > kMaxListElems ? -1 : qc::grad_norm_workspace(n); }
 
 int qc_grad_norm_multi(const void* const* grads, int32_t gtype, const int64_t* offsets, const int32_t* seg_first,
                        int32_t ntensors, int64_t n, double max_norm, void* workspace, int64_t workspace_bytes,

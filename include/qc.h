@@ -769,10 +769,12 @@ int qc_linear_mxfp4(const void* x, int32_t xtype, int64_t ldx, const uint8_t* b,
  *
  *   max_norm   above 0; infinity for the norm alone.
  *   workspace  device memory of at least qc_grad_norm_workspace(n) bytes,
- *              used during the call; 8-byte aligned.  (-1 for n < 0.)
+ *              used during the call; 8-byte aligned.  (-1, no status, for an n that the
+ *              norm refuses: below 0 or above 2^56.)  Calls that may run at the
+ *              same time need one each.
  *   out        fp32[2], written (4-byte aligned).
- * Errors: ARG (NULL pointer, bad type, n < 0, ntensors < 1, max_norm not above
- *         0, too little workspace), ALIGN.
+ * Errors: ARG (NULL pointer, bad type, n < 0 or above 2^56, ntensors < 1,
+ *         max_norm not above 0, too little workspace), ALIGN.
  */
 int64_t qc_grad_norm_workspace(int64_t n);
 int qc_grad_norm_multi(const void* const* grads, int32_t gtype, const int64_t* offsets, const int32_t* seg_first,
