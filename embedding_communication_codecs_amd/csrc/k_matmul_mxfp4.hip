@@ -114,11 +114,15 @@ struct Loader {
     __device__ __forceinline__ static int piece(int wave, int i, int lane) {
         return piece_slot(row(wave, i, lane), lane % 8);
     }
-    // load `i` of N of stage s.  WHOLE: the rows reach the stage's end.
+    // load `i` of N of stage s.  WHOLE: the rows reach the stage's end.  Where they
+    // may not, the stage is part of a lane's own offset: beside it, what brings a
+    // piece of a stage past the end back to the row's last one would make that
+    // offset negative, which buffer addressing takes for one past the descriptor.
     template <bool WHOLE>
     __device__ __forceinline__ void load(int i, uint32_t lds, int wave, int s, int len) const {
-        const int over = WHOLE ? 0 : max(s * kStage + piece(wave, i, lane_id()) * 16 - (len - 16), 0);
-        load_lds16(rsrc, lds + (wave * N + i) * 1024, off[i] - over, s * kStage);
+        const uint32_t to = lds + (wave * N + i) * 1024;
+        if constexpr (WHOLE) load_lds16(rsrc, to, off[i], s * kStage);
+        else load_lds16(rsrc, to, off[i] + min(s * kStage, len - 16 - piece(wave, i, lane_id()) * 16), 0);
     }
 };
 
