@@ -807,7 +807,9 @@ constexpr Shape kShapes[] = {
     {128, 128, 7.2f, 2.9f, 4.5f, 2.75f}, {128, 256, 7.4f, 5.0f, 4.0f, 5.1f},   {256, 256, 10.8f, 7.6f, 8.3f, 7.5f},
 };
 constexpr int kAll = sizeof(kShapes) / sizeof(kShapes[0]), kFirstPipe = 4;
-// Parts are joined by a launch of its own (2.5 us) that reads them at 4 TB/s.
+// Parts are joined by a launch of its own (2.5 us) that reads them at 4 TB/s (130
+// x 120 x 30050 in 15 parts: 11.8 us, 2.9 to 3.8 of them the join, whose bytes
+// take 0.2).
 // Only the pipelined tiles are split, as the others share k among their waves;
 // a part has at least four stages.
 constexpr int kMaxSplits = 16, kLeastStages = 4;
@@ -887,10 +889,19 @@ Args args_of(const void* a, const void* a_scales, const void* b, const void* b_s
                 0};
 }
 
-// Up to kFew tokens are encoded by the blocks that multiply them (8 tokens x
-// 4096 x 4096 6.2 us, in two launches 6.9; 16 tokens 8.0 and 7.0).  Blocks of 32
-// channels where those of 16 are more than the compute units and each encodes
-// eight tokens (8 x 8192 x 8192 11.0 us against 15.5).
+// Up to kFew tokens are encoded by the blocks that multiply them.  In us, and in
+// parentheses an encoding and a product in two launches, per call of a captured
+// graph and, where the host is the slower side, per call from Python:
+//                     a graph                                       from Python
+//   n 4096  k 4096    1 token 2.9 (4.7), 4: 4.2 (5.1), 8: 5.5 (5.2)    8: 6.6 (9.2)
+//   n 8192  k 8192    5.6 (7.8)          7.9 (8.1)     8.9 (8.2)       8.9 (9.0)
+//   n 4096  k 11008   4.5 (6.4)          6.6 (6.7)     9.2 (7.2)       9.2 (9.2)
+//   n 11008 k 4096    4.8 (9.3)          7.0 (9.8)     11.4 (10.3)    10.5 (9.2)
+// One launch is the faster one up to 4 tokens; with 5 to 8 it saves the host 2.6
+// us, and the GPU takes up to a quarter longer, as every block encodes all of
+// them.  16 tokens x 4096 x 4096 from Python: 8.0 (7.0).  Blocks of 32 channels
+// where those of 16 are more than the compute units and each encodes eight
+// tokens (8 x 8192 x 8192 8.9 us against 15.5).
 constexpr int kFew = 8;
 bool takes_fused(int64_t m, int64_t n) { return m <= kFew && (n + 15) / 16 <= kMaxGrid; }
 

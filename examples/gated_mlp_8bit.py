@@ -10,7 +10,8 @@ travels as an INT8 payload with error feedback, as it would between workers
 (one worker here), before a plain SGD step on the fp32 master weights.
 
 With --products mxfp4 the forward and input-gradient products run on MXFP4
-codes (a power-of-two scale per 32 values) instead; with --optimizer adamw or
+codes (a power-of-two scale per 32 values) instead, while the weight gradients
+still come from the 8-bit checkpoints; with --optimizer adamw or
 adamw8 the gradients are clipped and AdamW takes the step, over the list of
 both weights, its states in fp32 or in 8 bits.
 

@@ -769,10 +769,11 @@ int qc_linear_mxfp4(const void* x, int32_t xtype, int64_t ldx, const uint8_t* b,
  *
  *   max_norm   above 0; infinity for the norm alone.
  *   workspace  device memory of at least qc_grad_norm_workspace(n) bytes,
- *              used during the call; 8-byte aligned.  (-1, no status, for an n that the
- *              norm refuses: below 0 or above 2^56.)  Calls that may run at the
- *              same time need one each.
- *   out        fp32[2], written (4-byte aligned).
+ *              used during the call; 8-byte aligned.  (-1, no status, for an n
+ *              that the norm refuses: below 0 or above 2^56.)  Calls that may
+ *              run at the same time need one each.
+ *   out        fp32[2], written (4-byte aligned); with n == 0 left as it was
+ *              (a step over an empty list reads no coefficient).
  * Errors: ARG (NULL pointer, bad type, n < 0 or above 2^56, ntensors < 1,
  *         max_norm not above 0, too little workspace), ALIGN.
  */
@@ -791,6 +792,10 @@ int qc_grad_norm_multi(const void* const* grads, int32_t gtype, const int64_t* o
  * beta2), each rounded to nearest, with beta and 1 - beta rounded to fp32: their
  * bits, and the 8-bit states below, are the same on every host.
  * With an eps of 0 an element whose gradients were all zero becomes 0 / 0.
+ * The step is taken whatever the coefficient is: with a NaN, as the norm gives
+ * for gradients that are not finite, every weight and state of the list becomes
+ * NaN.  A caller that would rather leave such a step out reads the coefficient
+ * first, and captures the norm and the step into graphs of their own.
  *
  *   params      read (unless master is given) and written, rounded once.
  *   master      fp32[n] or NULL: with bf16 parameters, the weights proper,
@@ -828,6 +833,15 @@ int qc_adamw_multi(void* const* params, int32_t ptype, const void* const* grads,
  * scale = max(amax * fl(1 / F(largest)), 2^-100) with amax the block's largest
  * magnitude, 0 where that is 0.  A block with an infinity or a NaN gets scale
  * NaN and codes 0 and stands for NaNs.
+ *
+ * Blocks are of the concatenation, so one may hold the end of a tensor and the
+ * start of the next, or several small ones.  What shares a block shares its
+ * scale: no r above zero is held as less than 1 / 59,753 of the block's largest,
+ * which holds back the steps of elements with far smaller gradients, and one
+ * state that is not finite makes the others of its block NaN, also those of
+ * another tensor.  Tensors of a multiple of 256 elements, first in the list,
+ * share no block; one that is to share none otherwise is stepped in a list of
+ * its own.
  *
  * After a step, y = |x| * fl(1 / scale) lies between two codes; it becomes the
  * upper one where its place between them is above 1 - u, u = u32 / 2^32 with
