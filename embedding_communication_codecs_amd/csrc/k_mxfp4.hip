@@ -88,19 +88,20 @@ k_enc_mxfp4(const T* __restrict__ x, int64_t ldx, Sizes z, Coded k) {
 }
 
 // ---------------------------------------------------------------- columns
-// The transpose's encoding, with or without the matrix's own: tiles of 128 x 128
-// through LDS, 512 threads each.  A thread loads four pieces of 8 values (and
-// encodes them by rows from its registers); then it takes 2 columns x 16 rows,
-// half a group of each, whose other half its neighbour has, and their codes
-// leave through LDS again, 64 bytes of a row of the transpose side by side.
-// Both encodings of 8192 x 8192: bf16 48 us, 4.3 TB/s, fp32 67 us, 5.1; the
-// transpose's alone 37 us, 4.6, and 59 us, 5.1.  (With 256 threads and whole
+// The transpose's encoding, with or without the matrix's own: tiles of 128 x
+// 128 through LDS, 512 threads each. A thread loads four pieces of 8 values
+// (and encodes them by rows from its registers); then it takes 2 columns x 16
+// rows, half a group of each, whose other half its neighbour has, and their
+// codes leave through LDS again, 64 bytes of a row of the transpose side by
+// side. Both encodings of 8192 x 8192: bf16 48 us, 4.3 TB/s, fp32 67 us, 5.1;
+// the transpose's alone 37 us, 4.6, and 59 us, 5.1. (With 256 threads and whole
 // groups, whose waves have twice the instructions, 1 and 4 us more, and 1027 x
-// 770 6.0 and 6.6 us against 4.8 and 5.5; with 1024 as long.  1027 x 770 is 63
-// tiles, so three quarters of the compute units have none.  Tiles inside the matrix look at no bounds: 1.5 and 4.5 us.  Tiles of 256 rows,
-// whose codes leave 128 bytes side by side, take 44 us for this bf16 matrix, but
-// 34.2 against 33.6 for 8192 x 6144, 33.8 against 32.2 for 4096 x 11008, and
-// 16.0 against 13.6 for 4096 x 4096.)
+// 770 6.0 and 6.6 us against 4.8 and 5.5; with 1024 as long. 1027 x 770 is 63
+// tiles, so three quarters of the compute units have none. Tiles inside the
+// matrix look at no bounds: 1.5 and 4.5 us. Tiles of 256 rows, whose codes
+// leave 128 bytes side by side, take 44 us for this bf16 matrix, but 34.2
+// against 33.6 for 8192 x 6144, 33.8 against 32.2 for 4096 x 11008, and 16.0
+// against 13.6 for 4096 x 4096.)
 constexpr int kTile = 128, kHalfGroup = 16;
 
 // Byte of a row of the tile in LDS.  A wave reads 32 pairs of columns in two

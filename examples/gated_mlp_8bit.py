@@ -11,9 +11,9 @@ travels as an INT8 payload with error feedback, as it would between workers
 
 With --products mxfp4 the forward and input-gradient products run on MXFP4
 codes (a power-of-two scale per 32 values) instead, while the weight gradients
-still come from the 8-bit checkpoints; with --optimizer adamw or
-adamw8 the gradients are clipped and AdamW takes the step, over the list of
-both weights, its states in fp32 or in 8 bits.
+still come from the 8-bit checkpoints; with --optimizer adamw or adamw8 the
+gradients are clipped and AdamW takes the step, over the list of both weights,
+its states in fp32 or in 8 bits.
 
     python examples/gated_mlp_8bit.py [--tokens T] [--width D] [--hidden H] [--steps N]
         [--products int8|mxfp4] [--optimizer sgd|adamw|adamw8]
